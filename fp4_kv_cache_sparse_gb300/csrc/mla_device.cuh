@@ -331,7 +331,6 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return r;
 }
 
-// Least e with amax * 2^-e <= 448 (0 for amax == 0), clamped to [-127, 127].
 // Conjugate rotary embedding of one interleaved pair (a, b) by
 // phi = pos * freq ("deepseek-ai/FlashMLA", "What it is": the output-side
 // RoPE), in two steps so that a kernel can compute each pair's angle once
@@ -352,13 +351,15 @@ __device__ __forceinline__ void rope_conj_apply(float& a, float& b, float cs, fl
   b = __fmaf_rn(y, cs, -__fmul_rn(x, sn));
 }
 
+// Least e with amax * 2^-e <= 448 = 1.75 * 2^8 (0 for amax == 0 or NaN),
+// clamped to [-127, 127].  With amax = m * 2^E, m in [1, 2), that is E - 8 for
+// m <= 1.75 and E - 7 above: adding 0x1FFFFF carries a mantissa past 0x600000
+// (1.75) into the exponent field.  Subnormals clamp; infinity gives 120, so
+// every input ends in the same few instructions.
 __device__ __forceinline__ int fp8_block_exponent(float amax) {
   if (!(amax > 0.f)) return 0;
-  int E;
-  frexpf(amax, &E);  // amax = f 2^E, f in [0.5, 1)
-  int e = E - 10;    // amax 2^-e >= 2^9 > 448
-  while (ldexpf(amax, -e) > 448.f) ++e;
-  return e < -127 ? -127 : (e > 127 ? 127 : e);
+  const int e = static_cast<int>((__float_as_uint(amax) + 0x1FFFFFu) >> 23) - 135;
+  return e < -127 ? -127 : e;
 }
 
 }  // namespace mla

@@ -88,3 +88,18 @@ def test_written_records_decode_as_the_decode_kernel_reads_them():
         got = mla.dequantize(pool, kv_format).view(torch.int16).cpu().numpy().view(np.uint16)
         want = oracle.bf16_rne(dec(ENCODE[kv_format](x)))
         assert np.array_equal(got, want)
+
+
+def test_writer_ends_on_an_infinite_latent():
+    """An infinity is outside the writer's contract (finite latents), but the
+    call ends and every other block of the token is written as ever."""
+    bits, x = _latents(8, 13)
+    bits[:, 64] = 0x7F80  # +inf in dim 64: FP8 block 2
+    pool = _pool(mla.KV_FP8_528, 64)
+    mla.kv_write(torch.from_numpy(bits.view(np.int16)).to(DEV), torch.arange(8, dtype=torch.int32, device=DEV), pool)
+    torch.cuda.synchronize()
+    got, want = pool.cpu().numpy()[:8], oracle.encode_fp8(x)
+    other = np.ones(528, dtype=bool)
+    other[64:96] = False
+    other[512 + 2] = False
+    assert np.array_equal(got[:, other], want[:, other])
