@@ -94,6 +94,64 @@ cudaError_t launch_dequant(int kv_format, const uint8_t* records, int64_t n, uin
 cudaError_t launch_kv_write(int kv_format, const uint16_t* latents, const int32_t* slots, int64_t n, uint8_t* pool,
                             int64_t pool_tokens, int32_t* d_error, cudaStream_t stream);
 
+// Requests of one page plan: their prefix sums live in shared memory.
+constexpr int kPlanMaxBatch = 8192;
+cudaError_t launch_page_plan(const int32_t* cached_lens, const int32_t* new_lens, int batch, int32_t* block_table,
+                             int max_pages, int32_t* free_pages, int num_pages, const int32_t* num_free,
+                             int32_t* seq_lens, int32_t* num_free_out, int32_t* cu_new, int32_t* slots,
+                             int32_t* positions, int max_new, int32_t* d_error, cudaStream_t stream);
+
+// Rotary positions; strides in elements, checked by the caller.
+struct RopeParams {
+  const void* x;
+  void* y;
+  int64_t x_row, x_head, y_row, y_head, n;
+  int heads, head_dim, offset;
+  const int32_t* positions;
+  bool conjugate;
+};
+cudaError_t launch_rope(int dtype, const RopeParams& p, const mla_rope_table_t& table, cudaStream_t stream);
+
+// RMS norm with the residual's addition to FP8 blocks; strides in elements.
+struct NormParams {
+  const void* x;
+  const void* residual;  // nullable
+  const void* weight;
+  void* residual_out;    // nullable
+  uint8_t* codes;
+  uint8_t* scales;
+  int64_t x_row, residual_row, residual_out_row, codes_row, scales_row, n;
+  int dim;
+  float eps;
+};
+cudaError_t launch_rms_norm_fp8(int dtype, const NormParams& p, cudaStream_t stream);
+
+// Attention over a paged FP4 cache.
+struct PagedParams {
+  const uint16_t* q;           // bf16 [batch * rows][512]
+  const uint8_t* kv;           // FP4 records
+  const int32_t* block_table;  // [batch][max_pages]
+  const int32_t* seq_lens;     // [batch]
+  uint16_t* out;               // bf16 [batch * rows][512]
+  float* lse;                  // [batch * rows]
+  float* ws_o;
+  float* ws_lse;
+  int32_t* ws_info;
+  int32_t* d_error;            // nullable
+  int batch, s, h, rows;       // rows = s * h query rows of a sequence
+  int max_pages, window, sinks;
+  int64_t num_pages;
+  float scale_log2;            // sm_scale * log2(e)
+};
+struct PagedPlan {
+  int nr;          // query rows a CTA works on: 16, 32 or 64
+  int groups;      // row groups of a sequence
+  int num_parts;
+  size_t ws_o_bytes, ws_lse_bytes, ws_bytes;
+};
+PagedPlan paged_plan(const mla_paged_problem_t* p, int num_parts);
+cudaError_t launch_paged_decode(const PagedParams& p, const PagedPlan& plan, cudaStream_t stream);
+
 // cuTensorMapEncodeTiled from the driver, looked up once (thread-safe
 // static initialization); nullptr if the driver does not offer it.
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,

@@ -62,7 +62,9 @@ enum {
 enum {
   MLA_DEVERR_BAD_INDEX = 1,     /* an index was < -1 or >= num_pages*64; that entry was skipped */
   MLA_DEVERR_TIMEOUT = 2,       /* a bounded on-chip wait gave up; outputs are undefined */
-  MLA_DEVERR_BAD_METADATA = 4   /* scheduler metadata inconsistent with the problem; work skipped */
+  MLA_DEVERR_BAD_METADATA = 4,  /* scheduler metadata inconsistent with the problem; work skipped */
+  MLA_DEVERR_NO_ROOM = 8,       /* page plan: not enough free pages, or more new tokens than slots */
+  MLA_DEVERR_BAD_LENGTH = 16    /* a request length is negative or past its block table row */
 };
 
 #define MLA_HEAD_DIM 512
@@ -276,6 +278,174 @@ mla_status_t mla_sparse_decode_noalloc(const mla_problem_t* problem,
  */
 mla_status_t mla_kv_write(int32_t kv_format, const void* latents, const int32_t* slots, int64_t n, void* pool,
                           int64_t num_pages, int32_t* d_error, mla_stream_t stream);
+
+/*
+ * Block tables and slot maps of a paged pool, built on the device from
+ * request lengths: where mla_kv_write puts each new token, which pages
+ * mla_paged_decode_fp4 reads, and which position mla_rope turns it to.  One
+ * call per step and no host synchronisation, so a captured graph replays it.
+ *
+ * Request r holds cached_lens[r] = c tokens in the first ceil(c / 64) entries
+ * of its block table row and appends new_lens[r] = n tokens:
+ *   n >= 0  it takes ceil((c + n) / 64) - ceil(c / 64) pages from the top of
+ *           the free stack, in request order (its first new page is the topmost
+ *           one left), and they follow its held pages in its row.  New token i
+ *           has position p = c + i and slot 64 * row[p / 64] + p % 64.
+ *   n = -1  the request has ended: its held pages go back onto the stack (in
+ *           request and row order, all before any page is taken); its length
+ *           becomes 0 and its row is left as it is.
+ * The tokens are packed in request order: those of r at cu_new[r] ..
+ * cu_new[r + 1] - 1 of slots and positions.  Entries from cu_new[batch] on to
+ * max_new get slot -1 (which mla_kv_write skips) and position 0.
+ *
+ *   cached_lens, new_lens  int32 [batch].
+ *   block_table   int32 [batch][max_pages]; only entries of pages taken are written.
+ *   free_pages    int32 [num_pages]: the stack of free page ids, top last.
+ *   num_free      int32 [1]: how many there are.
+ *   seq_lens      int32 [batch], written: c + n (may be cached_lens itself).
+ *   num_free_out  int32 [1], written (may be num_free itself).
+ *   cu_new        int32 [batch + 1], written.
+ *   slots, positions  int32 [max_new], written to the end.
+ *   d_error       device int32 or NULL; bits are OR-ed into it.
+ * The call refuses as a whole -- tables, stack and lengths stay as they are,
+ * cu_new is all 0 and every slot -1 -- when a length is negative or past
+ * 64 * max_pages (MLA_DEVERR_BAD_LENGTH), when pages or slots do not suffice
+ * (MLA_DEVERR_NO_ROOM), or when num_free lies outside [0, num_pages] or more
+ * pages come back than the stack holds (MLA_DEVERR_BAD_METADATA).  A page id
+ * outside [0, num_pages) gives its tokens slot -1 and MLA_DEVERR_BAD_INDEX.
+ * batch is at most 8192 and num_pages * 64 below 2^31 (MLA_ERR_UNSUPPORTED).
+ * Apart from the two pairs named, no buffer may overlap another.
+ */
+mla_status_t mla_page_plan(const int32_t* cached_lens, const int32_t* new_lens, int32_t batch,
+                           int32_t* block_table, int32_t max_pages,
+                           int32_t* free_pages, int32_t num_pages, const int32_t* num_free,
+                           int32_t* seq_lens, int32_t* num_free_out, int32_t* cu_new,
+                           int32_t* slots, int32_t* positions, int32_t max_new,
+                           int32_t* d_error, mla_stream_t stream);
+
+/* Element types of activations. */
+enum { MLA_BF16 = 0, MLA_FP16 = 1, MLA_FP32 = 2 };
+
+/*
+ * Rotary positions.  A table holds, for each of the rope_dim / 2 pairs, the
+ * turns per position as a 64-bit fixed-point fraction: position times step,
+ * modulo 2^64, is the exact phase at any int32 position, so far positions
+ * lose nothing and no cosine table is read.
+ */
+enum { MLA_ROPE_INTERLEAVED = 0, MLA_ROPE_HALF = 1 };     /* pairs (2j, 2j+1), or (j, j + rope_dim/2) */
+enum { MLA_ROPE_PLAIN = 0, MLA_ROPE_LINEAR = 1, MLA_ROPE_YARN = 2 };
+#define MLA_ROPE_MAX_DIM 256
+typedef struct {
+  int32_t rope_dim;          /* even, 2 .. MLA_ROPE_MAX_DIM */
+  int32_t layout;            /* MLA_ROPE_INTERLEAVED or MLA_ROPE_HALF */
+  float factor;              /* on the rotated dims (the attention factor of long contexts), finite */
+  uint64_t step[MLA_ROPE_MAX_DIM / 2];
+} mla_rope_table_t;
+
+/*
+ * Fill a table (host only) from frequencies f_j in radians per position:
+ * step_j = f_j / (2 pi) * 2^64, |f_j| <= pi.  mla_rope_table computes
+ * f_j = theta^(-2j / rope_dim) and scales it for contexts past original_len:
+ *   MLA_ROPE_LINEAR  f_j / scale.
+ *   MLA_ROPE_YARN    f_j (1 - g_j) + f_j / scale * g_j with the ramp
+ *                    g_j = clamp((j - lo) / max(hi - lo, 0.001), 0, 1), where
+ *                    dim(r) = rope_dim ln(original_len / (2 pi r)) / (2 ln theta),
+ *                    lo = max(floor(dim(beta_fast)), 0),
+ *                    hi = min(ceil(dim(beta_slow)), rope_dim - 1).
+ * factor is taken as given (YaRN models commonly use 0.1 ln(scale) + 1).
+ */
+mla_status_t mla_rope_table(mla_rope_table_t* table, int32_t rope_dim, int32_t layout, double theta,
+                            int32_t scaling, double scale, double original_len, double beta_fast, double beta_slow,
+                            double factor);
+mla_status_t mla_rope_table_from_freqs(mla_rope_table_t* table, int32_t rope_dim, int32_t layout,
+                                       const double* freqs, double factor);
+
+/*
+ * y = x with dims offset .. offset + rope_dim - 1 of every head turned:
+ * pair (a, b) at position p -> factor * (a cos - b sin, b cos + a sin) of the
+ * angle p f_j, computed in fp32 and rounded once.  The other dims are copied
+ * (out of place) or left (in place).  With conjugate != 0 the angle is
+ * negated: the transpose, which takes a gradient of y to the gradient of x.
+ *   x, y      dtype [n][heads][head_dim] with element strides row_stride and
+ *             head_stride (the last dim dense), element aligned; y may be x
+ *             itself with the same strides (in place) and must not overlap
+ *             it otherwise.
+ *   positions int32 [n].
+ * Rows that start on 16-byte boundaries and ranges that are whole 16-byte
+ * pieces move in 16-byte accesses, others element by element.
+ */
+mla_status_t mla_rope(int32_t dtype, const void* x, int64_t x_row_stride, int64_t x_head_stride, void* y,
+                      int64_t y_row_stride, int64_t y_head_stride, int64_t n, int32_t heads, int32_t head_dim,
+                      int32_t offset, const int32_t* positions, const mla_rope_table_t* table, int32_t conjugate,
+                      mla_stream_t stream);
+
+/*
+ * Root-mean-square norm with the residual's addition, cast to FP8 blocks:
+ *     s = x + residual        (fp32; residual may be NULL)
+ *     residual_out = s        (rounded to dtype; may be residual itself, NULL to drop it)
+ *     v = s / sqrt(mean(s^2) + eps) * weight          (fp32 throughout)
+ * and per 32 values of v the least power of two 2^e with amax * 2^-e <= 448
+ * (scale byte 127 + e; 127 for an all-zero block; e >= -127), each value
+ * rounded to the nearest E4M3FN.  The norm is taken of the unrounded sum.
+ * codes and scales have row strides of their own, so with dim 512, codes = r
+ * and scales = r + 512 at stride 528 the rows are cache records.
+ *   x, residual, residual_out, weight  dtype; rows at element strides, each
+ *             row 16-byte aligned (weight [dim], 16-byte aligned).
+ *   codes     uint8, rows 8-byte aligned; scales uint8 [n][dim / 32].
+ *   dim       a multiple of 32, at most 16384 (MLA_ERR_UNSUPPORTED otherwise).
+ * Infinities and NaN in a row make that row's codes undefined; no other row.
+ */
+mla_status_t mla_rms_norm_fp8(int32_t dtype, const void* x, int64_t x_stride, const void* residual,
+                              int64_t residual_stride, const void* weight, float eps, void* residual_out,
+                              int64_t residual_out_stride, void* codes, int64_t codes_stride, void* scales,
+                              int64_t scales_stride, int64_t n, int32_t dim, mla_stream_t stream);
+
+/*
+ * Attention over the pages of a cache held in 4 bits: every query token sees
+ * the tokens of its own sequence, all of them or a window and the first few.
+ */
+typedef struct {
+  int32_t batch;        /* b >= 1 */
+  int32_t seq_len_q;    /* s >= 1: the last s tokens of each sequence are the query tokens */
+  int32_t h_q;          /* query heads, 1 .. 128 */
+  int32_t head_dim;     /* must be 512 */
+  int32_t page_size;    /* must be 64 */
+  int32_t max_pages;    /* entries of a block table row */
+  int32_t window;       /* tokens seen back from the query token, itself included; 0 = all */
+  int32_t sinks;        /* the first tokens of a sequence, seen whatever the window */
+  int64_t num_pages;    /* pages in the pool (bounds check of the block table) */
+  int32_t kv_format;    /* must be MLA_KV_FP4_288 */
+  float sm_scale;       /* softmax scale applied to q.k */
+} mla_paged_problem_t;
+
+/* Host-only planning: the part count (num_sms = 0 asks the current device) and the workspace bytes. */
+mla_status_t mla_paged_decode_plan(const mla_paged_problem_t* problem, int32_t num_sms, int32_t* num_parts_out,
+                                   size_t* workspace_bytes_out);
+
+/*
+ * One attention step.  Query token i of sequence b stands at position
+ * p = seq_lens[b] - s + i and sees the cached tokens j <= p with
+ * window == 0, j > p - window or j < sinks; over those, with latents k_j,
+ *     lse = ln sum_j exp(sm_scale <q, k_j>),  out = sum_j exp(sm_scale <q, k_j> - lse) k_j.
+ * A query token that sees nothing (an empty sequence, p < 0) gets +0 and -inf.
+ *   q            bf16 [batch][s][h_q][512], 16-byte aligned, finite.
+ *   kv           uint8 [num_pages][64][288] FP4 records, 16-byte aligned.
+ *                Records past a sequence's end are never used, whatever bytes they hold.
+ *   block_table  int32 [batch][max_pages]: page ids; entries past ceil(len / 64) are not read.
+ *                The tokens of a page id outside [0, num_pages) are skipped
+ *                and flagged (MLA_DEVERR_BAD_INDEX).
+ *   seq_lens     int32 [batch] (device), the query tokens included; negative or past
+ *                64 * max_pages: treated as 0 and flagged (MLA_DEVERR_BAD_LENGTH).
+ *   num_parts, workspace, workspace_bytes   as mla_paged_decode_plan says; the
+ *                workspace is 16-byte aligned and needs no initialisation.
+ *                Calls that share one must not overlap.
+ *   out          bf16 [batch][s][h_q][512], 16-byte aligned;  lse  float [batch][s][h_q].
+ *   d_error      device int32 or NULL.
+ */
+mla_status_t mla_paged_decode_fp4(const mla_paged_problem_t* problem, const void* q, const void* kv,
+                                  const int32_t* block_table, const int32_t* seq_lens, int32_t num_parts,
+                                  void* workspace, size_t workspace_bytes, void* out, float* lse, int32_t* d_error,
+                                  mla_stream_t stream);
 
 /* Static description of a status code. */
 const char* mla_status_string(mla_status_t status);
