@@ -111,7 +111,7 @@ mla_status_t validate_paged(const mla_paged_problem_t* p) {
   if (p->head_dim != MLA_HEAD_DIM || p->page_size != MLA_PAGE_SIZE || p->h_q > 128) return MLA_ERR_UNSUPPORTED;
   // Positions, rows and tiles are counted in 32 bits.
   const int64_t most = int64_t(1) << 31, rows = static_cast<int64_t>(p->seq_len_q) * p->h_q;
-  if (static_cast<int64_t>(p->max_pages) * MLA_PAGE_SIZE >= most || rows * p->batch >= most ||
+  if (static_cast<int64_t>(p->max_pages) * MLA_PAGE_SIZE >= most - 256 || rows * p->batch >= most ||
       static_cast<int64_t>(p->batch) * p->max_pages >= most)
     return MLA_ERR_UNSUPPORTED;
   const int64_t units = p->batch * ((rows + 15) / 16);

@@ -1,10 +1,52 @@
 // paged.cu -- attention over the pages of a cache held in 4 bits
-// (include/mla.h, mla_paged_decode_fp4).
+// (include/mla.h, mla_paged_decode_fp4), on the tensor cores of sm_103a.
 //
-// One block per sixteen query rows of a sequence; tiles of 32 tokens are
-// decoded to fp32 in shared memory and attended with an online softmax.
+// For every query row (query token x head) r of a sequence, over the cached
+// tokens j that its mask lets it see, each decoded from its FP4 record to a
+// 512-dim latent k_j that is key and value:
+//     x_rj = scale <q_r, k_j>,  m_r = running maximum,  p_rj = 2^(x_rj - m_r),
+//     l_r = sum_j p_rj,  O_r = sum_j p_rj k_j,  out = O / l,  lse = m + log l.
+//
+// Work.  A unit is one group of up to NR (16, 32 or 64) query rows of one
+// sequence; its items are the 128-token tiles that some row of it sees (the
+// tiles of the sinks and of the window only).  All items in order are cut
+// into gridDim.x equal runs, one per CTA (one CTA per SM); the lengths are on
+// the device, so every CTA derives the cut itself by a scan over the units.
+// A unit cut by a run's end leaves normalised fp32 partials, merged by a
+// second kernel.
+//
+// One CTA, 18 warps (26 with 64 rows):
+//   loader (1 warp)    each tile's two pages by bulk copies (records are
+//                      contiguous in a page) into a ring of raw FP4 tiles.
+//   K warps (4)        raw FP4 -> f16 into tensor memory, lane = token: the A
+//                      operand of S^T = K Q^T, a 128-dim quarter at a time.
+//   V warps (4)        raw FP4 -> f16 into shared memory (128-byte swizzle),
+//                      in units of 64 tokens x 128 dims: the MN-major A
+//                      operand of O^T += V^T P^T.
+//   issuer (1 warp)    all tensor-core work; S^T of the next tile goes before
+//                      O^T of this one, so the softmax runs beside O^T.
+//   softmax (8 or 16)  thread = token x 8 or 16 rows: scale, mask, lazy
+//                      running maximum, P^T to shared memory, row sums in
+//                      registers; at a unit's end the epilogue, before it
+//                      the next unit's Q.
+// A tile is decoded twice (K to tensor memory, V to shared memory) because
+// that is cheaper than the shared memory it saves: one f16 tile is 128 KB,
+// and kept from S^T to O^T it would leave room for nothing beside it; raw it
+// is 36 KB, so two or three tiles are in flight and neither copy of a quarter
+// lives longer than the product that reads it.  With K in tensor memory
+// shared memory carries 128 KB of V in and out per tile and the small
+// operands, which is what bounds the kernel.
+//
+// Numbers.  e2m1 x e4m3 has at most 6 significant bits and lies in f16's
+// range, so K and V are exact in f16.  Q (bf16) is scaled by a power of two
+// per row to put its largest value in [2^14, 2^15) and is then exact in f16
+// down to 2^-28 of that; below, 2^-39 of the row's largest value is lost.  P
+// is f16 with the maximum at 2^7 (at most 2^15 with the lazy maximum's slack
+// of 2^8): 11 bits, where bf16 has 8, and weights down to 2^-31 of the
+// largest still count.  Sums, maxima and O are fp32.
 #include <cstdint>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "mla_device.cuh"
 #include "mla_internal.h"
@@ -13,114 +55,936 @@ namespace mla {
 
 namespace {
 
-constexpr int kRows = 16;
-constexpr int kTokens = 32;
-constexpr int kStride = 516;
-constexpr int kSmem = (kRows + kTokens) * kStride * 4 + kRows * (kTokens + 3) * 4;
+constexpr int kRawBytes = kTile * kRecFp4;   // one tile of records
+constexpr int kPageBytes = kPage * kRecFp4;
+constexpr int kVUnitBytes = 64 * 128 * 2;    // 64 tokens x 128 dims
+constexpr int kVUnits = 8;                   // per tile: two token halves x four dim quarters
+constexpr int kInfoRing = 8;
+constexpr uint64_t kPagedWaitNs = 2000000000ull;  // 2 s per wait
+constexpr float kSlack = 8.f;                // the running maximum may lag by 2^8
+constexpr float kPBias = 7.f;                // P of the maximum is 2^7
+constexpr float kNoMax = -3.0e38f;           // running maximum before any visible token
 
-__global__ void __launch_bounds__(256) paged_simple_kernel(const PagedParams p, int groups) {
-  extern __shared__ float smf[];
-  float* sq = smf;
-  float* sk = sq + kRows * kStride;
-  float* sp = sk + kTokens * kStride;
-  float* sm = sp + kRows * kTokens;
-  float* sl = sm + kRows;
-  float* sa = sl + kRows;
+template <int NR>
+struct PSmem {
+  // Softmax threads hold 16 rows each (8 with 16 rows): scores and sums stay in registers.
+  static constexpr int kSides = NR == 64 ? 4 : 2;
+  static constexpr int kSoftmaxWarps = 4 * kSides;
+  static constexpr int kKWarp0 = kSoftmaxWarps, kVWarp0 = kKWarp0 + 4, kLoadWarp = kVWarp0 + 4, kMmaWarp = kLoadWarp + 1;
+  static constexpr int kThreads = (kMmaWarp + 1) * 32;
+  static constexpr int kRaw = NR == 16 ? 3 : 2;                    // raw tiles
+  static constexpr int kKRing = NR == 64 ? 2 : 4;                  // K quarters in tensor memory
+  static constexpr int kVRing = NR == 64 ? 3 : (NR == 32 ? 6 : 5);  // V units
+  static constexpr int kQBytes = NR * kD * 2;
+  static constexpr int kPBytes = kTile * NR * 2;
+  static constexpr int kQOff = 0;
+  static constexpr int kVOff = kQOff + kQBytes;
+  static constexpr int kPOff = kVOff + kVRing * kVUnitBytes;
+  static constexpr int kRawOff = kPOff + 2 * kPBytes;
+  static constexpr int kBarOff = kRawOff + kRaw * kRawBytes;
+  static constexpr int kNumBars = 2 * kRaw + 2 * kKRing + 2 * kVRing + 8 + 3 + kInfoRing;
+  static constexpr int kColOff = (kBarOff + kNumBars * 8 + 15) & ~15;  // per-row arrays
+  // float m[NR], alpha[NR], scale[NR], linv[NR]; int hi[NR], lo[NR]; float red[4][NR]
+  static constexpr int kInfoOff = kColOff + 10 * NR * 4;
+  static constexpr int kMiscOff = kInfoOff + kInfoRing * 16;
+  static constexpr int kEnd = kMiscOff + 256;
+  static constexpr int kAlloc = kEnd + 1024;
+  static_assert(kAlloc <= 232448, "shared memory of one CTA");
+  // Barrier indices.
+  static constexpr int bRawFull = 0, bRawFree = bRawFull + kRaw, bKFull = bRawFree + kRaw, bKFree = bKFull + kKRing,
+                       bVFull = bKFree + kKRing, bVFree = bVFull + kVRing, bSFull = bVFree + kVRing,
+                       bSFree = bSFull + 2, bPFull = bSFree + 2, bPFree = bPFull + 2, bQFull = bPFree + 2,
+                       bOFree = bQFull + 1, bDrain = bOFree + 1, bInfo = bDrain + 1;
+  static_assert(bInfo + kInfoRing == kNumBars, "barriers");
+  // Tensor memory columns: O^T quarters, S^T buffers, K quarters.
+  static constexpr int cO = 0, cS = 4 * NR, cK = 6 * NR;
+  static_assert(cK + kKRing * 64 <= 512, "tensor memory");
+};
+
+// ------------------------------------------------------------------ geometry
+
+// The tiles that a unit's rows see.
+struct Unit {
+  int b, row0, nrows;   // sequence, first row of the group, rows in it
+  int first;            // position of the sequence's first query token
+  int p_lo, p_hi;       // positions of the group's first and last query token
+  int sink_tiles;       // tiles of the sinks that lie before the window's
+  int win_tile;         // first tile of the window
+  int start;            // first position of the window
+  int tiles;            // at least 1 (a unit that sees nothing still writes its rows)
+};
+
+__device__ __forceinline__ int checked_len(const PagedParams& p, int b, bool& bad) {
+  const int len = __ldg(p.seq_lens + b);
+  bad = len < 0 || len > p.max_pages * kPage;
+  return bad ? 0 : len;
+}
+
+// First position that the window of a query token at `at` holds.
+__device__ __forceinline__ int window_start(const PagedParams& p, int at) {
+  const int64_t from = static_cast<int64_t>(at) - p.window + 1;
+  return p.window > 0 && from > 0 ? static_cast<int>(from) : 0;
+}
+
+template <int NR>
+__device__ __forceinline__ Unit unit_of(const PagedParams& p, int groups, int u, bool& bad) {
+  Unit t;
+  t.b = u / groups;
+  t.row0 = (u - t.b * groups) * NR;
+  t.nrows = min(NR, p.rows - t.row0);
+  const int len = checked_len(p, t.b, bad);
+  t.first = len - p.s;
+  t.p_lo = t.first + t.row0 / p.h;
+  t.p_hi = t.first + (t.row0 + t.nrows - 1) / p.h;
+  const int end = max(t.p_hi + 1, 0);
+  t.start = window_start(p, t.p_lo);
+  t.start = min(t.start, end);
+  t.win_tile = t.start / kTile;
+  t.sink_tiles = min((min(p.sinks, end) + kTile - 1) / kTile, t.win_tile);
+  t.tiles = max(t.sink_tiles + (end + kTile - 1) / kTile - t.win_tile, 1);
+  return t;
+}
+
+__device__ __forceinline__ int tile_of(const Unit& u, int k) {
+  return k < u.sink_tiles ? k : u.win_tile + (k - u.sink_tiles);
+}
+
+// What the loader tells the other warps of an item: {tokens of page 0 |
+// tokens of page 1 << 8 | flags << 16, tile, unit, -}.  A piece is the part of
+// a unit that lies in this CTA's run.
+enum : int {
+  kOpens = 1 << 16,      // first item of a piece
+  kCloses = 2 << 16,     // last item of a piece
+  kFromStart = 4 << 16,  // the piece begins with its unit
+  kToEnd = 8 << 16,      // the piece ends with its unit
+  kWhole = 16 << 16      // every row sees every token
+};
+__device__ __forceinline__ bool token_there(int info, int row) {
+  return (row & 63) < ((info >> (row >= 64 ? 8 : 0)) & 0xFF);
+}
+
+// ------------------------------------------------------------------ small wrappers
+
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
+  static_assert(N == 8 || N == 16 || N == 32, "columns");
+  if constexpr (N == 8) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+        : "r"(taddr)
+        : "memory");
+  } else if constexpr (N == 16) {
+    tmem_ld16(taddr, r);
+  } else {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,"
+        "%29,%30,%31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+  }
+}
+
+// One elected lane of a converged warp issues; A in tensor memory or shared memory.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void commit_one(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void expect_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+               "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// Instruction descriptor of kind::f16 with f16 operands and fp32 accumulation.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn, bool b_mn) {
+  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// 32 consecutive dims of a record: 16 data bytes and their two scale bytes
+// (sc, low byte first) -> 16 f16x2, exact.
+__device__ __forceinline__ void decode32(const uint4& data, uint32_t sc, uint32_t (&o)[16]) {
+  const uint32_t s2 = e4m3x2_to_f16x2(sc);
+  const uint32_t s0 = __byte_perm(s2, s2, 0x1010), s1 = __byte_perm(s2, s2, 0x3232);
+  const uint32_t w[4] = {data.x, data.y, data.z, data.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t a, b, c, d;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+        : "r"(w[k]));
+    const uint32_t s = k < 2 ? s0 : s1;
+    o[4 * k + 0] = mul_f16x2(a, s);
+    o[4 * k + 1] = mul_f16x2(b, s);
+    o[4 * k + 2] = mul_f16x2(c, s);
+    o[4 * k + 3] = mul_f16x2(d, s);
+  }
+}
+
+// Reduction of v[N] over the 32 lanes; afterwards lane l holds in v[0 ..
+// max(N/32, 1)) the columns column_of<N>(l).
+template <int SIZE, int O>
+struct LaneReduce {
+  template <int N, typename Op>
+  __device__ __forceinline__ static void run(float (&v)[N], int lane, Op op) {
+    if constexpr (O == 0) {
+      return;
+    } else if constexpr (SIZE == 1) {
+      v[0] = op(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], O));
+      LaneReduce<1, O / 2>::run(v, lane, op);
+    } else {
+      constexpr int H = SIZE / 2;
+      const bool up = (lane & O) != 0;
+#pragma unroll
+      for (int k = 0; k < H; ++k) {
+        const float send = up ? v[k] : v[k + H];
+        const float keep = up ? v[k + H] : v[k];
+        v[k] = op(keep, __shfl_xor_sync(0xFFFFFFFFu, send, O));
+      }
+      LaneReduce<H, O / 2>::run(v, lane, op);
+    }
+  }
+};
+template <int N>
+__device__ __forceinline__ int column_of(int lane) {
+  static_assert(N <= 32, "one column per lane");
+  return lane / (32 / N);
+}
+struct OpMax {
+  __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+struct OpAdd {
+  __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+
+__device__ __forceinline__ bool any_of(int id, int threads, bool mine) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred pi, po;\n\t"
+      "setp.ne.s32 pi, %1, 0;\n\t"
+      "bar.red.or.pred po, %2, %3, pi;\n\t"
+      "selp.s32 %0, 1, 0, po;\n\t}"
+      : "=r"(r)
+      : "r"(mine ? 1 : 0), "r"(id), "r"(threads)
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// ------------------------------------------------------------------ the kernel
+
+template <int NR>
+__global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(const PagedParams p, const int groups) {
+  using L = PSmem<NR>;
+  constexpr int NC = NR / L::kSides;  // rows of a softmax thread
+  constexpr int kPagedThreads = L::kThreads, kSoftmaxWarps = L::kSoftmaxWarps;
+  constexpr int kKWarp0 = L::kKWarp0, kVWarp0 = L::kVWarp0, kLoadWarp = L::kLoadWarp, kMmaWarp = L::kMmaWarp;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem + L::kQOff;
+  uint8_t* sV = smem + L::kVOff;
+  uint8_t* sP = smem + L::kPOff;
+  uint8_t* sRaw = smem + L::kRawOff;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
+  float* c_m = reinterpret_cast<float*>(smem + L::kColOff);
+  float* c_alpha = c_m + NR;
+  float* c_scale = c_alpha + NR;
+  float* c_linv = c_scale + NR;
+  int* c_hi = reinterpret_cast<int*>(c_linv + NR);
+  int* c_lo = c_hi + NR;
+  float* red = reinterpret_cast<float*>(c_lo + NR);
+  int4* info = reinterpret_cast<int4*>(smem + L::kInfoOff);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
+  int* start_u = reinterpret_cast<int*>(smem + L::kMiscOff + 8);    // {unit, items before it}
+  int* warp_sum = reinterpret_cast<int*>(smem + L::kMiscOff + 32);  // [warps]
+
   const int tid = threadIdx.x;
-  const int b = blockIdx.x / groups, r0 = (blockIdx.x % groups) * kRows;
-  int len = p.seq_lens[b];
-  if (len < 0 || len > p.max_pages * 64) {
-    if (tid == 0 && p.d_error) atomicOr(p.d_error, MLA_DEVERR_BAD_LENGTH);
-    len = 0;
+  const int warp = tid >> 5;
+  const int lane = tid & 31;
+  const int part = blockIdx.x;
+
+  if (tid == 0) {
+    for (int i = 0; i < L::kRaw; ++i) {
+      mbar_init(&bars[L::bRawFull + i], 1);
+      mbar_init(&bars[L::bRawFree + i], 8);
+    }
+    for (int i = 0; i < L::kKRing; ++i) {
+      mbar_init(&bars[L::bKFull + i], 4);
+      mbar_init(&bars[L::bKFree + i], 1);
+    }
+    for (int i = 0; i < L::kVRing; ++i) {
+      mbar_init(&bars[L::bVFull + i], 4);
+      mbar_init(&bars[L::bVFree + i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars[L::bSFull + i], 1);
+      mbar_init(&bars[L::bSFree + i], kSoftmaxWarps);
+      mbar_init(&bars[L::bPFull + i], kSoftmaxWarps);
+      mbar_init(&bars[L::bPFree + i], 1);
+    }
+    mbar_init(&bars[L::bQFull], kSoftmaxWarps);
+    mbar_init(&bars[L::bOFree], kSoftmaxWarps);
+    mbar_init(&bars[L::bDrain], 1);
+    for (int i = 0; i < kInfoRing; ++i) mbar_init(&bars[L::bInfo + i], 1);
+    *abort_flag = 0;
+    start_u[0] = -1;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_proxy_async_smem();
   }
-  const uint16_t* q = p.q + (static_cast<int64_t>(b) * p.rows + r0) * 512;
-  for (int e = tid; e < kRows * 512; e += 256) {
-    const int r = e >> 9;
-    sq[r * kStride + (e & 511)] = r0 + r < p.rows ? __uint_as_float(static_cast<uint32_t>(q[e]) << 16) * p.scale_log2 : 0.f;
+  if (warp == kMmaWarp) tmem_alloc(tmem_slot, 512);
+
+  // The cut: items of all units, this part's run, and the unit it begins in.
+  const int units = p.batch * groups;
+  const int per = (units + kPagedThreads - 1) / kPagedThreads;
+  const int u_a = min(units, tid * per), u_b = min(units, u_a + per);
+  int mine = 0;
+  for (int u = u_a; u < u_b; ++u) {
+    bool bad;
+    mine += unit_of<NR>(p, groups, u, bad).tiles;
+    if (bad && part == 0 && p.d_error) atomicOr(p.d_error, MLA_DEVERR_BAD_LENGTH);
   }
-  if (tid < kRows) {
-    sm[tid] = -INFINITY;
-    sl[tid] = 0.f;
-  }
-  float acc[2][kRows];
+  int incl = mine;
 #pragma unroll
-  for (int r = 0; r < kRows; ++r) acc[0][r] = acc[1][r] = 0.f;
-  const int first = len - p.s;
-  int p_lo = first + r0 / p.h, p_hi = first + min(p.rows - 1, r0 + kRows - 1) / p.h;
-  for (int t0 = 0; t0 <= p_hi; t0 += kTokens) {
-    if (p.window > 0 && t0 >= p.sinks && t0 + kTokens - 1 <= p_lo - p.window) continue;
-    __syncthreads();
-    for (int e = tid; e < kTokens * 256; e += 256) {
-      const int t = e >> 8, k = e & 255;
-      float lo = 0.f, hi = 0.f;
-      if (t0 + t < len) {
-        const int page = p.block_table[static_cast<int64_t>(b) * p.max_pages + ((t0 + t) >> 6)];
-        if (page >= 0 && page < p.num_pages) {
-          const uint8_t* rec = p.kv + (static_cast<int64_t>(page) * 64 + ((t0 + t) & 63)) * kRecFp4;
-          const uint32_t s16 = e4m3x2_to_f16x2(rec[256 + (k >> 3)]);
-          const uint32_t v16 = e2m1x2_to_f16x2(rec[k]);
-          const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(s16 & 0xFFFF)));
-          lo = s * __half2float(__ushort_as_half(static_cast<unsigned short>(v16 & 0xFFFF)));
-          hi = s * __half2float(__ushort_as_half(static_cast<unsigned short>(v16 >> 16)));
-        }
-      }
-      sk[t * kStride + 2 * k] = lo;
-      sk[t * kStride + 2 * k + 1] = hi;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  int before = 0, total = 0;
+  for (int w = 0; w < kPagedThreads / 32; ++w) {
+    const int v = warp_sum[w];
+    if (w < warp) before += v;
+    total += v;
+  }
+  const int share = (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+  const int64_t g0_wide = static_cast<int64_t>(part) * share;
+  const int g0 = static_cast<int>(min(g0_wide, static_cast<int64_t>(total)));
+  const int g1 = static_cast<int>(min(g0_wide + share, static_cast<int64_t>(total)));
+  const int excl = before + incl - mine;
+  if (g0 < g1 && excl <= g0 && g0 < excl + mine) {
+    int at = excl, u = u_a;
+    for (;; ++u) {
+      bool bad;
+      const int t = unit_of<NR>(p, groups, u, bad).tiles;
+      if (g0 < at + t) break;
+      at += t;
     }
-    __syncthreads();
-    for (int e = tid; e < kRows * kTokens; e += 256) {
-      const int r = e / kTokens, t = e % kTokens, j = t0 + t;
-      const int at = first + (r0 + r) / p.h;
-      bool see = r0 + r < p.rows && j <= at && (p.window == 0 || j > at - p.window || j < p.sinks);
-      if (see) {
-        const int page = p.block_table[static_cast<int64_t>(b) * p.max_pages + (j >> 6)];
-        if (page < 0 || page >= p.num_pages) {
-          see = false;
-          if (p.d_error) atomicOr(p.d_error, MLA_DEVERR_BAD_INDEX);
-        }
-      }
-      float x = 0.f;
-      if (see)
-        for (int d = 0; d < 512; ++d) x = fmaf(sq[r * kStride + d], sk[t * kStride + d], x);
-      sp[e] = see ? x : -INFINITY;
-    }
-    __syncthreads();
-    if (tid < kRows) {
-      float m = sm[tid];
-      for (int t = 0; t < kTokens; ++t) m = fmaxf(m, sp[tid * kTokens + t]);
-      const float a = m == -INFINITY ? 0.f : exp2f(sm[tid] - m);
-      float l = 0.f;  // the tile's own sum first, so that long rows lose no digits
-      for (int t = 0; t < kTokens; ++t) {
-        const float e = m == -INFINITY ? 0.f : exp2f(sp[tid * kTokens + t] - m);
-        sp[tid * kTokens + t] = e;
-        l += e;
-      }
-      sm[tid] = m;
-      sl[tid] = sl[tid] * a + l;
-      sa[tid] = a;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      float u = acc[0][r] * sa[r], v = acc[1][r] * sa[r];
-      for (int t = 0; t < kTokens; ++t) {
-        u = fmaf(sp[r * kTokens + t], sk[t * kStride + 2 * tid], u);
-        v = fmaf(sp[r * kTokens + t], sk[t * kStride + 2 * tid + 1], v);
-      }
-      acc[0][r] = u;
-      acc[1][r] = v;
-    }
+    start_u[0] = u;
+    start_u[1] = at;
   }
   __syncthreads();
+  const uint32_t tmem = *tmem_slot;
+
+  if (g0 >= g1) {
+    if (tid == 0) p.ws_info[part * 4] = -1;
+  } else {
+    const uint32_t items = static_cast<uint32_t>(g1 - g0);
+
+    if (warp == kLoadWarp) {
+      // ---------------------------------------------------------------- loader
+      // It alone walks the units; the others read what it found.
+      int u = start_u[0], k = g0 - start_u[1];
+      bool bad_len;
+      Unit unit = unit_of<NR>(p, groups, u, bad_len);
+      for (uint32_t n = 0; n < items; ++n) {
+        const int slot = n % L::kRaw;
+        if (n >= L::kRaw)
+          mbar_wait(&bars[L::bRawFree + slot], (n / L::kRaw - 1) & 1, abort_flag, p.d_error, kPagedWaitNs);
+        const int tile = tile_of(unit, k);
+        const int end = unit.p_hi + 1;
+        // Lane j < 2 looks after page j of the tile: copied up to the last
+        // visible token, not at all when the window and the sinks leave it out.
+        int tokens = 0;
+        bool bad = false;
+        const uint8_t* src = nullptr;
+        if (lane < 2) {
+          const int pos = tile * kTile + lane * kPage;
+          const bool seen = pos < end && (pos + kPage > unit.start || pos < p.sinks);
+          if (seen) {
+            const int page = __ldg(p.block_table + static_cast<int64_t>(unit.b) * p.max_pages + tile * 2 + lane);
+            if (page >= 0 && page < p.num_pages) {
+              tokens = min(kPage, end - pos);
+              src = p.kv + static_cast<int64_t>(page) * kPageBytes;
+            } else {
+              bad = true;
+            }
+          }
+        }
+        if (bad && p.d_error) atomicOr(p.d_error, MLA_DEVERR_BAD_INDEX);
+        const int t0 = __shfl_sync(0xFFFFFFFFu, tokens, 0), t1 = __shfl_sync(0xFFFFFFFFu, tokens, 1);
+        if (lane == 0) {
+          int word = t0 | (t1 << 8);
+          const int t_end = tile * kTile + kTile - 1;
+          if (t0 + t1 == kTile && t_end <= unit.p_lo &&
+              (p.window == 0 || tile * kTile > unit.p_hi - p.window || t_end < p.sinks))
+            word |= kWhole;
+          if (n == 0 || k == 0) word |= kOpens;
+          if (n + 1 == items || k + 1 == unit.tiles) word |= kCloses;
+          // A piece begins with its unit unless the run's first item lies inside the unit.
+          if (!(g0 > start_u[1] && u == start_u[0])) word |= kFromStart;
+          if (k + 1 == unit.tiles) word |= kToEnd;
+          info[n % kInfoRing] = make_int4(word, tile, u, 0);
+          mbar_arrive(&bars[L::bInfo + n % kInfoRing]);
+          expect_tx(&bars[L::bRawFull + slot], static_cast<uint32_t>(t0 + t1) * kRecFp4);
+        }
+        __syncwarp();
+        if (tokens > 0)
+          bulk_load(sRaw + slot * kRawBytes + lane * kPageBytes, src, static_cast<uint32_t>(tokens) * kRecFp4,
+                    &bars[L::bRawFull + slot]);
+        if (n + 1 == items && lane == 0) {
+          // A unit that begins in this part and is cut by its end is merged on
+          // this part's behalf: {unit, last part with a piece of it}.
+          const bool merges = k + 1 < unit.tiles && !(g0 > start_u[1] && u == start_u[0]);
+          p.ws_info[part * 4] = merges ? u : -1;
+          p.ws_info[part * 4 + 1] = (g1 + (unit.tiles - k - 1) - 1) / share;
+        }
+        if (++k == unit.tiles && n + 1 < items) {
+          k = 0;
+          unit = unit_of<NR>(p, groups, ++u, bad_len);
+        }
+      }
+      // Every copy has landed before the CTA may end (they have, unless a wait gave up).
+      for (uint32_t i = items > L::kRaw ? items - L::kRaw : 0; i < items; ++i) {
+        const uint64_t t0 = global_timer_ns();
+        while (!mbar_try_wait(&bars[L::bRawFull + i % L::kRaw], (i / L::kRaw) & 1) &&
+               global_timer_ns() - t0 < kPagedWaitNs) {
+        }
+      }
+    } else if (warp >= kKWarp0 && warp < kVWarp0) {
+      // ---------------------------------------------------------------- K: lane = token
+      const int quad = warp & 3;
+      const int row = quad * 32 + lane;
+      const uint32_t tK = tmem + (static_cast<uint32_t>(quad * 32) << 16) + L::cK;
+      // Rows are 288 bytes apart: lanes 4..7 of every eight read their two
+      // 16-byte pieces in the other order, which spreads eight lanes over all banks.
+      const bool swap = (lane & 4) != 0;
+      uint32_t kq = 0;
+      for (uint32_t n = 0; n < items; ++n) {
+        const int slot = n % L::kRaw;
+        mbar_wait(&bars[L::bRawFull + slot], (n / L::kRaw) & 1, abort_flag, p.d_error, kPagedWaitNs);
+        const uint8_t* rec = sRaw + slot * kRawBytes + row * kRecFp4;
+        const bool there = token_there(info[n % kInfoRing].x, row);
+        uint4 sc[2];
+        sc[0] = *reinterpret_cast<const uint4*>(rec + 256);
+        sc[1] = *reinterpret_cast<const uint4*>(rec + 272);
+        if (!there) sc[0] = sc[1] = make_uint4(0, 0, 0, 0);  // scale 0: the token is all zeros
+        const uint32_t scw[8] = {sc[0].x, sc[0].y, sc[0].z, sc[0].w, sc[1].x, sc[1].y, sc[1].z, sc[1].w};
 #pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    if (r0 + r >= p.rows) break;
-    const int64_t row = static_cast<int64_t>(b) * p.rows + r0 + r;
-    const float inv = sl[r] > 0.f ? 1.f / sl[r] : 0.f;
-    *reinterpret_cast<__nv_bfloat162*>(p.out + row * 512 + 2 * tid) =
-        __floats2bfloat162_rn(acc[0][r] * inv, acc[1][r] * inv);
-    if (tid == 0) p.lse[row] = sl[r] > 0.f ? (sm[r] + log2f(sl[r])) * 0.6931471805599453f : -INFINITY;
+        for (int qq = 0; qq < 4; ++qq, ++kq) {
+          const int ks = kq % L::kKRing;
+          if (kq >= L::kKRing)
+            mbar_wait(&bars[L::bKFree + ks], (kq / L::kKRing - 1) & 1, abort_flag, p.d_error, kPagedWaitNs);
+          __syncwarp();
+          tc_fence_after();
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const uint8_t* src = rec + qq * 64 + hh * 32;
+            const uint4 a = *reinterpret_cast<const uint4*>(src + (swap ? 16 : 0));
+            const uint4 b = *reinterpret_cast<const uint4*>(src + (swap ? 0 : 16));
+            const uint4 d0 = swap ? b : a, d1 = swap ? a : b;
+            uint32_t o[16];
+            const uint32_t s = scw[qq * 2 + hh];
+            decode32(d0, s & 0xFFFFu, o);
+            tmem_st16(tK + ks * 64 + hh * 32, o);
+            decode32(d1, s >> 16, o);
+            tmem_st16(tK + ks * 64 + hh * 32 + 16, o);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[L::bKFull + ks]);
+        }
+        if (lane == 0) mbar_arrive(&bars[L::bRawFree + slot]);
+      }
+    } else if (warp >= kVWarp0 && warp < kLoadWarp) {
+      // ---------------------------------------------------------------- V: shared memory
+      // Eight lanes cover four tokens x two neighbouring 16-byte pieces, which
+      // is free of bank conflicts both ways; a warp covers 8 tokens x 4 pieces.
+      const int vw = warp - kVWarp0;
+      const int piece = (lane & 1) | ((lane >> 2) & 2);         // 32-dim piece of the quarter
+      const int tok = ((lane >> 1) & 3) | ((lane >> 2) & 4);    // token within eight
+      uint32_t vu = 0;
+      for (uint32_t n = 0; n < items; ++n) {
+        const int slot = n % L::kRaw;
+        mbar_wait(&bars[L::bRawFull + slot], (n / L::kRaw) & 1, abort_flag, p.d_error, kPagedWaitNs);
+        const int inf = info[n % kInfoRing].x;
+        const uint8_t* raw = sRaw + slot * kRawBytes;
+#pragma unroll 1
+        for (int v = 0; v < kVUnits; ++v, ++vu) {
+          const int half = v >> 2, qq = v & 3;
+          const int have = (inf >> (8 * half)) & 0xFF;
+          const int vs = vu % L::kVRing;
+          uint4 data[2];
+          uint32_t sc[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int t = vw * 16 + i * 8 + tok;
+            const uint8_t* rec = raw + (half * 64 + t) * kRecFp4;
+            data[i] = *reinterpret_cast<const uint4*>(rec + qq * 64 + piece * 16);
+            sc[i] = t < have ? *reinterpret_cast<const uint16_t*>(rec + 256 + qq * 8 + piece * 2) : 0u;
+          }
+          if (vu >= L::kVRing)
+            mbar_wait(&bars[L::bVFree + vs], (vu / L::kVRing - 1) & 1, abort_flag, p.d_error, kPagedWaitNs);
+          uint8_t* dst = sV + vs * kVUnitBytes + (piece >> 1) * 8192;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int t = vw * 16 + i * 8 + tok;
+            uint32_t o[16];
+            decode32(data[i], sc[i], o);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<uint4*>(dst + swz<128>(t * 128 + (piece & 1) * 64 + j * 16)) =
+                  make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[L::bVFull + vs]);
+        }
+        if (lane == 0) mbar_arrive(&bars[L::bRawFree + slot]);
+      }
+    } else if (warp == kMmaWarp) {
+      // ---------------------------------------------------------------- issuer
+      constexpr uint32_t idesc_qk = idesc_f16(128, NR, false, false);
+      constexpr uint32_t idesc_pv = idesc_f16(128, NR, true, true);
+      constexpr uint32_t p_sbo = 8 * 2 * NR;  // eight rows of P^T
+      constexpr uint32_t p_swz = NR == 64 ? kSwizzle128 : (NR == 32 ? kSwizzle64 : kSwizzle32);
+      const uint32_t q_base = smem_u32(sQ), v_base = smem_u32(sV), p_base = smem_u32(sP);
+      uint32_t kq = 0, vu = 0, q_pieces = 0, o_pieces = 0;
+      // S^T = K Q^T of item n; returns its flags.
+      const auto scores = [&](uint32_t n) {
+        int flags = 0;
+        if (n >= 2) mbar_wait(&bars[L::bSFree + (n & 1)], (n / 2 - 1) & 1, abort_flag, p.d_error, kPagedWaitNs);
+#pragma unroll 1
+        for (int qq = 0; qq < 4; ++qq, ++kq) {
+          const int ks = kq % L::kKRing;
+          mbar_wait(&bars[L::bKFull + ks], (kq / L::kKRing) & 1, abort_flag, p.d_error, kPagedWaitNs);
+          if (qq == 0) {
+            flags = info[n % kInfoRing].x;
+            if (flags & kOpens)
+              mbar_wait(&bars[L::bQFull], q_pieces++ & 1, abort_flag, p.d_error, kPagedWaitNs);
+          }
+          __syncwarp();
+          tc_fence_after();
+          const uint64_t b0 = make_smem_desc(q_base + 2 * qq * (NR * 128), 16, 1024, kSwizzle128);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            mma_f16_ts(tmem + L::cS + (n & 1) * NR, tmem + L::cK + ks * 64 + j * 8,
+                       b0 + (((j >> 2) * NR * 128 + (j & 3) * 32) >> 4), idesc_qk, (qq | j) != 0);
+          commit_one(&bars[L::bKFree + ks]);
+        }
+        commit_one(&bars[L::bSFull + (n & 1)]);
+        return flags;
+      };
+      // O^T += V^T P^T of item n.
+      const auto values = [&](uint32_t n, bool opens) {
+        mbar_wait(&bars[L::bPFull + (n & 1)], (n / 2) & 1, abort_flag, p.d_error, kPagedWaitNs);
+        if (opens && o_pieces++ > 0)
+          mbar_wait(&bars[L::bOFree], (o_pieces - 2) & 1, abort_flag, p.d_error, kPagedWaitNs);
+        const uint64_t pb = make_smem_desc(p_base + (n & 1) * L::kPBytes, 16 * p_sbo, p_sbo, p_swz);
+#pragma unroll 1
+        for (int v = 0; v < kVUnits; ++v, ++vu) {
+          const int vs = vu % L::kVRing;
+          mbar_wait(&bars[L::bVFull + vs], (vu / L::kVRing) & 1, abort_flag, p.d_error, kPagedWaitNs);
+          __syncwarp();
+          tc_fence_after();
+          const uint64_t a0 = make_smem_desc(v_base + vs * kVUnitBytes, 8192, 1024, kSwizzle128);
+          const int half = v >> 2, qq = v & 3;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mma_f16_ss(tmem + L::cO + qq * NR, a0 + ((j * 2048) >> 4), pb + (((half * 4 + j) * 2 * p_sbo) >> 4),
+                       idesc_pv, !(opens && half == 0 && j == 0));
+          commit_one(&bars[L::bVFree + vs]);
+        }
+        commit_one(&bars[L::bPFree + (n & 1)]);
+      };
+      int flags = scores(0);
+      for (uint32_t n = 0; n < items; ++n) {
+        // At a piece's end the next scores wait for another Q: finish it first.
+        const bool closes = (flags & kCloses) != 0, opens = (flags & kOpens) != 0;
+        if (!closes) flags = scores(n + 1);
+        values(n, opens);
+        if (closes && n + 1 < items) flags = scores(n + 1);
+      }
+      commit_one(&bars[L::bDrain]);
+      __syncwarp();
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(&bars[L::bDrain], 0)) {
+        if (global_timer_ns() - t0 > kPagedWaitNs) {
+          if (p.d_error) atomicOr(p.d_error, MLA_DEVERR_TIMEOUT);
+          break;
+        }
+      }
+    } else if (warp < kSoftmaxWarps) {
+      // ---------------------------------------------------------------- softmax
+      constexpr int kSoftmaxThreads = kSoftmaxWarps * 32;
+      const int quad = warp & 3, side = warp >> 2;
+      const int row = quad * 32 + lane;      // token of the tile
+      const int c0 = side * NC;              // first row of this thread
+      const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+      const uint32_t tS = tmem + lanes + L::cS + c0, tO = tmem + lanes + L::cO;
+
+      // Q rows of a unit: bf16 -> scaled f16, K-major with 128-byte swizzle,
+      // one row per warp at a time (lane = 16 dims); and the rows' masks.
+      const auto load_q = [&](int u) {
+        bool bad_len;
+        const Unit t = unit_of<NR>(p, groups, u, bad_len);
+        const uint16_t* q = p.q + (static_cast<int64_t>(t.b) * p.rows + t.row0) * kD;
+#pragma unroll 1
+        for (int r = warp; r < NR; r += kSoftmaxWarps) {
+          uint4 a = make_uint4(0, 0, 0, 0), b = a;
+          if (r < t.nrows) {
+            const uint4* src = reinterpret_cast<const uint4*>(q + static_cast<int64_t>(r) * kD + lane * 16);
+            a = __ldg(src);
+            b = __ldg(src + 1);
+          }
+          const uint32_t wv[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+          // The largest exponent of the row (the sign bits shifted out).
+          uint32_t top = 0;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) top = max(top, max((wv[k] << 17) >> 24, (wv[k] << 1) >> 24));
+          top = __reduce_max_sync(0xFFFFFFFFu, top);
+          // Largest value to [2^14, 2^15); nothing to scale in a row of zeros or of infinities.
+          const int e = top == 0 || top == 255 ? 0 : max(static_cast<int>(top) - 127 - 14, -100);
+          const float up = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+          uint32_t h[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            h[k] = pack_f16x2(__uint_as_float(wv[k] << 16) * up, __uint_as_float(wv[k] & 0xFFFF0000u) * up);
+          uint8_t* dst = sQ + (lane >> 2) * (NR * 128);
+          const uint32_t off = r * 128 + (lane & 3) * 32;
+          *reinterpret_cast<uint4*>(dst + swz<128>(off)) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(dst + swz<128>(off + 16)) = make_uint4(h[4], h[5], h[6], h[7]);
+          if (lane == 0) {
+            c_scale[r] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+            c_m[r] = kNoMax;
+            const int hi = t.first + min(t.row0 + r, p.rows - 1) / p.h;
+            c_hi[r] = hi;
+            c_lo[r] = window_start(p, hi);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[L::bQFull]);
+        named_bar_sync(1, kSoftmaxThreads);  // the row arrays are complete
+      };
+      // This thread's scores of an item, scaled and masked.
+      const auto scores = [&](uint32_t n, const int4& it, float (&x)[NC]) {
+        uint32_t r[NC];
+        tmem_ld<NC>(tS + (n & 1) * NR, r);
+        const float4* sc4 = reinterpret_cast<const float4*>(c_scale + c0);
+#pragma unroll
+        for (int k = 0; k < NC / 4; ++k) {
+          const float4 s = sc4[k];
+          x[4 * k] = __uint_as_float(r[4 * k]) * s.x;
+          x[4 * k + 1] = __uint_as_float(r[4 * k + 1]) * s.y;
+          x[4 * k + 2] = __uint_as_float(r[4 * k + 2]) * s.z;
+          x[4 * k + 3] = __uint_as_float(r[4 * k + 3]) * s.w;
+        }
+        if (!(it.x & kWhole)) {
+          const int pos = it.y * kTile + row;
+          const bool there = token_there(it.x, row), sink = pos < p.sinks;
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const bool see = there && pos <= c_hi[c0 + c] && (sink || pos >= c_lo[c0 + c]);
+            x[c] = see ? x[c] : -INFINITY;
+          }
+        }
+      };
+
+      load_q(start_u[0]);
+      float l[NC];
+#pragma unroll 1
+      for (uint32_t n = 0; n < items; ++n) {
+        mbar_wait(&bars[L::bInfo + n % kInfoRing], (n / kInfoRing) & 1, abort_flag, p.d_error, kPagedWaitNs);
+        int4 it = info[n % kInfoRing];
+        it.z = min(max(it.z, 0), units - 1);  // (after a wait that gave up it may be anything)
+        if (it.x & kOpens) {
+#pragma unroll
+          for (int c = 0; c < NC; ++c) l[c] = 0.f;
+        }
+        mbar_wait(&bars[L::bSFull + (n & 1)], (n / 2) & 1, abort_flag, p.d_error, kPagedWaitNs);
+        __syncwarp();
+        tc_fence_after();
+        const float4* m4 = reinterpret_cast<const float4*>(c_m + c0);
+        float excess = -INFINITY;
+        {
+          float x[NC];
+          scores(n, it, x);
+#pragma unroll
+          for (int k = 0; k < NC / 4; ++k) {
+            const float4 m = m4[k];
+            excess = fmaxf(excess, fmaxf(fmaxf(x[4 * k] - m.x, x[4 * k + 1] - m.y),
+                                         fmaxf(x[4 * k + 2] - m.z, x[4 * k + 3] - m.w)));
+          }
+        }
+        if (any_of(2, kSoftmaxThreads, excess > kSlack)) {
+          // Exact maxima of the tile's rows.
+          {
+            float x[NC];
+            scores(n, it, x);
+            LaneReduce<NC, 16>::run(x, lane, OpMax());
+            if (lane % (32 / NC) == 0) red[quad * NR + c0 + column_of<NC>(lane)] = x[0];
+          }
+          named_bar_sync(1, kSoftmaxThreads);
+          bool moved = false;
+          if (tid < NR) {
+            const float mt = fmaxf(fmaxf(red[tid], red[NR + tid]), fmaxf(red[2 * NR + tid], red[3 * NR + tid]));
+            const float old = c_m[tid];
+            float alpha = 1.f;
+            if (mt > old + kSlack) {
+              alpha = ex2_approx(old - mt);
+              moved = old != kNoMax;
+              c_m[tid] = mt;
+            }
+            c_alpha[tid] = alpha;
+          }
+          if (any_of(2, kSoftmaxThreads, moved)) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) l[c] *= c_alpha[c0 + c];
+            // O^T follows, once the product before this one is complete.
+            if (!(it.x & kOpens)) {
+              mbar_wait(&bars[L::bPFree + ((n - 1) & 1)], ((n - 1) / 2) & 1, abort_flag, p.d_error, kPagedWaitNs);
+              __syncwarp();
+              tc_fence_after();
+#pragma unroll 1
+              for (int i = side; i < 4 * (NR / 16); i += L::kSides) {
+                const int qq = i / (NR / 16), cc = (i % (NR / 16)) * 16;
+                uint32_t o[16];
+                tmem_ld16(tO + qq * NR + cc, o);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * c_alpha[cc + k]);
+                tmem_st16(tO + qq * NR + cc, o);
+              }
+              tmem_wait_st();
+            }
+          }
+        }
+        // P = 2^(x - m + 7), row `row` of P^T (MN-major), once the product
+        // two items back has read this buffer.
+        if (n >= 2) mbar_wait(&bars[L::bPFree + (n & 1)], (n / 2 - 1) & 1, abort_flag, p.d_error, kPagedWaitNs);
+        __syncwarp();
+        {
+          float x[NC];
+          scores(n, it, x);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[L::bSFree + (n & 1)]);
+          uint8_t* dst = sP + (n & 1) * L::kPBytes;
+#pragma unroll
+          for (int k = 0; k < NC / 8; ++k) {
+            float e[8];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float4 m = m4[2 * k + j];
+              e[4 * j] = ex2_approx(x[8 * k + 4 * j] - (m.x - kPBias));
+              e[4 * j + 1] = ex2_approx(x[8 * k + 4 * j + 1] - (m.y - kPBias));
+              e[4 * j + 2] = ex2_approx(x[8 * k + 4 * j + 2] - (m.z - kPBias));
+              e[4 * j + 3] = ex2_approx(x[8 * k + 4 * j + 3] - (m.w - kPBias));
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) l[8 * k + j] += e[j];
+            *reinterpret_cast<uint4*>(dst + swz<2 * NR>(row * (2 * NR) + c0 * 2 + k * 16)) =
+                make_uint4(pack_f16x2(e[0], e[1]), pack_f16x2(e[2], e[3]), pack_f16x2(e[4], e[5]),
+                           pack_f16x2(e[6], e[7]));
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[L::bPFull + (n & 1)]);
+        if (!(it.x & kCloses)) continue;
+
+        // The piece's end: row sums over the tile's tokens, then O^T / l.
+        LaneReduce<NC, 16>::run(l, lane, OpAdd());
+        if (lane % (32 / NC) == 0) red[quad * NR + c0 + column_of<NC>(lane)] = l[0];
+        named_bar_sync(1, kSoftmaxThreads);
+        const bool whole_unit = (it.x & (kFromStart | kToEnd)) == (kFromStart | kToEnd);
+        // Partials: slot 2 part + 1 for a piece that begins its unit, 2 part for one that goes on with it.
+        const int prow = (part * 2 + ((it.x & kFromStart) ? 1 : 0)) * NR;
+        const int ub = it.z / groups, urow0 = (it.z - ub * groups) * NR;
+        const int orow = ub * p.rows + urow0, nrows = min(NR, p.rows - urow0);
+        if (tid < NR) {
+          const float sum = (red[tid] + red[NR + tid]) + (red[2 * NR + tid] + red[3 * NR + tid]);
+          c_linv[tid] = sum > 0.f ? 1.f / sum : 0.f;
+          const float lse = sum > 0.f ? (c_m[tid] - kPBias + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+          if (!whole_unit)
+            p.ws_lse[prow + tid] = lse;
+          else if (tid < nrows)
+            p.lse[orow + tid] = lse;
+        }
+        named_bar_sync(1, kSoftmaxThreads);
+        // The next unit's Q goes in while the last product runs (this piece's scores are all done).
+        if (n + 1 < items) load_q(min(it.z + 1, units - 1));
+        mbar_wait(&bars[L::bPFree + (n & 1)], (n / 2) & 1, abort_flag, p.d_error, kPagedWaitNs);
+        __syncwarp();
+        tc_fence_after();
+        // Lane = dim, columns = rows.
+#pragma unroll 1
+        for (int i = side; i < 4 * (NR / 16); i += L::kSides) {
+          const int qq = i / (NR / 16), cc = (i % (NR / 16)) * 16;
+          const int d = qq * 128 + row;
+          uint32_t o[16];
+          tmem_ld16(tO + qq * NR + cc, o);
+          if (whole_unit) {
+            // Even lanes take row cc + k of dims (d, d + 1), odd lanes row cc + k + 1.
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+              const float a = __uint_as_float(o[k]) * c_linv[cc + k], b = __uint_as_float(o[k + 1]) * c_linv[cc + k + 1];
+              const float got = __shfl_xor_sync(0xFFFFFFFFu, (lane & 1) ? a : b, 1);
+              const __nv_bfloat162 v = (lane & 1) ? __floats2bfloat162_rn(got, b) : __floats2bfloat162_rn(a, got);
+              const int r = cc + k + (lane & 1);
+              if (r < nrows)
+                *reinterpret_cast<__nv_bfloat162*>(p.out + static_cast<int64_t>(orow + r) * kD + (d & ~1)) = v;
+            }
+          } else {
+            float* dst = p.ws_o + static_cast<int64_t>(prow + cc) * kD + d;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) dst[k * kD] = __uint_as_float(o[k]) * c_linv[cc + k];
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[L::bOFree]);
+        named_bar_sync(1, kSoftmaxThreads);  // the row sums' arrays may change again
+      }
+    }
   }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Merge of a unit cut by parts: pieces with normalised outputs o_i and
+// log-sum-exps L_i give L = ln sum exp L_i and sum exp(L_i - L) o_i.  One warp
+// per row, a block of four rows per part and row group.
+__global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p, const int groups, const int nr) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int part = blockIdx.x, lane = threadIdx.x & 31;
+  const int r = static_cast<int>(blockIdx.y) * 4 + (threadIdx.x >> 5);
+  const int u = p.ws_info[part * 4];
+  if (u < 0) return;
+  const int last = p.ws_info[part * 4 + 1];
+  const int b = u / groups, row0 = (u - b * groups) * nr;
+  if (r >= nr || row0 + r >= p.rows) return;
+  // Piece 0 is this part's slot 2 part + 1, piece i part + i's slot 2 (part + i).
+  const int pieces = last - part + 1;
+  const auto prow = [&](int i) { return (static_cast<int64_t>(part + i) * 2 + (i == 0 ? 1 : 0)) * nr + r; };
+  float m = -INFINITY;
+  for (int i = lane; i < pieces; i += 32) m = fmaxf(m, p.ws_lse[prow(i)]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  const float mu = m == -INFINITY ? 0.f : m;
+  float z = 0.f;
+  for (int i = lane; i < pieces; i += 32) z += expf(p.ws_lse[prow(i)] - mu);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
+  const float inv = z > 0.f ? 1.f / z : 0.f;
+  float4 acc[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < pieces; ++i) {
+    const int64_t pr = prow(i);
+    const float wgt = expf(p.ws_lse[pr] - mu) * inv;
+    const float4* src = reinterpret_cast<const float4*>(p.ws_o + pr * kD);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 v = src[k * 32 + lane];
+      acc[k].x = fmaf(wgt, v.x, acc[k].x);
+      acc[k].y = fmaf(wgt, v.y, acc[k].y);
+      acc[k].z = fmaf(wgt, v.z, acc[k].z);
+      acc[k].w = fmaf(wgt, v.w, acc[k].w);
+    }
+  }
+  const int64_t row = static_cast<int64_t>(b) * p.rows + row0 + r;
+  uint2* dst = reinterpret_cast<uint2*>(p.out + row * kD);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(acc[k].x, acc[k].y), c = __floats2bfloat162_rn(acc[k].z, acc[k].w);
+    dst[k * 32 + lane] =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&c));
+  }
+  if (lane == 0) p.lse[row] = z > 0.f ? m + logf(z) : -INFINITY;
+}
+
+template <int NR>
+cudaError_t launch(const PagedParams& p, const PagedPlan& plan, cudaStream_t stream) {
+  static std::atomic<uint64_t> configured{0};
+  cudaError_t e = max_dynamic_smem_once(configured, reinterpret_cast<const void*>(paged_decode_kernel<NR>),
+                                        PSmem<NR>::kAlloc);
+  if (e != cudaSuccess) return e;
+  paged_decode_kernel<NR><<<plan.num_parts, PSmem<NR>::kThreads, PSmem<NR>::kAlloc, stream>>>(p, plan.groups);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // The merge may be scheduled while the decode drains; its blocks wait for it.
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(plan.num_parts), NR / 4);
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_merge_kernel, p, plan.groups, NR);
 }
 
 }  // namespace
@@ -138,12 +1002,11 @@ PagedPlan paged_plan(const mla_paged_problem_t* p, int num_parts) {
 }
 
 cudaError_t launch_paged_decode(const PagedParams& p, const PagedPlan& plan, cudaStream_t stream) {
-  static std::atomic<uint64_t> configured{0};
-  const cudaError_t e = max_dynamic_smem_once(configured, reinterpret_cast<const void*>(paged_simple_kernel), kSmem);
-  if (e != cudaSuccess) return e;
-  const int groups = (p.rows + kRows - 1) / kRows;
-  paged_simple_kernel<<<static_cast<unsigned>(p.batch) * groups, 256, kSmem, stream>>>(p, groups);
-  return cudaGetLastError();
+  switch (plan.nr) {
+    case 16: return launch<16>(p, plan, stream);
+    case 32: return launch<32>(p, plan, stream);
+    default: return launch<64>(p, plan, stream);
+  }
 }
 
 }  // namespace mla
