@@ -55,36 +55,45 @@ namespace mla {
 
 namespace {
 
-constexpr int kRawBytes = kTile * kRecFp4;   // one tile of records
 constexpr int kPageBytes = kPage * kRecFp4;
-constexpr int kVUnitBytes = 64 * 128 * 2;    // 64 tokens x 128 dims
-constexpr int kVUnits = 8;                   // per tile: two token halves x four dim quarters
+constexpr int kVUnitTokens = 64;
+constexpr int kVUnitBytes = kVUnitTokens * 128 * 2;  // 64 tokens x 128 dims of V, two chunks of 64 dims
 constexpr int kInfoRing = 8;
 constexpr uint64_t kPagedWaitNs = 2000000000ull;  // 2 s per wait
+#ifndef KUNROLL
+#define KUNROLL 1
+#define VPIECES 4
+#define QUNROLL 1
+#define PUNROLL 1
+#endif
+constexpr int kUk = KUNROLL, kUq = QUNROLL, kUp = PUNROLL;
 constexpr float kSlack = 8.f;                // the running maximum may lag by 2^8
 constexpr float kPBias = 7.f;                // P of the maximum is 2^7
 constexpr float kNoMax = -3.0e38f;           // running maximum before any visible token
 
 template <int NR>
 struct PSmem {
-  // Softmax threads hold 16 rows each (8 with 16 rows): scores and sums stay in registers.
-  static constexpr int kSides = NR == 64 ? 4 : 2;
+  static constexpr int kSides = 2;  // softmax threads hold half of the rows each: exponents and sums stay in registers
   static constexpr int kSoftmaxWarps = 4 * kSides;
-  static constexpr int kKWarp0 = kSoftmaxWarps, kVWarp0 = kKWarp0 + 4, kLoadWarp = kVWarp0 + 4, kMmaWarp = kLoadWarp + 1;
-  static constexpr int kThreads = (kMmaWarp + 1) * 32;
-  static constexpr int kRaw = NR == 16 ? 3 : 2;                    // raw tiles
-  static constexpr int kKRing = NR == 64 ? 2 : 4;                  // K quarters in tensor memory
-  static constexpr int kVRing = NR == 64 ? 3 : (NR == 32 ? 6 : 5);  // V units
+  static constexpr int kKWarp0 = kSoftmaxWarps, kVWarp0 = kKWarp0 + 4, kLoadWarp = kVWarp0 + 4;
+  static constexpr int kScoreWarp = kLoadWarp + 1, kValueWarp = kScoreWarp + 1;
+  static constexpr int kThreads = (kValueWarp + 1) * 32;
+  // Rings: raw pages, K quarters in tensor memory, V units.  A page lives
+  // from its load to the end of its V decode, about ten thousand cycles, so
+  // the more of them fit the better.
+  static constexpr int kRaw = NR == 64 ? 4 : (NR == 32 ? 6 : 7);
+  static constexpr int kKRing = NR == 64 ? 2 : 4;
+  static constexpr int kVRing = 4;  // one for each V warp
   static constexpr int kQBytes = NR * kD * 2;
   static constexpr int kPBytes = kTile * NR * 2;
   static constexpr int kQOff = 0;
   static constexpr int kVOff = kQOff + kQBytes;
   static constexpr int kPOff = kVOff + kVRing * kVUnitBytes;
-  static constexpr int kRawOff = kPOff + 2 * kPBytes;
-  static constexpr int kBarOff = kRawOff + kRaw * kRawBytes;
-  static constexpr int kNumBars = 2 * kRaw + 2 * kKRing + 2 * kVRing + 8 + 3 + kInfoRing;
+  static constexpr int kRawOff = kPOff + kPBytes;
+  static constexpr int kBarOff = kRawOff + kRaw * kPageBytes;
+  static constexpr int kNumBars = 2 * kRaw + 2 * kKRing + 2 * kVRing + 6 + 3 + kInfoRing;
   static constexpr int kColOff = (kBarOff + kNumBars * 8 + 15) & ~15;  // per-row arrays
-  // float m[NR], alpha[NR], scale[NR], linv[NR]; int hi[NR], lo[NR]; float red[4][NR]
+  // float mb[NR], alpha[NR], scale[NR], linv[NR]; int hi[NR], lo[NR]; float red[4][NR]
   static constexpr int kInfoOff = kColOff + 10 * NR * 4;
   static constexpr int kMiscOff = kInfoOff + kInfoRing * 16;
   static constexpr int kEnd = kMiscOff + 256;
@@ -93,7 +102,7 @@ struct PSmem {
   // Barrier indices.
   static constexpr int bRawFull = 0, bRawFree = bRawFull + kRaw, bKFull = bRawFree + kRaw, bKFree = bKFull + kKRing,
                        bVFull = bKFree + kKRing, bVFree = bVFull + kVRing, bSFull = bVFree + kVRing,
-                       bSFree = bSFull + 2, bPFull = bSFree + 2, bPFree = bPFull + 2, bQFull = bPFree + 2,
+                       bSFree = bSFull + 2, bPFull = bSFree + 2, bPFree = bPFull + 1, bQFull = bPFree + 1,
                        bOFree = bQFull + 1, bDrain = bOFree + 1, bInfo = bDrain + 1;
   static_assert(bInfo + kInfoRing == kNumBars, "barriers");
   // Tensor memory columns: O^T quarters, S^T buffers, K quarters.
@@ -192,23 +201,65 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
   }
 }
 
-// One elected lane of a converged warp issues; A in tensor memory or shared memory.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t acc) {
+// Bounded wait of a whole warp on an mbarrier phase; the clock is read only
+// now and then, as nearly all waits are short.  After kPagedWaitNs, or once
+// another warp of the CTA has given up, it goes on with the abort flag set, so
+// that every warp still reaches the kernel's end.
+__device__ __forceinline__ void wait_for(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* d_error) {
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+    if ((i & 63) == 0) {
+      const uint64_t t = global_timer_ns();
+      if (t0 == 0) t0 = t;
+      const bool late = t - t0 > kPagedWaitNs;
+      if (late || *abort_flag) {
+        *abort_flag = 1;
+        if (late && d_error) atomicOr(d_error, MLA_DEVERR_TIMEOUT);
+        break;
+      }
+    }
+  }
+  __syncwarp();
+}
+
+// The wait for the tensor core's end before tensor memory goes away: it does
+// not heed the abort flag, but has its own bound.
+__device__ __forceinline__ void wait_drain(uint64_t* bar, int32_t* d_error) {
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, 0)) {
+    if (global_timer_ns() - t0 > kPagedWaitNs) {
+      if (d_error) atomicOr(d_error, MLA_DEVERR_TIMEOUT);
+      break;
+    }
+  }
+  __syncwarp();
+}
+
+// One elected lane of a converged warp issues; A in tensor memory or in
+// shared memory.  Descriptors come as their two halves: only the low one (the
+// start address) differs between the products of a matrix.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                           uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(acc)
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc)
       : "memory");
 }
-__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                           uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %2};\n\t"
+      "mov.b64 b, {%3, %4};\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(acc)
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc)
       : "memory");
 }
 __device__ __forceinline__ void commit_one(uint64_t* bar) {
@@ -327,9 +378,11 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 template <int NR>
 __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(const PagedParams p, const int groups) {
   using L = PSmem<NR>;
-  constexpr int NC = NR / L::kSides;  // rows of a softmax thread
+  constexpr int NC = NR / L::kSides;    // rows of a softmax thread
+  constexpr int HC = NR == 32 ? 16 : 8;  // of which it works on so many at a time
   constexpr int kPagedThreads = L::kThreads, kSoftmaxWarps = L::kSoftmaxWarps;
-  constexpr int kKWarp0 = L::kKWarp0, kVWarp0 = L::kVWarp0, kLoadWarp = L::kLoadWarp, kMmaWarp = L::kMmaWarp;
+  constexpr int kKWarp0 = L::kKWarp0, kVWarp0 = L::kVWarp0, kLoadWarp = L::kLoadWarp;
+  constexpr int kScoreWarp = L::kScoreWarp, kValueWarp = L::kValueWarp;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem + L::kQOff;
@@ -337,8 +390,8 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
   uint8_t* sP = smem + L::kPOff;
   uint8_t* sRaw = smem + L::kRawOff;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
-  float* c_m = reinterpret_cast<float*>(smem + L::kColOff);
-  float* c_alpha = c_m + NR;
+  float* c_mb = reinterpret_cast<float*>(smem + L::kColOff);  // m - 7
+  float* c_alpha = c_mb + NR;
   float* c_scale = c_alpha + NR;
   float* c_linv = c_scale + NR;
   int* c_hi = reinterpret_cast<int*>(c_linv + NR);
@@ -358,32 +411,32 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
   if (tid == 0) {
     for (int i = 0; i < L::kRaw; ++i) {
       mbar_init(&bars[L::bRawFull + i], 1);
-      mbar_init(&bars[L::bRawFree + i], 8);
+      mbar_init(&bars[L::bRawFree + i], 6);  // two K warps and the four V warps
     }
     for (int i = 0; i < L::kKRing; ++i) {
       mbar_init(&bars[L::bKFull + i], 4);
       mbar_init(&bars[L::bKFree + i], 1);
     }
     for (int i = 0; i < L::kVRing; ++i) {
-      mbar_init(&bars[L::bVFull + i], 4);
+      mbar_init(&bars[L::bVFull + i], 1);
       mbar_init(&bars[L::bVFree + i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars[L::bSFull + i], 1);
       mbar_init(&bars[L::bSFree + i], kSoftmaxWarps);
-      mbar_init(&bars[L::bPFull + i], kSoftmaxWarps);
-      mbar_init(&bars[L::bPFree + i], 1);
     }
+    mbar_init(&bars[L::bPFull], kSoftmaxWarps);
+    mbar_init(&bars[L::bPFree], 1);
     mbar_init(&bars[L::bQFull], kSoftmaxWarps);
     mbar_init(&bars[L::bOFree], kSoftmaxWarps);
-    mbar_init(&bars[L::bDrain], 1);
+    mbar_init(&bars[L::bDrain], 2);
     for (int i = 0; i < kInfoRing; ++i) mbar_init(&bars[L::bInfo + i], 1);
     *abort_flag = 0;
     start_u[0] = -1;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
   }
-  if (warp == kMmaWarp) tmem_alloc(tmem_slot, 512);
+  if (warp == kValueWarp) tmem_alloc(tmem_slot, 512);
 
   // The cut: items of all units, this part's run, and the unit it begins in.
   const int units = p.batch * groups;
@@ -441,10 +494,9 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
       int u = start_u[0], k = g0 - start_u[1];
       bool bad_len;
       Unit unit = unit_of<NR>(p, groups, u, bad_len);
+      int slot = 0;
+      uint32_t parity = 1;
       for (uint32_t n = 0; n < items; ++n) {
-        const int slot = n % L::kRaw;
-        if (n >= L::kRaw)
-          mbar_wait(&bars[L::bRawFree + slot], (n / L::kRaw - 1) & 1, abort_flag, p.d_error, kPagedWaitNs);
         const int tile = tile_of(unit, k);
         const int end = unit.p_hi + 1;
         // Lane j < 2 looks after page j of the tile: copied up to the last
@@ -467,25 +519,30 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
         }
         if (bad && p.d_error) atomicOr(p.d_error, MLA_DEVERR_BAD_INDEX);
         const int t0 = __shfl_sync(0xFFFFFFFFu, tokens, 0), t1 = __shfl_sync(0xFFFFFFFFu, tokens, 1);
-        if (lane == 0) {
-          int word = t0 | (t1 << 8);
-          const int t_end = tile * kTile + kTile - 1;
-          if (t0 + t1 == kTile && t_end <= unit.p_lo &&
-              (p.window == 0 || tile * kTile > unit.p_hi - p.window || t_end < p.sinks))
-            word |= kWhole;
-          if (n == 0 || k == 0) word |= kOpens;
-          if (n + 1 == items || k + 1 == unit.tiles) word |= kCloses;
-          // A piece begins with its unit unless the run's first item lies inside the unit.
-          if (!(g0 > start_u[1] && u == start_u[0])) word |= kFromStart;
-          if (k + 1 == unit.tiles) word |= kToEnd;
-          info[n % kInfoRing] = make_int4(word, tile, u, 0);
-          mbar_arrive(&bars[L::bInfo + n % kInfoRing]);
-          expect_tx(&bars[L::bRawFull + slot], static_cast<uint32_t>(t0 + t1) * kRecFp4);
+        int word = t0 | (t1 << 8);
+        const int t_end = tile * kTile + kTile - 1;
+        if (t0 + t1 == kTile && t_end <= unit.p_lo &&
+            (p.window == 0 || tile * kTile > unit.p_hi - p.window || t_end < p.sinks))
+          word |= kWhole;
+        if (n == 0 || k == 0) word |= kOpens;
+        if (n + 1 == items || k + 1 == unit.tiles) word |= kCloses;
+        // A piece begins with its unit unless the run's first item lies inside the unit.
+        if (!(g0 > start_u[1] && u == start_u[0])) word |= kFromStart;
+        if (k + 1 == unit.tiles) word |= kToEnd;
+#pragma unroll 1
+        for (int j = 0; j < 2; ++j) {
+          wait_for(&bars[L::bRawFree + slot], parity, abort_flag, p.d_error);
+          if (j == 0 && lane == 0) {
+            info[n % kInfoRing] = make_int4(word, tile, u, 0);
+            mbar_arrive(&bars[L::bInfo + n % kInfoRing]);
+          }
+          if (lane == j) {
+            expect_tx(&bars[L::bRawFull + slot], static_cast<uint32_t>(tokens) * kRecFp4);
+            if (tokens > 0)
+              bulk_load(sRaw + slot * kPageBytes, src, static_cast<uint32_t>(tokens) * kRecFp4, &bars[L::bRawFull + slot]);
+          }
+          if (++slot == L::kRaw) slot = 0, parity ^= 1;
         }
-        __syncwarp();
-        if (tokens > 0)
-          bulk_load(sRaw + slot * kRawBytes + lane * kPageBytes, src, static_cast<uint32_t>(tokens) * kRecFp4,
-                    &bars[L::bRawFull + slot]);
         if (n + 1 == items && lane == 0) {
           // A unit that begins in this part and is cut by its end is merged on
           // this part's behalf: {unit, last part with a piece of it}.
@@ -496,10 +553,16 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
         if (++k == unit.tiles && n + 1 < items) {
           k = 0;
           unit = unit_of<NR>(p, groups, ++u, bad_len);
+          // Its Q on the way to L2, a few tiles before it is read.
+          const uint8_t* next = reinterpret_cast<const uint8_t*>(
+              p.q + (static_cast<int64_t>(unit.b) * p.rows + unit.row0) * kD);
+          for (int line = lane; line < unit.nrows * 8; line += 32)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(next + line * 128));
         }
       }
       // Every copy has landed before the CTA may end (they have, unless a wait gave up).
-      for (uint32_t i = items > L::kRaw ? items - L::kRaw : 0; i < items; ++i) {
+      const uint32_t pages = 2 * items;
+      for (uint32_t i = pages > L::kRaw ? pages - L::kRaw : 0; i < pages; ++i) {
         const uint64_t t0 = global_timer_ns();
         while (!mbar_try_wait(&bars[L::bRawFull + i % L::kRaw], (i / L::kRaw) & 1) &&
                global_timer_ns() - t0 < kPagedWaitNs) {
@@ -513,36 +576,36 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
       // Rows are 288 bytes apart: lanes 4..7 of every eight read their two
       // 16-byte pieces in the other order, which spreads eight lanes over all banks.
       const bool swap = (lane & 4) != 0;
-      uint32_t kq = 0;
+      const uint8_t* rows = sRaw + (row & 63) * kRecFp4;
+      const int near = swap ? 16 : 0, far = 16 - near;
+      int slot = quad >> 1;  // the warp's page of the tile
+      uint32_t raw_parity = 0;
+#pragma unroll 1
       for (uint32_t n = 0; n < items; ++n) {
-        const int slot = n % L::kRaw;
-        mbar_wait(&bars[L::bRawFull + slot], (n / L::kRaw) & 1, abort_flag, p.d_error, kPagedWaitNs);
-        const uint8_t* rec = sRaw + slot * kRawBytes + row * kRecFp4;
+        wait_for(&bars[L::bRawFull + slot], raw_parity, abort_flag, p.d_error);
+        const uint8_t* rec = rows + slot * kPageBytes;
         const bool there = token_there(info[n % kInfoRing].x, row);
-        uint4 sc[2];
-        sc[0] = *reinterpret_cast<const uint4*>(rec + 256);
-        sc[1] = *reinterpret_cast<const uint4*>(rec + 272);
-        if (!there) sc[0] = sc[1] = make_uint4(0, 0, 0, 0);  // scale 0: the token is all zeros
-        const uint32_t scw[8] = {sc[0].x, sc[0].y, sc[0].z, sc[0].w, sc[1].x, sc[1].y, sc[1].z, sc[1].w};
-#pragma unroll
-        for (int qq = 0; qq < 4; ++qq, ++kq) {
-          const int ks = kq % L::kKRing;
-          if (kq >= L::kKRing)
-            mbar_wait(&bars[L::bKFree + ks], (kq / L::kKRing - 1) & 1, abort_flag, p.d_error, kPagedWaitNs);
-          __syncwarp();
+#pragma unroll 1
+        for (int qq = 0; qq < 4; ++qq) {
+          const int ks = qq % L::kKRing;
+          const uint32_t parity = (L::kKRing == 4 ? n : static_cast<uint32_t>(qq / L::kKRing)) & 1;
+          const uint8_t* src = rec + qq * 64;
+          uint2 sc = *reinterpret_cast<const uint2*>(rec + 256 + qq * 8);
+          if (!there) sc = make_uint2(0, 0);  // scale 0: the token is all zeros
+          // A fresh barrier counts as one whose phase 1 is over.
+          wait_for(&bars[L::bKFree + ks], parity ^ 1, abort_flag, p.d_error);
           tc_fence_after();
-#pragma unroll
+          const uint32_t t = tK + ks * 64;
+#pragma unroll kUk
           for (int hh = 0; hh < 2; ++hh) {
-            const uint8_t* src = rec + qq * 64 + hh * 32;
-            const uint4 a = *reinterpret_cast<const uint4*>(src + (swap ? 16 : 0));
-            const uint4 b = *reinterpret_cast<const uint4*>(src + (swap ? 0 : 16));
-            const uint4 d0 = swap ? b : a, d1 = swap ? a : b;
+            const uint4 a = *reinterpret_cast<const uint4*>(src + hh * 32 + near);
+            const uint4 b = *reinterpret_cast<const uint4*>(src + hh * 32 + far);
             uint32_t o[16];
-            const uint32_t s = scw[qq * 2 + hh];
-            decode32(d0, s & 0xFFFFu, o);
-            tmem_st16(tK + ks * 64 + hh * 32, o);
-            decode32(d1, s >> 16, o);
-            tmem_st16(tK + ks * 64 + hh * 32 + 16, o);
+            const uint32_t s = hh ? sc.y : sc.x;
+            decode32(swap ? b : a, s & 0xFFFFu, o);
+            tmem_st16(t + hh * 32, o);
+            decode32(swap ? a : b, s >> 16, o);
+            tmem_st16(t + hh * 32 + 16, o);
           }
           tmem_wait_st();
           tc_fence_before();
@@ -550,125 +613,125 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
           if (lane == 0) mbar_arrive(&bars[L::bKFull + ks]);
         }
         if (lane == 0) mbar_arrive(&bars[L::bRawFree + slot]);
+        if ((slot += 2) >= L::kRaw) slot -= L::kRaw, raw_parity ^= 1;
       }
     } else if (warp >= kVWarp0 && warp < kLoadWarp) {
       // ---------------------------------------------------------------- V: shared memory
-      // Eight lanes cover four tokens x two neighbouring 16-byte pieces, which
-      // is free of bank conflicts both ways; a warp covers 8 tokens x 4 pieces.
-      const int vw = warp - kVWarp0;
+      // A warp owns one dim quarter.  Eight lanes cover four tokens x two
+      // neighbouring 16-byte pieces, which is free of bank conflicts both ways;
+      // the warp covers 8 tokens x 4 pieces at a time.
+      const int qq = warp - kVWarp0;
       const int piece = (lane & 1) | ((lane >> 2) & 2);         // 32-dim piece of the quarter
       const int tok = ((lane >> 1) & 3) | ((lane >> 2) & 4);    // token within eight
-      uint32_t vu = 0;
-      for (uint32_t n = 0; n < items; ++n) {
-        const int slot = n % L::kRaw;
-        mbar_wait(&bars[L::bRawFull + slot], (n / L::kRaw) & 1, abort_flag, p.d_error, kPagedWaitNs);
-        const int inf = info[n % kInfoRing].x;
-        const uint8_t* raw = sRaw + slot * kRawBytes;
+      const uint8_t* rows = sRaw + tok * kRecFp4 + qq * 64;
+      uint8_t* rows_v = sV + (piece >> 1) * (kVUnitTokens * 128) + tok * 128;
+      int off[4];  // the lane's four 16-byte units of a 128-byte row, swizzled
+#pragma unroll
+      for (int j = 0; j < 4; ++j) off[j] = (((piece & 1) * 4 + j) ^ tok) * 16;
+      uint8_t* dst = rows_v + qq * kVUnitBytes;
+      int slot = 0;
+      uint32_t raw_parity = 0;
 #pragma unroll 1
-        for (int v = 0; v < kVUnits; ++v, ++vu) {
-          const int half = v >> 2, qq = v & 3;
-          const int have = (inf >> (8 * half)) & 0xFF;
-          const int vs = vu % L::kVRing;
-          uint4 data[2];
-          uint32_t sc[2];
+      for (uint32_t n = 0; n < items; ++n) {
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          wait_for(&bars[L::bRawFull + slot], raw_parity, abort_flag, p.d_error);
+          const int have = ((info[n % kInfoRing].x >> (8 * half)) & 0xFF) - tok;  // rows of this lane below it are there
+          const uint8_t* rec = rows + slot * kPageBytes;
+          const uint8_t* scl = rec + 256 - qq * 56 + piece * 2;
+#pragma unroll 1
+          for (int i0 = 0; i0 < 8; i0 += VPIECES) {
+            uint4 data[VPIECES];
+            uint32_t sc[VPIECES];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int t = vw * 16 + i * 8 + tok;
-            const uint8_t* rec = raw + (half * 64 + t) * kRecFp4;
-            data[i] = *reinterpret_cast<const uint4*>(rec + qq * 64 + piece * 16);
-            sc[i] = t < have ? *reinterpret_cast<const uint16_t*>(rec + 256 + qq * 8 + piece * 2) : 0u;
-          }
-          if (vu >= L::kVRing)
-            mbar_wait(&bars[L::bVFree + vs], (vu / L::kVRing - 1) & 1, abort_flag, p.d_error, kPagedWaitNs);
-          uint8_t* dst = sV + vs * kVUnitBytes + (piece >> 1) * 8192;
+            for (int i = 0; i < VPIECES; ++i) {
+              data[i] = *reinterpret_cast<const uint4*>(rec + (i0 + i) * 8 * kRecFp4 + piece * 16);
+              sc[i] = *reinterpret_cast<const uint16_t*>(scl + (i0 + i) * 8 * kRecFp4);
+            }
+            if (i0 == 0) wait_for(&bars[L::bVFree + qq], half ^ 1, abort_flag, p.d_error);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int t = vw * 16 + i * 8 + tok;
-            uint32_t o[16];
-            decode32(data[i], sc[i], o);
+            for (int i = 0; i < VPIECES; ++i) {
+              uint32_t o[16];
+              decode32(data[i], (i0 + i) * 8 < have ? sc[i] : 0u, o);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              *reinterpret_cast<uint4*>(dst + swz<128>(t * 128 + (piece & 1) * 64 + j * 16)) =
-                  make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+              for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<uint4*>(dst + (i0 + i) * 1024 + off[j]) =
+                    make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            }
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[L::bVFull + vs]);
-        }
-        if (lane == 0) mbar_arrive(&bars[L::bRawFree + slot]);
-      }
-    } else if (warp == kMmaWarp) {
-      // ---------------------------------------------------------------- issuer
-      constexpr uint32_t idesc_qk = idesc_f16(128, NR, false, false);
-      constexpr uint32_t idesc_pv = idesc_f16(128, NR, true, true);
-      constexpr uint32_t p_sbo = 8 * 2 * NR;  // eight rows of P^T
-      constexpr uint32_t p_swz = NR == 64 ? kSwizzle128 : (NR == 32 ? kSwizzle64 : kSwizzle32);
-      const uint32_t q_base = smem_u32(sQ), v_base = smem_u32(sV), p_base = smem_u32(sP);
-      uint32_t kq = 0, vu = 0, q_pieces = 0, o_pieces = 0;
-      // S^T = K Q^T of item n; returns its flags.
-      const auto scores = [&](uint32_t n) {
-        int flags = 0;
-        if (n >= 2) mbar_wait(&bars[L::bSFree + (n & 1)], (n / 2 - 1) & 1, abort_flag, p.d_error, kPagedWaitNs);
-#pragma unroll 1
-        for (int qq = 0; qq < 4; ++qq, ++kq) {
-          const int ks = kq % L::kKRing;
-          mbar_wait(&bars[L::bKFull + ks], (kq / L::kKRing) & 1, abort_flag, p.d_error, kPagedWaitNs);
-          if (qq == 0) {
-            flags = info[n % kInfoRing].x;
-            if (flags & kOpens)
-              mbar_wait(&bars[L::bQFull], q_pieces++ & 1, abort_flag, p.d_error, kPagedWaitNs);
+          if (lane == 0) {
+            mbar_arrive(&bars[L::bVFull + qq]);
+            mbar_arrive(&bars[L::bRawFree + slot]);
           }
-          __syncwarp();
+          if (++slot == L::kRaw) slot = 0, raw_parity ^= 1;
+        }
+      }
+    } else if (warp == kScoreWarp) {
+      // ---------------------------------------------------------------- S^T = K Q^T
+      constexpr uint32_t idesc = idesc_f16(128, NR, false, false);
+      const uint64_t q_desc = make_smem_desc(smem_u32(sQ), 16, 1024, kSwizzle128);
+      const uint32_t q_lo = static_cast<uint32_t>(q_desc);
+      const uint32_t q_hi = static_cast<uint32_t>(q_desc >> 32);
+      uint32_t q_parity = 0;
+#pragma unroll 1
+      for (uint32_t n = 0; n < items; ++n) {
+        const uint32_t d = tmem + L::cS + (n & 1) * NR;
+        wait_for(&bars[L::bSFree + (n & 1)], ((n >> 1) & 1) ^ 1, abort_flag, p.d_error);
+#pragma unroll kUq
+        for (int qq = 0; qq < 4; ++qq) {
+          const int ks = qq % L::kKRing;
+          wait_for(&bars[L::bKFull + ks], (L::kKRing == 4 ? n : static_cast<uint32_t>(qq / L::kKRing)) & 1, abort_flag,
+                   p.d_error);
+          if (qq == 0 && (info[n % kInfoRing].x & kOpens)) {
+            wait_for(&bars[L::bQFull], q_parity, abort_flag, p.d_error);
+            q_parity ^= 1;
+          }
           tc_fence_after();
-          const uint64_t b0 = make_smem_desc(q_base + 2 * qq * (NR * 128), 16, 1024, kSwizzle128);
+          const uint32_t a = tmem + L::cK + ks * 64, b = q_lo + ((2 * qq * NR * 128) >> 4);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            mma_f16_ts(tmem + L::cS + (n & 1) * NR, tmem + L::cK + ks * 64 + j * 8,
-                       b0 + (((j >> 2) * NR * 128 + (j & 3) * 32) >> 4), idesc_qk, (qq | j) != 0);
+            mma_f16_ts(d, a + j * 8, b + (((j >> 2) * NR * 128 + (j & 3) * 32) >> 4), q_hi, idesc, (qq | j) != 0);
           commit_one(&bars[L::bKFree + ks]);
         }
         commit_one(&bars[L::bSFull + (n & 1)]);
-        return flags;
-      };
-      // O^T += V^T P^T of item n.
-      const auto values = [&](uint32_t n, bool opens) {
-        mbar_wait(&bars[L::bPFull + (n & 1)], (n / 2) & 1, abort_flag, p.d_error, kPagedWaitNs);
-        if (opens && o_pieces++ > 0)
-          mbar_wait(&bars[L::bOFree], (o_pieces - 2) & 1, abort_flag, p.d_error, kPagedWaitNs);
-        const uint64_t pb = make_smem_desc(p_base + (n & 1) * L::kPBytes, 16 * p_sbo, p_sbo, p_swz);
-#pragma unroll 1
-        for (int v = 0; v < kVUnits; ++v, ++vu) {
-          const int vs = vu % L::kVRing;
-          mbar_wait(&bars[L::bVFull + vs], (vu / L::kVRing) & 1, abort_flag, p.d_error, kPagedWaitNs);
-          __syncwarp();
-          tc_fence_after();
-          const uint64_t a0 = make_smem_desc(v_base + vs * kVUnitBytes, 8192, 1024, kSwizzle128);
-          const int half = v >> 2, qq = v & 3;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mma_f16_ss(tmem + L::cO + qq * NR, a0 + ((j * 2048) >> 4), pb + (((half * 4 + j) * 2 * p_sbo) >> 4),
-                       idesc_pv, !(opens && half == 0 && j == 0));
-          commit_one(&bars[L::bVFree + vs]);
-        }
-        commit_one(&bars[L::bPFree + (n & 1)]);
-      };
-      int flags = scores(0);
-      for (uint32_t n = 0; n < items; ++n) {
-        // At a piece's end the next scores wait for another Q: finish it first.
-        const bool closes = (flags & kCloses) != 0, opens = (flags & kOpens) != 0;
-        if (!closes) flags = scores(n + 1);
-        values(n, opens);
-        if (closes && n + 1 < items) flags = scores(n + 1);
       }
       commit_one(&bars[L::bDrain]);
-      __syncwarp();
-      const uint64_t t0 = global_timer_ns();
-      while (!mbar_try_wait(&bars[L::bDrain], 0)) {
-        if (global_timer_ns() - t0 > kPagedWaitNs) {
-          if (p.d_error) atomicOr(p.d_error, MLA_DEVERR_TIMEOUT);
-          break;
+      wait_drain(&bars[L::bDrain], p.d_error);
+    } else if (warp == kValueWarp) {
+      // ---------------------------------------------------------------- O^T += V^T P^T
+      constexpr uint32_t idesc = idesc_f16(128, NR, true, true);
+      constexpr uint32_t p_sbo = 8 * 2 * NR;  // eight rows of P^T
+      constexpr uint32_t p_swz = NR == 64 ? kSwizzle128 : (NR == 32 ? kSwizzle64 : kSwizzle32);
+      const uint64_t v_desc = make_smem_desc(smem_u32(sV), kVUnitTokens * 128, 1024, kSwizzle128);
+      const uint64_t p_desc = make_smem_desc(smem_u32(sP), 16 * p_sbo, p_sbo, p_swz);
+      const uint32_t v_lo = static_cast<uint32_t>(v_desc), p_lo = static_cast<uint32_t>(p_desc);
+      const uint32_t v_hi = static_cast<uint32_t>(v_desc >> 32), p_hi = static_cast<uint32_t>(p_desc >> 32);
+      uint32_t o_parity = 1;
+#pragma unroll 1
+      for (uint32_t n = 0; n < items; ++n) {
+        wait_for(&bars[L::bPFull], n & 1, abort_flag, p.d_error);
+        const bool opens = (info[n % kInfoRing].x & kOpens) != 0;
+        if (opens) {
+          wait_for(&bars[L::bOFree], o_parity, abort_flag, p.d_error);
+          o_parity ^= 1;
         }
+#pragma unroll kUp
+        for (int v = 0; v < 8; ++v) {
+          const int half = v >> 2, qq = v & 3;
+          wait_for(&bars[L::bVFull + qq], half, abort_flag, p.d_error);
+          tc_fence_after();
+          const uint32_t d = tmem + L::cO + qq * NR, a = v_lo + ((qq * kVUnitBytes) >> 4), b = p_lo + ((half * 8 * p_sbo) >> 4);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mma_f16_ss(d, a + ((j * 2048) >> 4), v_hi, b + ((j * 2 * p_sbo) >> 4), p_hi, idesc, !(opens && v < 4 && j == 0));
+          commit_one(&bars[L::bVFree + qq]);
+        }
+        commit_one(&bars[L::bPFree]);
       }
+      commit_one(&bars[L::bDrain]);
+      wait_drain(&bars[L::bDrain], p.d_error);
     } else if (warp < kSoftmaxWarps) {
       // ---------------------------------------------------------------- softmax
       constexpr int kSoftmaxThreads = kSoftmaxWarps * 32;
@@ -684,37 +747,47 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
         bool bad_len;
         const Unit t = unit_of<NR>(p, groups, u, bad_len);
         const uint16_t* q = p.q + (static_cast<int64_t>(t.b) * p.rows + t.row0) * kD;
+        constexpr int kRows = NR == 32 ? 4 : 2;  // rows whose loads are in flight together (registers)
 #pragma unroll 1
-        for (int r = warp; r < NR; r += kSoftmaxWarps) {
-          uint4 a = make_uint4(0, 0, 0, 0), b = a;
-          if (r < t.nrows) {
-            const uint4* src = reinterpret_cast<const uint4*>(q + static_cast<int64_t>(r) * kD + lane * 16);
-            a = __ldg(src);
-            b = __ldg(src + 1);
+        for (int r0 = warp * kRows; r0 < NR; r0 += kSoftmaxWarps * kRows) {
+          uint32_t wv[kRows][8];
+#pragma unroll
+          for (int i = 0; i < kRows; ++i) {
+            uint4 a = make_uint4(0, 0, 0, 0), b = a;
+            if (r0 + i < t.nrows) {
+              const uint4* src = reinterpret_cast<const uint4*>(q + static_cast<int64_t>(r0 + i) * kD + lane * 16);
+              a = __ldg(src);
+              b = __ldg(src + 1);
+            }
+            wv[i][0] = a.x, wv[i][1] = a.y, wv[i][2] = a.z, wv[i][3] = a.w;
+            wv[i][4] = b.x, wv[i][5] = b.y, wv[i][6] = b.z, wv[i][7] = b.w;
           }
-          const uint32_t wv[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-          // The largest exponent of the row (the sign bits shifted out).
-          uint32_t top = 0;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) top = max(top, max((wv[k] << 17) >> 24, (wv[k] << 1) >> 24));
-          top = __reduce_max_sync(0xFFFFFFFFu, top);
-          // Largest value to [2^14, 2^15); nothing to scale in a row of zeros or of infinities.
-          const int e = top == 0 || top == 255 ? 0 : max(static_cast<int>(top) - 127 - 14, -100);
-          const float up = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-          uint32_t h[8];
+          for (int i = 0; i < kRows; ++i) {
+            const int r = r0 + i;
+            // The largest exponent of the row (the sign bits shifted out).
+            uint32_t top = 0;
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            h[k] = pack_f16x2(__uint_as_float(wv[k] << 16) * up, __uint_as_float(wv[k] & 0xFFFF0000u) * up);
-          uint8_t* dst = sQ + (lane >> 2) * (NR * 128);
-          const uint32_t off = r * 128 + (lane & 3) * 32;
-          *reinterpret_cast<uint4*>(dst + swz<128>(off)) = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(dst + swz<128>(off + 16)) = make_uint4(h[4], h[5], h[6], h[7]);
-          if (lane == 0) {
-            c_scale[r] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-            c_m[r] = kNoMax;
-            const int hi = t.first + min(t.row0 + r, p.rows - 1) / p.h;
-            c_hi[r] = hi;
-            c_lo[r] = window_start(p, hi);
+            for (int k = 0; k < 8; ++k) top = max(top, max((wv[i][k] << 17) >> 24, (wv[i][k] << 1) >> 24));
+            top = __reduce_max_sync(0xFFFFFFFFu, top);
+            // Largest value to [2^14, 2^15); nothing to scale in a row of zeros or of infinities.
+            const int e = top == 0 || top == 255 ? 0 : max(static_cast<int>(top) - 127 - 14, -100);
+            const float up = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+            uint32_t h[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              h[k] = pack_f16x2(__uint_as_float(wv[i][k] << 16) * up, __uint_as_float(wv[i][k] & 0xFFFF0000u) * up);
+            uint8_t* dst = sQ + (lane >> 2) * (NR * 128);
+            const uint32_t off = r * 128 + (lane & 3) * 32;
+            *reinterpret_cast<uint4*>(dst + swz<128>(off)) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(dst + swz<128>(off + 16)) = make_uint4(h[4], h[5], h[6], h[7]);
+            if (lane == 0) {
+              c_scale[r] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+              c_mb[r] = kNoMax;
+              const int hi = t.first + min(t.row0 + r, p.rows - 1) / p.h;
+              c_hi[r] = hi;
+              c_lo[r] = window_start(p, hi);
+            }
           }
         }
         fence_proxy_async_smem();
@@ -722,26 +795,28 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
         if (lane == 0) mbar_arrive(&bars[L::bQFull]);
         named_bar_sync(1, kSoftmaxThreads);  // the row arrays are complete
       };
-      // This thread's scores of an item, scaled and masked.
-      const auto scores = [&](uint32_t n, const int4& it, float (&x)[NC]) {
-        uint32_t r[NC];
-        tmem_ld<NC>(tS + (n & 1) * NR, r);
-        const float4* sc4 = reinterpret_cast<const float4*>(c_scale + c0);
+      // This thread's exponents of rows h .. h + HC - 1 in an item, scale *
+      // score - (m - 7), or its scaled scores themselves (against_max false); masked.
+      const auto exponents = [&](uint32_t n, const int2& it, int h, float (&y)[HC], bool against_max) {
+        uint32_t r[HC];
+        tmem_ld<HC>(tS + (n & 1) * NR + h, r);
+        const float4* sc4 = reinterpret_cast<const float4*>(c_scale + c0 + h);
+        const float4* mb4 = reinterpret_cast<const float4*>(c_mb + c0 + h);
 #pragma unroll
-        for (int k = 0; k < NC / 4; ++k) {
-          const float4 s = sc4[k];
-          x[4 * k] = __uint_as_float(r[4 * k]) * s.x;
-          x[4 * k + 1] = __uint_as_float(r[4 * k + 1]) * s.y;
-          x[4 * k + 2] = __uint_as_float(r[4 * k + 2]) * s.z;
-          x[4 * k + 3] = __uint_as_float(r[4 * k + 3]) * s.w;
+        for (int k = 0; k < HC / 4; ++k) {
+          const float4 s = sc4[k], m = against_max ? mb4[k] : make_float4(0.f, 0.f, 0.f, 0.f);
+          y[4 * k] = fmaf(__uint_as_float(r[4 * k]), s.x, -m.x);
+          y[4 * k + 1] = fmaf(__uint_as_float(r[4 * k + 1]), s.y, -m.y);
+          y[4 * k + 2] = fmaf(__uint_as_float(r[4 * k + 2]), s.z, -m.z);
+          y[4 * k + 3] = fmaf(__uint_as_float(r[4 * k + 3]), s.w, -m.w);
         }
         if (!(it.x & kWhole)) {
           const int pos = it.y * kTile + row;
           const bool there = token_there(it.x, row), sink = pos < p.sinks;
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            const bool see = there && pos <= c_hi[c0 + c] && (sink || pos >= c_lo[c0 + c]);
-            x[c] = see ? x[c] : -INFINITY;
+          for (int c = 0; c < HC; ++c) {
+            const bool see = there && pos <= c_hi[c0 + h + c] && (sink || pos >= c_lo[c0 + h + c]);
+            y[c] = see ? y[c] : -INFINITY;
           }
         }
       };
@@ -750,46 +825,43 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
       float l[NC];
 #pragma unroll 1
       for (uint32_t n = 0; n < items; ++n) {
-        mbar_wait(&bars[L::bInfo + n % kInfoRing], (n / kInfoRing) & 1, abort_flag, p.d_error, kPagedWaitNs);
-        int4 it = info[n % kInfoRing];
-        it.z = min(max(it.z, 0), units - 1);  // (after a wait that gave up it may be anything)
+        wait_for(&bars[L::bInfo + n % kInfoRing], (n / kInfoRing) & 1, abort_flag, p.d_error);
+        const int2 it = *reinterpret_cast<const int2*>(&info[n % kInfoRing]);
         if (it.x & kOpens) {
 #pragma unroll
           for (int c = 0; c < NC; ++c) l[c] = 0.f;
         }
-        mbar_wait(&bars[L::bSFull + (n & 1)], (n / 2) & 1, abort_flag, p.d_error, kPagedWaitNs);
+        wait_for(&bars[L::bSFull + (n & 1)], (n >> 1) & 1, abort_flag, p.d_error);
         __syncwarp();
         tc_fence_after();
-        const float4* m4 = reinterpret_cast<const float4*>(c_m + c0);
-        float excess = -INFINITY;
-        {
-          float x[NC];
-          scores(n, it, x);
+        float top = -INFINITY;
+#pragma unroll 1
+        for (int h = 0; h < NC; h += HC) {
+          float y[HC];
+          exponents(n, it, h, y, true);
 #pragma unroll
-          for (int k = 0; k < NC / 4; ++k) {
-            const float4 m = m4[k];
-            excess = fmaxf(excess, fmaxf(fmaxf(x[4 * k] - m.x, x[4 * k + 1] - m.y),
-                                         fmaxf(x[4 * k + 2] - m.z, x[4 * k + 3] - m.w)));
-          }
+          for (int c = 0; c < HC; ++c) top = fmaxf(top, y[c]);
         }
-        if (any_of(2, kSoftmaxThreads, excess > kSlack)) {
+        if (any_of(2, kSoftmaxThreads, top > kSlack + kPBias)) {
           // Exact maxima of the tile's rows.
-          {
-            float x[NC];
-            scores(n, it, x);
-            LaneReduce<NC, 16>::run(x, lane, OpMax());
-            if (lane % (32 / NC) == 0) red[quad * NR + c0 + column_of<NC>(lane)] = x[0];
+#pragma unroll
+          for (int h = 0; h < NC; h += HC) {
+            float y[HC];
+            exponents(n, it, h, y, false);
+            LaneReduce<HC, 16>::run(y, lane, OpMax());
+            if (lane % (32 / HC) == 0) red[quad * NR + c0 + h + column_of<HC>(lane)] = y[0];
           }
           named_bar_sync(1, kSoftmaxThreads);
           bool moved = false;
           if (tid < NR) {
-            const float mt = fmaxf(fmaxf(red[tid], red[NR + tid]), fmaxf(red[2 * NR + tid], red[3 * NR + tid]));
-            const float old = c_m[tid];
+            const float mb =
+                fmaxf(fmaxf(red[tid], red[NR + tid]), fmaxf(red[2 * NR + tid], red[3 * NR + tid])) - kPBias;
+            const float old = c_mb[tid];
             float alpha = 1.f;
-            if (mt > old + kSlack) {
-              alpha = ex2_approx(old - mt);
+            if (mb > old + kSlack) {
+              alpha = ex2_approx(old - mb);
               moved = old != kNoMax;
-              c_m[tid] = mt;
+              c_mb[tid] = mb;
             }
             c_alpha[tid] = alpha;
           }
@@ -798,7 +870,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
             for (int c = 0; c < NC; ++c) l[c] *= c_alpha[c0 + c];
             // O^T follows, once the product before this one is complete.
             if (!(it.x & kOpens)) {
-              mbar_wait(&bars[L::bPFree + ((n - 1) & 1)], ((n - 1) / 2) & 1, abort_flag, p.d_error, kPagedWaitNs);
+              wait_for(&bars[L::bPFree], (n & 1) ^ 1, abort_flag, p.d_error);
               __syncwarp();
               tc_fence_after();
 #pragma unroll 1
@@ -814,39 +886,37 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
             }
           }
         }
-        // P = 2^(x - m + 7), row `row` of P^T (MN-major), once the product
-        // two items back has read this buffer.
-        if (n >= 2) mbar_wait(&bars[L::bPFree + (n & 1)], (n / 2 - 1) & 1, abort_flag, p.d_error, kPagedWaitNs);
-        __syncwarp();
-        {
-          float x[NC];
-          scores(n, it, x);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[L::bSFree + (n & 1)]);
-          uint8_t* dst = sP + (n & 1) * L::kPBytes;
+        // P = 2^y, row `row` of P^T (MN-major), once the last product has read the buffer.
 #pragma unroll
-          for (int k = 0; k < NC / 8; ++k) {
-            float e[8];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float4 m = m4[2 * k + j];
-              e[4 * j] = ex2_approx(x[8 * k + 4 * j] - (m.x - kPBias));
-              e[4 * j + 1] = ex2_approx(x[8 * k + 4 * j + 1] - (m.y - kPBias));
-              e[4 * j + 2] = ex2_approx(x[8 * k + 4 * j + 2] - (m.z - kPBias));
-              e[4 * j + 3] = ex2_approx(x[8 * k + 4 * j + 3] - (m.w - kPBias));
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) l[8 * k + j] += e[j];
-            *reinterpret_cast<uint4*>(dst + swz<2 * NR>(row * (2 * NR) + c0 * 2 + k * 16)) =
-                make_uint4(pack_f16x2(e[0], e[1]), pack_f16x2(e[2], e[3]), pack_f16x2(e[4], e[5]),
-                           pack_f16x2(e[6], e[7]));
+        for (int h = 0; h < NC; h += HC) {
+          float y[HC];
+          exponents(n, it, h, y, true);
+          if (h + HC == NC) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[L::bSFree + (n & 1)]);
           }
+          uint32_t e[HC / 2];
+#pragma unroll
+          for (int c = 0; c < HC; c += 2) {
+            const float a = ex2_approx(y[c]), b = ex2_approx(y[c + 1]);
+            l[h + c] += a;
+            l[h + c + 1] += b;
+            e[c / 2] = pack_f16x2(a, b);
+          }
+          if (h == 0) {
+            wait_for(&bars[L::bPFree], (n & 1) ^ 1, abort_flag, p.d_error);
+            __syncwarp();
+          }
+#pragma unroll
+          for (int k = 0; k < HC / 8; ++k)
+            *reinterpret_cast<uint4*>(sP + swz<2 * NR>(row * (2 * NR) + (c0 + h) * 2 + k * 16)) =
+                make_uint4(e[4 * k], e[4 * k + 1], e[4 * k + 2], e[4 * k + 3]);
         }
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[L::bPFull + (n & 1)]);
+        if (lane == 0) mbar_arrive(&bars[L::bPFull]);
         if (!(it.x & kCloses)) continue;
 
         // The piece's end: row sums over the tile's tokens, then O^T / l.
@@ -856,12 +926,13 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
         const bool whole_unit = (it.x & (kFromStart | kToEnd)) == (kFromStart | kToEnd);
         // Partials: slot 2 part + 1 for a piece that begins its unit, 2 part for one that goes on with it.
         const int prow = (part * 2 + ((it.x & kFromStart) ? 1 : 0)) * NR;
-        const int ub = it.z / groups, urow0 = (it.z - ub * groups) * NR;
+        const int u = min(max(info[n % kInfoRing].z, 0), units - 1);  // (after a wait that gave up it may be anything)
+        const int ub = u / groups, urow0 = (u - ub * groups) * NR;
         const int orow = ub * p.rows + urow0, nrows = min(NR, p.rows - urow0);
         if (tid < NR) {
           const float sum = (red[tid] + red[NR + tid]) + (red[2 * NR + tid] + red[3 * NR + tid]);
           c_linv[tid] = sum > 0.f ? 1.f / sum : 0.f;
-          const float lse = sum > 0.f ? (c_m[tid] - kPBias + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+          const float lse = sum > 0.f ? (c_mb[tid] + log2f(sum)) * 0.6931471805599453f : -INFINITY;
           if (!whole_unit)
             p.ws_lse[prow + tid] = lse;
           else if (tid < nrows)
@@ -869,8 +940,8 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
         }
         named_bar_sync(1, kSoftmaxThreads);
         // The next unit's Q goes in while the last product runs (this piece's scores are all done).
-        if (n + 1 < items) load_q(min(it.z + 1, units - 1));
-        mbar_wait(&bars[L::bPFree + (n & 1)], (n / 2) & 1, abort_flag, p.d_error, kPagedWaitNs);
+        if (n + 1 < items) load_q(min(u + 1, units - 1));
+        wait_for(&bars[L::bPFree], n & 1, abort_flag, p.d_error);
         __syncwarp();
         tc_fence_after();
         // Lane = dim, columns = rows.
@@ -907,7 +978,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kValueWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
