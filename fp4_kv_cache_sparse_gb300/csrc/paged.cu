@@ -25,7 +25,7 @@
 //                      operand of O^T += V^T P^T.
 //   issuer (1 warp)    all tensor-core work; S^T of the next tile goes before
 //                      O^T of this one, so the softmax runs beside O^T.
-//   softmax (8 or 16)  thread = token x 8 or 16 rows: scale, mask, lazy
+//   softmax (8 warps)  thread = token x half of the rows: scale, mask, lazy
 //                      running maximum, P^T to shared memory, row sums in
 //                      registers; at a unit's end the epilogue, before it
 //                      the next unit's Q.
@@ -60,13 +60,6 @@ constexpr int kVUnitTokens = 64;
 constexpr int kVUnitBytes = kVUnitTokens * 128 * 2;  // 64 tokens x 128 dims of V, two chunks of 64 dims
 constexpr int kInfoRing = 8;
 constexpr uint64_t kPagedWaitNs = 2000000000ull;  // 2 s per wait
-#ifndef KUNROLL
-#define KUNROLL 1
-#define VPIECES 4
-#define QUNROLL 1
-#define PUNROLL 1
-#endif
-constexpr int kUk = KUNROLL, kUq = QUNROLL, kUp = PUNROLL;
 constexpr float kSlack = 8.f;                // the running maximum may lag by 2^8
 constexpr float kPBias = 7.f;                // P of the maximum is 2^7
 constexpr float kNoMax = -3.0e38f;           // running maximum before any visible token
@@ -91,7 +84,7 @@ struct PSmem {
   static constexpr int kPOff = kVOff + kVRing * kVUnitBytes;
   static constexpr int kRawOff = kPOff + kPBytes;
   static constexpr int kBarOff = kRawOff + kRaw * kPageBytes;
-  static constexpr int kNumBars = 2 * kRaw + 2 * kKRing + 2 * kVRing + 6 + 3 + kInfoRing;
+  static constexpr int kNumBars = 2 * kRaw + 2 * kKRing + 2 * kVRing + 6 + 4 + kInfoRing;
   static constexpr int kColOff = (kBarOff + kNumBars * 8 + 15) & ~15;  // per-row arrays
   // float mb[NR], alpha[NR], scale[NR], linv[NR]; int hi[NR], lo[NR]; float red[4][NR]
   static constexpr int kInfoOff = kColOff + 10 * NR * 4;
@@ -103,7 +96,7 @@ struct PSmem {
   static constexpr int bRawFull = 0, bRawFree = bRawFull + kRaw, bKFull = bRawFree + kRaw, bKFree = bKFull + kKRing,
                        bVFull = bKFree + kKRing, bVFree = bVFull + kVRing, bSFull = bVFree + kVRing,
                        bSFree = bSFull + 2, bPFull = bSFree + 2, bPFree = bPFull + 1, bQFull = bPFree + 1,
-                       bOFree = bQFull + 1, bDrain = bOFree + 1, bInfo = bDrain + 1;
+                       bOFree = bQFull + 1, bDrain = bOFree + 1, bQRaw = bDrain + 1, bInfo = bQRaw + 1;
   static_assert(bInfo + kInfoRing == kNumBars, "barriers");
   // Tensor memory columns: O^T quarters, S^T buffers, K quarters.
   static constexpr int cO = 0, cS = 4 * NR, cK = 6 * NR;
@@ -281,6 +274,19 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 // Instruction descriptor of kind::f16 with f16 operands and fp32 accumulation.
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn, bool b_mn) {
   return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
@@ -376,10 +382,11 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 // ------------------------------------------------------------------ the kernel
 
 template <int NR>
-__global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(const PagedParams p, const int groups) {
+__global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(const PagedParams p, const int groups,
+                                                                                const __grid_constant__ CUtensorMap q_map) {
   using L = PSmem<NR>;
   constexpr int NC = NR / L::kSides;    // rows of a softmax thread
-  constexpr int HC = NR == 32 ? 16 : 8;  // of which it works on so many at a time
+  constexpr int HC = NR == 16 ? 8 : 16;  // of which it works on so many at a time
   constexpr int kPagedThreads = L::kThreads, kSoftmaxWarps = L::kSoftmaxWarps;
   constexpr int kKWarp0 = L::kKWarp0, kVWarp0 = L::kVWarp0, kLoadWarp = L::kLoadWarp;
   constexpr int kScoreWarp = L::kScoreWarp, kValueWarp = L::kValueWarp;
@@ -430,6 +437,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
     mbar_init(&bars[L::bQFull], kSoftmaxWarps);
     mbar_init(&bars[L::bOFree], kSoftmaxWarps);
     mbar_init(&bars[L::bDrain], 2);
+    mbar_init(&bars[L::bQRaw], 1);
     for (int i = 0; i < kInfoRing; ++i) mbar_init(&bars[L::bInfo + i], 1);
     *abort_flag = 0;
     start_u[0] = -1;
@@ -437,6 +445,10 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
     fence_proxy_async_smem();
   }
   if (warp == kValueWarp) tmem_alloc(tmem_slot, 512);
+
+  // Launched as a programmatic dependent: what comes before this line runs
+  // beside the end of the stream's previous kernel, nothing after it does.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // The cut: items of all units, this part's run, and the unit it begins in.
   const int units = p.batch * groups;
@@ -596,7 +608,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
           wait_for(&bars[L::bKFree + ks], parity ^ 1, abort_flag, p.d_error);
           tc_fence_after();
           const uint32_t t = tK + ks * 64;
-#pragma unroll kUk
+#pragma unroll 1
           for (int hh = 0; hh < 2; ++hh) {
             const uint4 a = *reinterpret_cast<const uint4*>(src + hh * 32 + near);
             const uint4 b = *reinterpret_cast<const uint4*>(src + hh * 32 + far);
@@ -640,17 +652,17 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
           const uint8_t* rec = rows + slot * kPageBytes;
           const uint8_t* scl = rec + 256 - qq * 56 + piece * 2;
 #pragma unroll 1
-          for (int i0 = 0; i0 < 8; i0 += VPIECES) {
-            uint4 data[VPIECES];
-            uint32_t sc[VPIECES];
+          for (int i0 = 0; i0 < 8; i0 += 4) {
+            uint4 data[4];
+            uint32_t sc[4];
 #pragma unroll
-            for (int i = 0; i < VPIECES; ++i) {
+            for (int i = 0; i < 4; ++i) {
               data[i] = *reinterpret_cast<const uint4*>(rec + (i0 + i) * 8 * kRecFp4 + piece * 16);
               sc[i] = *reinterpret_cast<const uint16_t*>(scl + (i0 + i) * 8 * kRecFp4);
             }
             if (i0 == 0) wait_for(&bars[L::bVFree + qq], half ^ 1, abort_flag, p.d_error);
 #pragma unroll
-            for (int i = 0; i < VPIECES; ++i) {
+            for (int i = 0; i < 4; ++i) {
               uint32_t o[16];
               decode32(data[i], (i0 + i) * 8 < have ? sc[i] : 0u, o);
 #pragma unroll
@@ -679,7 +691,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
       for (uint32_t n = 0; n < items; ++n) {
         const uint32_t d = tmem + L::cS + (n & 1) * NR;
         wait_for(&bars[L::bSFree + (n & 1)], ((n >> 1) & 1) ^ 1, abort_flag, p.d_error);
-#pragma unroll kUq
+#pragma unroll 1
         for (int qq = 0; qq < 4; ++qq) {
           const int ks = qq % L::kKRing;
           wait_for(&bars[L::bKFull + ks], (L::kKRing == 4 ? n : static_cast<uint32_t>(qq / L::kKRing)) & 1, abort_flag,
@@ -717,7 +729,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
           wait_for(&bars[L::bOFree], o_parity, abort_flag, p.d_error);
           o_parity ^= 1;
         }
-#pragma unroll kUp
+#pragma unroll 1
         for (int v = 0; v < 8; ++v) {
           const int half = v >> 2, qq = v & 3;
           wait_for(&bars[L::bVFull + qq], half, abort_flag, p.d_error);
@@ -741,65 +753,67 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
       const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
       const uint32_t tS = tmem + lanes + L::cS + c0, tO = tmem + lanes + L::cO;
 
-      // Q rows of a unit: bf16 -> scaled f16, K-major with 128-byte swizzle,
-      // one row per warp at a time (lane = 16 dims); and the rows' masks.
-      const auto load_q = [&](int u) {
+      // A unit's Q arrives by TMA as bf16, K-major with 128-byte swizzle ...
+      const auto request_q = [&](int u) {
+        const int b = u / groups, y = b * p.rows + (u - b * groups) * NR;
+        expect_tx(&bars[L::bQRaw], L::kQBytes);
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) tma_load_2d(sQ + c * (NR * 128), &q_map, c * 64, y, &bars[L::bQRaw]);
+      };
+      // ... and becomes scaled f16 in place, a row per warp at a time (lane =
+      // 16 dims); rows past the unit's become zeros.
+      uint32_t q_parity = 0;
+      const auto convert_q = [&](int u) {
         bool bad_len;
         const Unit t = unit_of<NR>(p, groups, u, bad_len);
-        const uint16_t* q = p.q + (static_cast<int64_t>(t.b) * p.rows + t.row0) * kD;
-        constexpr int kRows = NR == 32 ? 4 : 2;  // rows whose loads are in flight together (registers)
-#pragma unroll 1
-        for (int r0 = warp * kRows; r0 < NR; r0 += kSoftmaxWarps * kRows) {
-          uint32_t wv[kRows][8];
+        wait_for(&bars[L::bQRaw], q_parity, abort_flag, p.d_error);
+        q_parity ^= 1;
+        uint8_t* base = sQ + (lane >> 2) * (NR * 128);
+#pragma unroll 2
+        for (int r = warp; r < NR; r += kSoftmaxWarps) {
+          const uint32_t off = r * 128 + (lane & 3) * 32;
+          uint4* pa = reinterpret_cast<uint4*>(base + swz<128>(off));
+          uint4* pb = reinterpret_cast<uint4*>(base + swz<128>(off + 16));
+          const uint4 a = *pa, b = *pb;
+          uint32_t wv[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+          // The largest exponent of the row (the sign bits shifted out).
+          uint32_t top = 0;
 #pragma unroll
-          for (int i = 0; i < kRows; ++i) {
-            uint4 a = make_uint4(0, 0, 0, 0), b = a;
-            if (r0 + i < t.nrows) {
-              const uint4* src = reinterpret_cast<const uint4*>(q + static_cast<int64_t>(r0 + i) * kD + lane * 16);
-              a = __ldg(src);
-              b = __ldg(src + 1);
-            }
-            wv[i][0] = a.x, wv[i][1] = a.y, wv[i][2] = a.z, wv[i][3] = a.w;
-            wv[i][4] = b.x, wv[i][5] = b.y, wv[i][6] = b.z, wv[i][7] = b.w;
+          for (int k = 0; k < 8; ++k) {
+            if (r >= t.nrows) wv[k] = 0;
+            top = max(top, max((wv[k] << 17) >> 24, (wv[k] << 1) >> 24));
           }
+          top = __reduce_max_sync(0xFFFFFFFFu, top);
+          // Largest value to [2^14, 2^15); nothing to scale in a row of zeros or of infinities.
+          const int e = top == 0 || top == 255 ? 0 : max(static_cast<int>(top) - 127 - 14, -100);
+          const float up = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
-          for (int i = 0; i < kRows; ++i) {
-            const int r = r0 + i;
-            // The largest exponent of the row (the sign bits shifted out).
-            uint32_t top = 0;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) top = max(top, max((wv[i][k] << 17) >> 24, (wv[i][k] << 1) >> 24));
-            top = __reduce_max_sync(0xFFFFFFFFu, top);
-            // Largest value to [2^14, 2^15); nothing to scale in a row of zeros or of infinities.
-            const int e = top == 0 || top == 255 ? 0 : max(static_cast<int>(top) - 127 - 14, -100);
-            const float up = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-            uint32_t h[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              h[k] = pack_f16x2(__uint_as_float(wv[i][k] << 16) * up, __uint_as_float(wv[i][k] & 0xFFFF0000u) * up);
-            uint8_t* dst = sQ + (lane >> 2) * (NR * 128);
-            const uint32_t off = r * 128 + (lane & 3) * 32;
-            *reinterpret_cast<uint4*>(dst + swz<128>(off)) = make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4*>(dst + swz<128>(off + 16)) = make_uint4(h[4], h[5], h[6], h[7]);
-            if (lane == 0) {
-              c_scale[r] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-              c_mb[r] = kNoMax;
-              const int hi = t.first + min(t.row0 + r, p.rows - 1) / p.h;
-              c_hi[r] = hi;
-              c_lo[r] = window_start(p, hi);
-            }
+          for (int k = 0; k < 8; ++k)
+            wv[k] = pack_f16x2(__uint_as_float(wv[k] << 16) * up, __uint_as_float(wv[k] & 0xFFFF0000u) * up);
+          *pa = make_uint4(wv[0], wv[1], wv[2], wv[3]);
+          *pb = make_uint4(wv[4], wv[5], wv[6], wv[7]);
+          if (lane == 0) {
+            // Never 0, so that an infinite score stays infinite (scores are below 2^36).
+            const float s = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+            c_scale[r] = s == 0.f ? 1e-30f : s;
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[L::bQFull]);
+        if (tid < NR) {
+          const int hi = t.first + min(t.row0 + tid, p.rows - 1) / p.h;
+          c_mb[tid] = kNoMax;
+          c_hi[tid] = hi;
+          c_lo[tid] = window_start(p, hi);
+        }
         named_bar_sync(1, kSoftmaxThreads);  // the row arrays are complete
       };
       // This thread's exponents of rows h .. h + HC - 1 in an item, scale *
-      // score - (m - 7), or its scaled scores themselves (against_max false); masked.
-      const auto exponents = [&](uint32_t n, const int2& it, int h, float (&y)[HC], bool against_max) {
+      // score - (m - 7), or its scaled scores themselves (against_max false).
+      const auto exponents = [&](uint32_t s_col, int h, float (&y)[HC], bool against_max) {
         uint32_t r[HC];
-        tmem_ld<HC>(tS + (n & 1) * NR + h, r);
+        tmem_ld<HC>(s_col + h, r);
         const float4* sc4 = reinterpret_cast<const float4*>(c_scale + c0 + h);
         const float4* mb4 = reinterpret_cast<const float4*>(c_mb + c0 + h);
 #pragma unroll
@@ -810,18 +824,10 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
           y[4 * k + 2] = fmaf(__uint_as_float(r[4 * k + 2]), s.z, -m.z);
           y[4 * k + 3] = fmaf(__uint_as_float(r[4 * k + 3]), s.w, -m.w);
         }
-        if (!(it.x & kWhole)) {
-          const int pos = it.y * kTile + row;
-          const bool there = token_there(it.x, row), sink = pos < p.sinks;
-#pragma unroll
-          for (int c = 0; c < HC; ++c) {
-            const bool see = there && pos <= c_hi[c0 + h + c] && (sink || pos >= c_lo[c0 + h + c]);
-            y[c] = see ? y[c] : -INFINITY;
-          }
-        }
       };
 
-      load_q(start_u[0]);
+      if (tid == 0) request_q(start_u[0]);
+      convert_q(start_u[0]);
       float l[NC];
 #pragma unroll 1
       for (uint32_t n = 0; n < items; ++n) {
@@ -832,22 +838,42 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
           for (int c = 0; c < NC; ++c) l[c] = 0.f;
         }
         wait_for(&bars[L::bSFull + (n & 1)], (n >> 1) & 1, abort_flag, p.d_error);
-        __syncwarp();
         tc_fence_after();
+        const uint32_t s_col = tS + (n & 1) * NR;
+        // The piece's last scores are there, so its Q has been read: the next unit's may come.
+        if ((it.x & kCloses) && n + 1 < items && tid == 0) request_q(min(max(info[n % kInfoRing].z, 0) + 1, units - 1));
+        if (!(it.x & kWhole)) {
+          // Scores of tokens that a row does not see become infinite, of the sign that its scale turns to minus.
+          const int pos = it.y * kTile + row;
+          const bool there = token_there(it.x, row), sink = pos < p.sinks;
+#pragma unroll 1
+          for (int h = 0; h < NC; h += 8) {
+            uint32_t r[8];
+            tmem_ld<8>(s_col + h, r);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const int i = c0 + h + c;
+              const bool see = there && pos <= c_hi[i] && (sink || pos >= c_lo[i]);
+              if (!see) r[c] = c_scale[i] > 0.f ? 0xFF800000u : 0x7F800000u;
+            }
+            tmem_st8(s_col + h, r);
+          }
+          tmem_wait_st();
+        }
         float top = -INFINITY;
 #pragma unroll 1
         for (int h = 0; h < NC; h += HC) {
           float y[HC];
-          exponents(n, it, h, y, true);
+          exponents(s_col, h, y, true);
 #pragma unroll
           for (int c = 0; c < HC; ++c) top = fmaxf(top, y[c]);
         }
         if (any_of(2, kSoftmaxThreads, top > kSlack + kPBias)) {
           // Exact maxima of the tile's rows.
-#pragma unroll
+#pragma unroll 1
           for (int h = 0; h < NC; h += HC) {
             float y[HC];
-            exponents(n, it, h, y, false);
+            exponents(s_col, h, y, false);
             LaneReduce<HC, 16>::run(y, lane, OpMax());
             if (lane % (32 / HC) == 0) red[quad * NR + c0 + h + column_of<HC>(lane)] = y[0];
           }
@@ -890,7 +916,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
 #pragma unroll
         for (int h = 0; h < NC; h += HC) {
           float y[HC];
-          exponents(n, it, h, y, true);
+          exponents(s_col, h, y, true);
           if (h + HC == NC) {
             tc_fence_before();
             __syncwarp();
@@ -940,32 +966,43 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
         }
         named_bar_sync(1, kSoftmaxThreads);
         // The next unit's Q goes in while the last product runs (this piece's scores are all done).
-        if (n + 1 < items) load_q(min(u + 1, units - 1));
+        if (n + 1 < items) convert_q(min(u + 1, units - 1));
         wait_for(&bars[L::bPFree], n & 1, abort_flag, p.d_error);
         __syncwarp();
         tc_fence_after();
         // Lane = dim, columns = rows.
+        constexpr int EC = NR == 32 ? 32 : 16;  // columns at a time (registers)
 #pragma unroll 1
-        for (int i = side; i < 4 * (NR / 16); i += L::kSides) {
-          const int qq = i / (NR / 16), cc = (i % (NR / 16)) * 16;
+        for (int i = side; i < 4 * (NR / EC); i += L::kSides) {
+          const int qq = i / (NR / EC), cc = (i % (NR / EC)) * EC;
           const int d = qq * 128 + row;
-          uint32_t o[16];
-          tmem_ld16(tO + qq * NR + cc, o);
+          uint32_t o[EC];
+          tmem_ld<EC>(tO + qq * NR + cc, o);
+          const float4* l4 = reinterpret_cast<const float4*>(c_linv + cc);
+#pragma unroll
+          for (int k = 0; k < EC / 4; ++k) {
+            const float4 s = l4[k];
+            o[4 * k] = __float_as_uint(__uint_as_float(o[4 * k]) * s.x);
+            o[4 * k + 1] = __float_as_uint(__uint_as_float(o[4 * k + 1]) * s.y);
+            o[4 * k + 2] = __float_as_uint(__uint_as_float(o[4 * k + 2]) * s.z);
+            o[4 * k + 3] = __float_as_uint(__uint_as_float(o[4 * k + 3]) * s.w);
+          }
           if (whole_unit) {
             // Even lanes take row cc + k of dims (d, d + 1), odd lanes row cc + k + 1.
+            const bool odd = (lane & 1) != 0;
+            uint16_t* dst = p.out + static_cast<int64_t>(orow + cc + (odd ? 1 : 0)) * kD + (d & ~1);
+            const int left = nrows - cc - (odd ? 1 : 0);
 #pragma unroll
-            for (int k = 0; k < 16; k += 2) {
-              const float a = __uint_as_float(o[k]) * c_linv[cc + k], b = __uint_as_float(o[k + 1]) * c_linv[cc + k + 1];
-              const float got = __shfl_xor_sync(0xFFFFFFFFu, (lane & 1) ? a : b, 1);
-              const __nv_bfloat162 v = (lane & 1) ? __floats2bfloat162_rn(got, b) : __floats2bfloat162_rn(a, got);
-              const int r = cc + k + (lane & 1);
-              if (r < nrows)
-                *reinterpret_cast<__nv_bfloat162*>(p.out + static_cast<int64_t>(orow + r) * kD + (d & ~1)) = v;
+            for (int k = 0; k < EC; k += 2) {
+              const float a = __uint_as_float(o[k]), b = __uint_as_float(o[k + 1]);
+              const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 1);
+              const __nv_bfloat162 v = odd ? __floats2bfloat162_rn(got, b) : __floats2bfloat162_rn(a, got);
+              if (k < left) *reinterpret_cast<__nv_bfloat162*>(dst + k * kD) = v;
             }
           } else {
             float* dst = p.ws_o + static_cast<int64_t>(prow + cc) * kD + d;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) dst[k * kD] = __uint_as_float(o[k]) * c_linv[cc + k];
+            for (int k = 0; k < EC; ++k) dst[k * kD] = __uint_as_float(o[k]);
           }
         }
         tc_fence_before();
@@ -1042,19 +1079,36 @@ cudaError_t launch(const PagedParams& p, const PagedPlan& plan, cudaStream_t str
   cudaError_t e = max_dynamic_smem_once(configured, reinterpret_cast<const void*>(paged_decode_kernel<NR>),
                                         PSmem<NR>::kAlloc);
   if (e != cudaSuccess) return e;
-  paged_decode_kernel<NR><<<plan.num_parts, PSmem<NR>::kThreads, PSmem<NR>::kAlloc, stream>>>(p, plan.groups);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  // The merge may be scheduled while the decode drains; its blocks wait for it.
+  // Q viewed as rows of 512 bf16; a box is NR rows x 64 dims, 128-byte swizzled.
+  EncodeTiledFn enc = tensor_map_encoder();
+  if (enc == nullptr) return cudaErrorNotSupported;
+  CUtensorMap q_map;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(p.batch) * p.rows};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(kD) * 2};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(NR)};
+  const cuuint32_t estr[2] = {1, 1};
+  if (enc(&q_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(p.q), dims, strides, box, estr,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  // Both kernels are programmatic dependents: each may be scheduled while the
+  // one before it drains and waits for its end (griddepcontrol.wait) before it
+  // touches memory.
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(plan.num_parts), NR / 4);
-  cfg.blockDim = dim3(128);
-  cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  cfg.stream = stream;
+  cfg.gridDim = dim3(static_cast<unsigned>(plan.num_parts));
+  cfg.blockDim = dim3(PSmem<NR>::kThreads);
+  cfg.dynamicSmemBytes = PSmem<NR>::kAlloc;
+  e = cudaLaunchKernelEx(&cfg, paged_decode_kernel<NR>, p, plan.groups, q_map);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(static_cast<unsigned>(plan.num_parts), NR / 4);
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, paged_merge_kernel, p, plan.groups, NR);
 }
 
