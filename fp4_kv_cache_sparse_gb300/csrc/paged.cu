@@ -68,9 +68,13 @@ template <int NR>
 struct PSmem {
   static constexpr int kSides = 2;  // softmax threads hold half of the rows each: exponents and sums stay in registers
   static constexpr int kSoftmaxWarps = 4 * kSides;
-  static constexpr int kKWarp0 = kSoftmaxWarps, kVWarp0 = kKWarp0 + 4, kLoadWarp = kVWarp0 + 4;
-  static constexpr int kScoreWarp = kLoadWarp + 1, kValueWarp = kScoreWarp + 1;
-  static constexpr int kThreads = (kValueWarp + 1) * 32;
+  // Decode warps of each kind: eight hide more latency, but with more rows the
+  // softmax needs more registers than 28 warps leave it.
+  static constexpr int kDecodeWarps = NR == 16 ? 8 : 4;
+  static constexpr int kKWarp0 = kSoftmaxWarps, kVWarp0 = kKWarp0 + kDecodeWarps, kLoadWarp = kVWarp0 + kDecodeWarps;
+  static constexpr int kScoreWarp = kLoadWarp + 1, kValueWarp0 = kScoreWarp + 1;
+  static constexpr int kValueWarps = 2;
+  static constexpr int kThreads = (kValueWarp0 + kValueWarps) * 32;
   // Rings: raw pages, K quarters in tensor memory, V units.  A page lives
   // from its load to the end of its V decode, about ten thousand cycles, so
   // the more of them fit the better.
@@ -84,7 +88,7 @@ struct PSmem {
   static constexpr int kPOff = kVOff + kVRing * kVUnitBytes;
   static constexpr int kRawOff = kPOff + kPBytes;
   static constexpr int kBarOff = kRawOff + kRaw * kPageBytes;
-  static constexpr int kNumBars = 2 * kRaw + 2 * kKRing + 2 * kVRing + 6 + 4 + kInfoRing;
+  static constexpr int kNumBars = 2 * kRaw + 2 * kKRing + 2 * kVRing + 8 + 4 + kInfoRing;
   static constexpr int kColOff = (kBarOff + kNumBars * 8 + 15) & ~15;  // per-row arrays
   // float mb[NR], alpha[NR], scale[NR], linv[NR]; int hi[NR], lo[NR]; float red[4][NR]
   static constexpr int kInfoOff = kColOff + 10 * NR * 4;
@@ -95,7 +99,7 @@ struct PSmem {
   // Barrier indices.
   static constexpr int bRawFull = 0, bRawFree = bRawFull + kRaw, bKFull = bRawFree + kRaw, bKFree = bKFull + kKRing,
                        bVFull = bKFree + kKRing, bVFree = bVFull + kVRing, bSFull = bVFree + kVRing,
-                       bSFree = bSFull + 2, bPFull = bSFree + 2, bPFree = bPFull + 1, bQFull = bPFree + 1,
+                       bSFree = bSFull + 2, bPFull = bSFree + 2, bPFree = bPFull + 2, bQFull = bPFree + 2,
                        bOFree = bQFull + 1, bDrain = bOFree + 1, bQRaw = bDrain + 1, bInfo = bQRaw + 1;
   static_assert(bInfo + kInfoRing == kNumBars, "barriers");
   // Tensor memory columns: O^T quarters, S^T buffers, K quarters.
@@ -287,6 +291,26 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
                : "memory");
 }
 
+// Shared memory by 32-bit address.
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
 // Instruction descriptor of kind::f16 with f16 operands and fp32 accumulation.
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn, bool b_mn) {
   return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
@@ -386,10 +410,11 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
                                                                                 const __grid_constant__ CUtensorMap q_map) {
   using L = PSmem<NR>;
   constexpr int NC = NR / L::kSides;    // rows of a softmax thread
+  constexpr bool kKeep = NR == 16;
   constexpr int HC = NR == 16 ? 8 : 16;  // of which it works on so many at a time
   constexpr int kPagedThreads = L::kThreads, kSoftmaxWarps = L::kSoftmaxWarps;
   constexpr int kKWarp0 = L::kKWarp0, kVWarp0 = L::kVWarp0, kLoadWarp = L::kLoadWarp;
-  constexpr int kScoreWarp = L::kScoreWarp, kValueWarp = L::kValueWarp;
+  constexpr int kScoreWarp = L::kScoreWarp, kValueWarp0 = L::kValueWarp0;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem + L::kQOff;
@@ -418,25 +443,25 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
   if (tid == 0) {
     for (int i = 0; i < L::kRaw; ++i) {
       mbar_init(&bars[L::bRawFull + i], 1);
-      mbar_init(&bars[L::bRawFree + i], 6);  // two K warps and the four V warps
+      mbar_init(&bars[L::bRawFree + i], L::kDecodeWarps / 2 + L::kDecodeWarps);  // half of the K warps, all V warps
     }
     for (int i = 0; i < L::kKRing; ++i) {
       mbar_init(&bars[L::bKFull + i], 4);
       mbar_init(&bars[L::bKFree + i], 1);
     }
     for (int i = 0; i < L::kVRing; ++i) {
-      mbar_init(&bars[L::bVFull + i], 1);
+      mbar_init(&bars[L::bVFull + i], L::kDecodeWarps / 4);
       mbar_init(&bars[L::bVFree + i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars[L::bSFull + i], 1);
       mbar_init(&bars[L::bSFree + i], kSoftmaxWarps);
+      mbar_init(&bars[L::bPFull + i], kSoftmaxWarps / 2);  // P^T by halves of the tile's tokens
+      mbar_init(&bars[L::bPFree + i], L::kValueWarps);
     }
-    mbar_init(&bars[L::bPFull], kSoftmaxWarps);
-    mbar_init(&bars[L::bPFree], 1);
     mbar_init(&bars[L::bQFull], kSoftmaxWarps);
     mbar_init(&bars[L::bOFree], kSoftmaxWarps);
-    mbar_init(&bars[L::bDrain], 2);
+    mbar_init(&bars[L::bDrain], 1 + L::kValueWarps);
     mbar_init(&bars[L::bQRaw], 1);
     for (int i = 0; i < kInfoRing; ++i) mbar_init(&bars[L::bInfo + i], 1);
     *abort_flag = 0;
@@ -444,7 +469,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
   }
-  if (warp == kValueWarp) tmem_alloc(tmem_slot, 512);
+  if (warp == kValueWarp0) tmem_alloc(tmem_slot, 512);
 
   // Launched as a programmatic dependent: what comes before this line runs
   // beside the end of the stream's previous kernel, nothing after it does.
@@ -582,42 +607,39 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
       }
     } else if (warp >= kKWarp0 && warp < kVWarp0) {
       // ---------------------------------------------------------------- K: lane = token
-      const int quad = warp & 3;
-      const int row = quad * 32 + lane;
+      // Four warps, one for each quadrant of tensor memory lanes, decode a
+      // 128-dim quarter; of eight, two teams take quarters in turn.  (What
+      // stands in rows past the visible tokens only makes masked scores.)
+      constexpr int kTeams = L::kDecodeWarps / 4, kHalves = kTeams == 2 ? 1 : 2;  // (unrolled: two warps cover less latency)
+      const int quad = warp & 3, team = (warp - kKWarp0) >> 2;
       const uint32_t tK = tmem + (static_cast<uint32_t>(quad * 32) << 16) + L::cK;
-      // Rows are 288 bytes apart: lanes 4..7 of every eight read their two
-      // 16-byte pieces in the other order, which spreads eight lanes over all banks.
-      const bool swap = (lane & 4) != 0;
-      const uint8_t* rows = sRaw + (row & 63) * kRecFp4;
-      const int near = swap ? 16 : 0, far = 16 - near;
+      const uint32_t rows = smem_u32(sRaw) + ((quad & 1) * 32 + lane) * kRecFp4;
       int slot = quad >> 1;  // the warp's page of the tile
       uint32_t raw_parity = 0;
 #pragma unroll 1
       for (uint32_t n = 0; n < items; ++n) {
         wait_for(&bars[L::bRawFull + slot], raw_parity, abort_flag, p.d_error);
-        const uint8_t* rec = rows + slot * kPageBytes;
-        const bool there = token_there(info[n % kInfoRing].x, row);
 #pragma unroll 1
-        for (int qq = 0; qq < 4; ++qq) {
+        for (int qq = team; qq < 4; qq += kTeams) {
           const int ks = qq % L::kKRing;
           const uint32_t parity = (L::kKRing == 4 ? n : static_cast<uint32_t>(qq / L::kKRing)) & 1;
-          const uint8_t* src = rec + qq * 64;
-          uint2 sc = *reinterpret_cast<const uint2*>(rec + 256 + qq * 8);
-          if (!there) sc = make_uint2(0, 0);  // scale 0: the token is all zeros
+          const uint32_t src = rows + slot * kPageBytes + qq * 64;
+          const uint2 sc = lds64(src + 256 - qq * 56);
+          uint4 data[2] = {lds128(src), lds128(src + 16)};
           // A fresh barrier counts as one whose phase 1 is over.
           wait_for(&bars[L::bKFree + ks], parity ^ 1, abort_flag, p.d_error);
           tc_fence_after();
           const uint32_t t = tK + ks * 64;
-#pragma unroll 1
+#pragma unroll kHalves
           for (int hh = 0; hh < 2; ++hh) {
-            const uint4 a = *reinterpret_cast<const uint4*>(src + hh * 32 + near);
-            const uint4 b = *reinterpret_cast<const uint4*>(src + hh * 32 + far);
-            uint32_t o[16];
             const uint32_t s = hh ? sc.y : sc.x;
-            decode32(swap ? b : a, s & 0xFFFFu, o);
+            uint32_t o[16];
+            decode32(data[0], s & 0xFFFFu, o);
             tmem_st16(t + hh * 32, o);
-            decode32(swap ? a : b, s >> 16, o);
+            if (hh == 0) data[0] = lds128(src + 32);
+            decode32(data[1], s >> 16, o);
             tmem_st16(t + hh * 32 + 16, o);
+            if (hh == 0) data[1] = lds128(src + 48);
           }
           tmem_wait_st();
           tc_fence_before();
@@ -629,18 +651,21 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
       }
     } else if (warp >= kVWarp0 && warp < kLoadWarp) {
       // ---------------------------------------------------------------- V: shared memory
-      // A warp owns one dim quarter.  Eight lanes cover four tokens x two
-      // neighbouring 16-byte pieces, which is free of bank conflicts both ways;
-      // the warp covers 8 tokens x 4 pieces at a time.
-      const int qq = warp - kVWarp0;
+      // A warp owns one dim quarter (of eight, two share it, 32 tokens of a
+      // unit each).  Eight lanes cover four tokens x two neighbouring 16-byte
+      // pieces, which is free of bank conflicts both ways; the warp covers 8
+      // tokens x 4 pieces at a time.
+      constexpr int kShare = L::kDecodeWarps / 4;
+      const int qq = (warp - kVWarp0) & 3;
       const int piece = (lane & 1) | ((lane >> 2) & 2);         // 32-dim piece of the quarter
       const int tok = ((lane >> 1) & 3) | ((lane >> 2) & 4);    // token within eight
-      const uint8_t* rows = sRaw + tok * kRecFp4 + qq * 64;
-      uint8_t* rows_v = sV + (piece >> 1) * (kVUnitTokens * 128) + tok * 128;
-      int off[4];  // the lane's four 16-byte units of a 128-byte row, swizzled
+      const int first = ((warp - kVWarp0) >> 2) * 32 + tok;     // this lane's first record of a page
+      const uint32_t rows = smem_u32(sRaw) + first * kRecFp4 + qq * 64 + piece * 16;
+      const int scales = 256 - qq * 56 - piece * 14;            // from there to the scales
+      const uint32_t dst = smem_u32(sV) + qq * kVUnitBytes + (piece >> 1) * (kVUnitTokens * 128) + first * 128;
+      uint32_t off[4];  // the lane's four 16-byte units of a 128-byte row, swizzled
 #pragma unroll
-      for (int j = 0; j < 4; ++j) off[j] = (((piece & 1) * 4 + j) ^ tok) * 16;
-      uint8_t* dst = rows_v + qq * kVUnitBytes;
+      for (int j = 0; j < 4; ++j) off[j] = dst + (((piece & 1) * 4 + j) ^ tok) * 16;
       int slot = 0;
       uint32_t raw_parity = 0;
 #pragma unroll 1
@@ -648,17 +673,16 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           wait_for(&bars[L::bRawFull + slot], raw_parity, abort_flag, p.d_error);
-          const int have = ((info[n % kInfoRing].x >> (8 * half)) & 0xFF) - tok;  // rows of this lane below it are there
-          const uint8_t* rec = rows + slot * kPageBytes;
-          const uint8_t* scl = rec + 256 - qq * 56 + piece * 2;
+          const int have = ((info[n % kInfoRing].x >> (8 * half)) & 0xFF) - first;  // rows of this lane below it are there
+          const uint32_t src = rows + slot * kPageBytes;
 #pragma unroll 1
-          for (int i0 = 0; i0 < 8; i0 += 4) {
+          for (int i0 = 0; i0 < 8 / kShare; i0 += 4) {
             uint4 data[4];
             uint32_t sc[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              data[i] = *reinterpret_cast<const uint4*>(rec + (i0 + i) * 8 * kRecFp4 + piece * 16);
-              sc[i] = *reinterpret_cast<const uint16_t*>(scl + (i0 + i) * 8 * kRecFp4);
+              data[i] = lds128(src + (i0 + i) * 8 * kRecFp4);
+              sc[i] = lds16(src + scales + (i0 + i) * 8 * kRecFp4);
             }
             if (i0 == 0) wait_for(&bars[L::bVFree + qq], half ^ 1, abort_flag, p.d_error);
 #pragma unroll
@@ -667,8 +691,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
               decode32(data[i], (i0 + i) * 8 < have ? sc[i] : 0u, o);
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<uint4*>(dst + (i0 + i) * 1024 + off[j]) =
-                    make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                sts128(off[j] + (i0 + i) * 1024, o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
             }
           }
           fence_proxy_async_smem();
@@ -694,8 +717,8 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
 #pragma unroll 1
         for (int qq = 0; qq < 4; ++qq) {
           const int ks = qq % L::kKRing;
-          wait_for(&bars[L::bKFull + ks], (L::kKRing == 4 ? n : static_cast<uint32_t>(qq / L::kKRing)) & 1, abort_flag,
-                   p.d_error);
+          const uint32_t parity = (L::kKRing == 4 ? n : static_cast<uint32_t>(qq / L::kKRing)) & 1;
+          wait_for(&bars[L::bKFull + ks], parity, abort_flag, p.d_error);
           if (qq == 0 && (info[n % kInfoRing].x & kOpens)) {
             wait_for(&bars[L::bQFull], q_parity, abort_flag, p.d_error);
             q_parity ^= 1;
@@ -711,8 +734,11 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
       }
       commit_one(&bars[L::bDrain]);
       wait_drain(&bars[L::bDrain], p.d_error);
-    } else if (warp == kValueWarp) {
+    } else if (warp >= kValueWarp0) {
       // ---------------------------------------------------------------- O^T += V^T P^T
+      // Two warps, two dim quarters each: what waiting for one costs the other issues through.
+      constexpr int kMine = 4 / L::kValueWarps;
+      const int q0 = (warp - kValueWarp0) * kMine;
       constexpr uint32_t idesc = idesc_f16(128, NR, true, true);
       constexpr uint32_t p_sbo = 8 * 2 * NR;  // eight rows of P^T
       constexpr uint32_t p_swz = NR == 64 ? kSwizzle128 : (NR == 32 ? kSwizzle64 : kSwizzle32);
@@ -723,24 +749,31 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
       uint32_t o_parity = 1;
 #pragma unroll 1
       for (uint32_t n = 0; n < items; ++n) {
-        wait_for(&bars[L::bPFull], n & 1, abort_flag, p.d_error);
-        const bool opens = (info[n % kInfoRing].x & kOpens) != 0;
-        if (opens) {
-          wait_for(&bars[L::bOFree], o_parity, abort_flag, p.d_error);
-          o_parity ^= 1;
-        }
+        bool opens = false;
 #pragma unroll 1
-        for (int v = 0; v < 8; ++v) {
-          const int half = v >> 2, qq = v & 3;
-          wait_for(&bars[L::bVFull + qq], half, abort_flag, p.d_error);
-          tc_fence_after();
-          const uint32_t d = tmem + L::cO + qq * NR, a = v_lo + ((qq * kVUnitBytes) >> 4), b = p_lo + ((half * 8 * p_sbo) >> 4);
+        for (int half = 0; half < 2; ++half) {
+          wait_for(&bars[L::bPFull + half], n & 1, abort_flag, p.d_error);
+          if (half == 0) {
+            opens = (info[n % kInfoRing].x & kOpens) != 0;
+            if (opens) {
+              wait_for(&bars[L::bOFree], o_parity, abort_flag, p.d_error);
+              o_parity ^= 1;
+            }
+          }
+          const uint32_t b = p_lo + ((half * 8 * p_sbo) >> 4);
+#pragma unroll 1
+          for (int qq = q0; qq < q0 + kMine; ++qq) {
+            wait_for(&bars[L::bVFull + qq], half, abort_flag, p.d_error);
+            tc_fence_after();
+            const uint32_t d = tmem + L::cO + qq * NR, a = v_lo + ((qq * kVUnitBytes) >> 4);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mma_f16_ss(d, a + ((j * 2048) >> 4), v_hi, b + ((j * 2 * p_sbo) >> 4), p_hi, idesc, !(opens && v < 4 && j == 0));
-          commit_one(&bars[L::bVFree + qq]);
+            for (int j = 0; j < 4; ++j)
+              mma_f16_ss(d, a + ((j * 2048) >> 4), v_hi, b + ((j * 2 * p_sbo) >> 4), p_hi, idesc,
+                         !(opens && half == 0 && j == 0));
+            commit_one(&bars[L::bVFree + qq]);
+          }
+          commit_one(&bars[L::bPFree + half]);
         }
-        commit_one(&bars[L::bPFree]);
       }
       commit_one(&bars[L::bDrain]);
       wait_drain(&bars[L::bDrain], p.d_error);
@@ -776,14 +809,14 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
           uint4* pb = reinterpret_cast<uint4*>(base + swz<128>(off + 16));
           const uint4 a = *pa, b = *pb;
           uint32_t wv[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-          // The largest exponent of the row (the sign bits shifted out).
-          uint32_t top = 0;
+          // The largest magnitude of the row, two values to a word.
+          uint32_t two = 0;
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             if (r >= t.nrows) wv[k] = 0;
-            top = max(top, max((wv[k] << 17) >> 24, (wv[k] << 1) >> 24));
+            asm("max.u16x2 %0, %0, %1;" : "+r"(two) : "r"(wv[k] & 0x7FFF7FFFu));
           }
-          top = __reduce_max_sync(0xFFFFFFFFu, top);
+          const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, max(two >> 16, two & 0xFFFFu)) >> 7;
           // Largest value to [2^14, 2^15); nothing to scale in a row of zeros or of infinities.
           const int e = top == 0 || top == 255 ? 0 : max(static_cast<int>(top) - 127 - 14, -100);
           const float up = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
@@ -861,16 +894,21 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
           tmem_wait_st();
         }
         float top = -INFINITY;
-#pragma unroll 1
+        float kept[kKeep ? NC : 1];  // with few rows the exponents stay in registers
+#pragma unroll
         for (int h = 0; h < NC; h += HC) {
           float y[HC];
           exponents(s_col, h, y, true);
+          if constexpr (kKeep) {
+#pragma unroll
+            for (int c = 0; c < HC; ++c) kept[h + c] = y[c];
+          }
 #pragma unroll
           for (int c = 0; c < HC; ++c) top = fmaxf(top, y[c]);
         }
         if (any_of(2, kSoftmaxThreads, top > kSlack + kPBias)) {
           // Exact maxima of the tile's rows.
-#pragma unroll 1
+#pragma unroll
           for (int h = 0; h < NC; h += HC) {
             float y[HC];
             exponents(s_col, h, y, false);
@@ -891,13 +929,22 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
             }
             c_alpha[tid] = alpha;
           }
-          if (any_of(2, kSoftmaxThreads, moved)) {
+          const bool any_moved = any_of(2, kSoftmaxThreads, moved);
+          if constexpr (kKeep) {
+#pragma unroll
+            for (int h = 0; h < NC; h += HC) {
+              float y[HC];
+              exponents(s_col, h, y, true);
+#pragma unroll
+              for (int c = 0; c < HC; ++c) kept[h + c] = y[c];
+            }
+          }
+          if (any_moved) {
 #pragma unroll
             for (int c = 0; c < NC; ++c) l[c] *= c_alpha[c0 + c];
             // O^T follows, once the product before this one is complete.
             if (!(it.x & kOpens)) {
-              wait_for(&bars[L::bPFree], (n & 1) ^ 1, abort_flag, p.d_error);
-              __syncwarp();
+              wait_for(&bars[L::bPFree + 1], (n & 1) ^ 1, abort_flag, p.d_error);
               tc_fence_after();
 #pragma unroll 1
               for (int i = side; i < 4 * (NR / 16); i += L::kSides) {
@@ -912,37 +959,40 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
             }
           }
         }
-        // P = 2^y, row `row` of P^T (MN-major), once the last product has read the buffer.
+        // P = 2^y, row `row` of P^T (MN-major); all of it is at hand when the
+        // last product has read this half of the buffer.
+        uint32_t e[NC / 2];
 #pragma unroll
         for (int h = 0; h < NC; h += HC) {
           float y[HC];
-          exponents(s_col, h, y, true);
+          if constexpr (kKeep) {
+#pragma unroll
+            for (int c = 0; c < HC; ++c) y[c] = kept[h + c];
+          } else {
+            exponents(s_col, h, y, true);
+          }
           if (h + HC == NC) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[L::bSFree + (n & 1)]);
           }
-          uint32_t e[HC / 2];
 #pragma unroll
           for (int c = 0; c < HC; c += 2) {
             const float a = ex2_approx(y[c]), b = ex2_approx(y[c + 1]);
             l[h + c] += a;
             l[h + c + 1] += b;
-            e[c / 2] = pack_f16x2(a, b);
+            e[(h + c) / 2] = pack_f16x2(a, b);
           }
-          if (h == 0) {
-            wait_for(&bars[L::bPFree], (n & 1) ^ 1, abort_flag, p.d_error);
-            __syncwarp();
-          }
-#pragma unroll
-          for (int k = 0; k < HC / 8; ++k)
-            *reinterpret_cast<uint4*>(sP + swz<2 * NR>(row * (2 * NR) + (c0 + h) * 2 + k * 16)) =
-                make_uint4(e[4 * k], e[4 * k + 1], e[4 * k + 2], e[4 * k + 3]);
         }
+        wait_for(&bars[L::bPFree + (quad >> 1)], (n & 1) ^ 1, abort_flag, p.d_error);
+#pragma unroll
+        for (int k = 0; k < NC / 8; ++k)
+          *reinterpret_cast<uint4*>(sP + swz<2 * NR>(row * (2 * NR) + c0 * 2 + k * 16)) =
+              make_uint4(e[4 * k], e[4 * k + 1], e[4 * k + 2], e[4 * k + 3]);
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[L::bPFull]);
+        if (lane == 0) mbar_arrive(&bars[L::bPFull + (quad >> 1)]);
         if (!(it.x & kCloses)) continue;
 
         // The piece's end: row sums over the tile's tokens, then O^T / l.
@@ -967,8 +1017,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
         named_bar_sync(1, kSoftmaxThreads);
         // The next unit's Q goes in while the last product runs (this piece's scores are all done).
         if (n + 1 < items) convert_q(min(u + 1, units - 1));
-        wait_for(&bars[L::bPFree], n & 1, abort_flag, p.d_error);
-        __syncwarp();
+        wait_for(&bars[L::bPFree + 1], n & 1, abort_flag, p.d_error);
         tc_fence_after();
         // Lane = dim, columns = rows.
         constexpr int EC = NR == 32 ? 32 : 16;  // columns at a time (registers)
@@ -1015,7 +1064,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kValueWarp) {
+  if (warp == kValueWarp0) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
