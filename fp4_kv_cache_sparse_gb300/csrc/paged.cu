@@ -9,9 +9,10 @@
 //
 // Work.  A unit is one group of up to NR (16, 32 or 64) query rows of one
 // sequence; its items are the 128-token tiles that some row of it sees (the
-// tiles of the sinks and of the window only).  All items in order are cut
-// into gridDim.x equal runs, one per CTA (one CTA per SM); the lengths are on
-// the device, so every CTA derives the cut itself by a scan over the units.
+// tiles of the sinks and of the window only).  All units in order, each a
+// fixed cost and then its items, are cut into gridDim.x runs of equal cost, one
+// per CTA (one CTA per SM); the lengths are on the device, so every CTA derives
+// the cut itself by a scan over the units.
 // A unit cut by a run's end leaves normalised fp32 partials, merged by a
 // second kernel.
 //
@@ -60,13 +61,15 @@ constexpr int kVUnitTokens = 64;
 constexpr int kVUnitBytes = kVUnitTokens * 128 * 2;  // 64 tokens x 128 dims of V, two chunks of 64 dims
 constexpr int kInfoRing = 8;
 constexpr uint64_t kPagedWaitNs = 2000000000ull;  // 2 s per wait
+constexpr int kUnitCost = 2;                 // what a unit's Q and epilogue take, in tiles
 constexpr float kSlack = 8.f;                // the running maximum may lag by 2^8
 constexpr float kPBias = 7.f;                // P of the maximum is 2^7
 constexpr float kNoMax = -3.0e38f;           // running maximum before any visible token
 
 template <int NR>
 struct PSmem {
-  static constexpr int kSides = 2;  // softmax threads hold half of the rows each: exponents and sums stay in registers
+  // A softmax thread holds NR / kSides rows: exponents and sums stay in registers.
+  static constexpr int kSides = NR == 64 ? 4 : 2;
   static constexpr int kSoftmaxWarps = 4 * kSides;
   // Decode warps of each kind: eight hide more latency, but with more rows the
   // softmax needs more registers than 28 warps leave it.
@@ -432,7 +435,8 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
   int4* info = reinterpret_cast<int4*>(smem + L::kInfoOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
-  int* start_u = reinterpret_cast<int*>(smem + L::kMiscOff + 8);    // {unit, items before it}
+  // This part's run: first unit, its item that the run begins with, items; and the cost of every run.
+  int* cut = reinterpret_cast<int*>(smem + L::kMiscOff + 8);
   int* warp_sum = reinterpret_cast<int*>(smem + L::kMiscOff + 32);  // [warps]
 
   const int tid = threadIdx.x;
@@ -465,7 +469,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
     mbar_init(&bars[L::bQRaw], 1);
     for (int i = 0; i < kInfoRing; ++i) mbar_init(&bars[L::bInfo + i], 1);
     *abort_flag = 0;
-    start_u[0] = -1;
+    cut[2] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
   }
@@ -482,7 +486,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
   int mine = 0;
   for (int u = u_a; u < u_b; ++u) {
     bool bad;
-    mine += unit_of<NR>(p, groups, u, bad).tiles;
+    mine += unit_of<NR>(p, groups, u, bad).tiles + kUnitCost;
     if (bad && part == 0 && p.d_error) atomicOr(p.d_error, MLA_DEVERR_BAD_LENGTH);
   }
   int incl = mine;
@@ -501,34 +505,49 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
     if (w < warp) before += v;
     total += v;
   }
-  const int share = (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
-  const int64_t g0_wide = static_cast<int64_t>(part) * share;
-  const int g0 = static_cast<int>(min(g0_wide, static_cast<int64_t>(total)));
-  const int g1 = static_cast<int>(min(g0_wide + share, static_cast<int64_t>(total)));
-  const int excl = before + incl - mine;
-  if (g0 < g1 && excl <= g0 && g0 < excl + mine) {
-    int at = excl, u = u_a;
-    for (;; ++u) {
+  {
+    const int share = (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+    const int64_t from = static_cast<int64_t>(part) * share;
+    const int g0 = static_cast<int>(min(from, static_cast<int64_t>(total)));
+    const int g1 = static_cast<int>(min(from + share, static_cast<int64_t>(total)));
+    // A unit takes kUnitCost, then one for each of its tiles.  The run begins
+    // in the unit whose last tile lies at or past g0; the thread that summed
+    // that unit counts the run's tiles.
+    const int excl = before + incl - mine;
+    if (g0 < g1 && excl <= g0 && g0 < excl + mine) {
+      int at = excl, u = u_a;
       bool bad;
-      const int t = unit_of<NR>(p, groups, u, bad).tiles;
-      if (g0 < at + t) break;
-      at += t;
+      int tiles = unit_of<NR>(p, groups, u, bad).tiles;
+      while (at + kUnitCost + tiles <= g0) {
+        at += kUnitCost + tiles;
+        tiles = unit_of<NR>(p, groups, ++u, bad).tiles;
+      }
+      const int k = max(g0 - at - kUnitCost, 0);
+      cut[0] = u;
+      cut[1] = k;
+      int count = max(min(at + kUnitCost + tiles, g1) - (at + kUnitCost + k), 0);
+      for (at += kUnitCost + tiles; at + kUnitCost < g1; at += kUnitCost + tiles) {
+        tiles = unit_of<NR>(p, groups, ++u, bad).tiles;
+        count += min(at + kUnitCost + tiles, g1) - (at + kUnitCost);
+      }
+      cut[2] = count;
+      cut[3] = share;
     }
-    start_u[0] = u;
-    start_u[1] = at;
   }
   __syncthreads();
   const uint32_t tmem = *tmem_slot;
+  const uint32_t items = static_cast<uint32_t>(cut[2]);
 
-  if (g0 >= g1) {
+  if (items == 0) {
     if (tid == 0) p.ws_info[part * 4] = -1;
   } else {
-    const uint32_t items = static_cast<uint32_t>(g1 - g0);
 
     if (warp == kLoadWarp) {
       // ---------------------------------------------------------------- loader
       // It alone walks the units; the others read what it found.
-      int u = start_u[0], k = g0 - start_u[1];
+      int u = cut[0], k = cut[1];
+      const bool mid = k > 0;  // the run begins inside its first unit
+      const int u_first = u;
       bool bad_len;
       Unit unit = unit_of<NR>(p, groups, u, bad_len);
       int slot = 0;
@@ -564,7 +583,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
         if (n == 0 || k == 0) word |= kOpens;
         if (n + 1 == items || k + 1 == unit.tiles) word |= kCloses;
         // A piece begins with its unit unless the run's first item lies inside the unit.
-        if (!(g0 > start_u[1] && u == start_u[0])) word |= kFromStart;
+        if (!(mid && u == u_first)) word |= kFromStart;
         if (k + 1 == unit.tiles) word |= kToEnd;
 #pragma unroll 1
         for (int j = 0; j < 2; ++j) {
@@ -583,9 +602,9 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
         if (n + 1 == items && lane == 0) {
           // A unit that begins in this part and is cut by its end is merged on
           // this part's behalf: {unit, last part with a piece of it}.
-          const bool merges = k + 1 < unit.tiles && !(g0 > start_u[1] && u == start_u[0]);
+          const bool merges = k + 1 < unit.tiles && !(mid && u == u_first);
           p.ws_info[part * 4] = merges ? u : -1;
-          p.ws_info[part * 4 + 1] = (g1 + (unit.tiles - k - 1) - 1) / share;
+          p.ws_info[part * 4 + 1] = part + (cut[3] - 1 + unit.tiles - k - 1) / cut[3];
         }
         if (++k == unit.tiles && n + 1 < items) {
           k = 0;
@@ -663,9 +682,8 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
       const uint32_t rows = smem_u32(sRaw) + first * kRecFp4 + qq * 64 + piece * 16;
       const int scales = 256 - qq * 56 - piece * 14;            // from there to the scales
       const uint32_t dst = smem_u32(sV) + qq * kVUnitBytes + (piece >> 1) * (kVUnitTokens * 128) + first * 128;
-      uint32_t off[4];  // the lane's four 16-byte units of a 128-byte row, swizzled
-#pragma unroll
-      for (int j = 0; j < 4; ++j) off[j] = dst + (((piece & 1) * 4 + j) ^ tok) * 16;
+      // The lane's first 16-byte unit of a 128-byte row, swizzled; unit j is at this ^ 16 j.
+      const uint32_t unit0 = dst + (((piece & 1) * 4) ^ tok) * 16;
       int slot = 0;
       uint32_t raw_parity = 0;
 #pragma unroll 1
@@ -691,7 +709,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
               decode32(data[i], (i0 + i) * 8 < have ? sc[i] : 0u, o);
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                sts128(off[j] + (i0 + i) * 1024, o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                sts128((unit0 ^ (16 * j)) + (i0 + i) * 1024, o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
             }
           }
           fence_proxy_async_smem();
@@ -797,12 +815,13 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
       // 16 dims); rows past the unit's become zeros.
       uint32_t q_parity = 0;
       const auto convert_q = [&](int u) {
+        constexpr int kRowsAtOnce = NR == 16 ? 2 : 1;  // (registers)
         bool bad_len;
         const Unit t = unit_of<NR>(p, groups, u, bad_len);
         wait_for(&bars[L::bQRaw], q_parity, abort_flag, p.d_error);
         q_parity ^= 1;
         uint8_t* base = sQ + (lane >> 2) * (NR * 128);
-#pragma unroll 2
+#pragma unroll kRowsAtOnce
         for (int r = warp; r < NR; r += kSoftmaxWarps) {
           const uint32_t off = r * 128 + (lane & 3) * 32;
           uint4* pa = reinterpret_cast<uint4*>(base + swz<128>(off));
@@ -859,8 +878,8 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
         }
       };
 
-      if (tid == 0) request_q(start_u[0]);
-      convert_q(start_u[0]);
+      if (tid == 0) request_q(cut[0]);
+      convert_q(cut[0]);
       float l[NC];
 #pragma unroll 1
       for (uint32_t n = 0; n < items; ++n) {
