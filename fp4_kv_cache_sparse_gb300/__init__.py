@@ -274,33 +274,44 @@ def decode(q, kv, indices, extra_kv=None, extra_indices=None, sm_scale=None):
 # ---------------------------------------------------------------------------
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or (lambda: torch.cuda.current_device())
+
+
 def _device_of(t, what):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what}: expected a torch.Tensor")
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{what}: tensor must be on a CUDA device (no CPU path)")
-    return t.get_device()
+    return dev
 
 
-def _arg(t, dev, dtype, what, shape=None):
-    """Address of a dense tensor of this type (and shape) on device dev; None stays None."""
-    if t is None:
-        return None
+def _refuse(t, dev, dtype, what, shape):
     if _device_of(t, what) != dev:
         raise ValueError(f"{what}: all tensors of a call must be on one device")
     if t.dtype is not dtype:
         raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what}: tensor must be contiguous")
+    raise ValueError(f"{what}: tensor must be contiguous")
+
+
+def _arg(t, dev, dtype, what, shape=None):
+    """Address of a dense tensor of this type (and shape) on device dev; None stays None."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not dtype or (
+            shape is not None and t.shape != shape) or not t.is_contiguous():
+        _refuse(t, dev, dtype, what, shape)
     return t.data_ptr()
 
 
 def _call(fn, what, dev, stream, *args):
     """fn(*args, stream) on device dev."""
-    raw = stream.cuda_stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
-    if dev == torch.cuda.current_device():
+    raw = stream.cuda_stream if stream is not None else _raw_stream(dev)
+    if dev == _current_device():
         status = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
@@ -418,10 +429,8 @@ def _rows(t, dev, dtype, what, shape):
     """Address and row stride of a [n, d] tensor whose rows are dense."""
     if t is None:
         return None, 0
-    if _device_of(t, what) != dev:
-        raise ValueError(f"{what}: all tensors of a call must be on one device")
-    if t.dtype is not dtype or t.shape != shape:
-        raise ValueError(f"{what}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not dtype or t.shape != shape:
+        _refuse(t, dev, dtype, what, shape)
     s0, s1 = t.stride()
     if s1 != 1 and shape[1] > 1:
         raise ValueError(f"{what}: rows must be dense")

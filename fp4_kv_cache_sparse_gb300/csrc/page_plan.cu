@@ -1,13 +1,16 @@
 // page_plan.cu -- block tables and slot maps from request lengths, on the
 // device (include/mla.h, mla_page_plan).
 //
-// One cluster of eight CTAs does the whole call.  Every CTA scans all requests
+// One cluster of eight CTAs changes the state.  Every CTA scans all requests
 // (three prefix sums: new tokens, pages taken, pages given back) into its own
 // shared memory, so nothing but one cluster barrier stands between reading the
 // old state and writing the new one in place: before it the ended requests'
-// pages are pushed, after it pages are popped, lengths replaced and the slot
-// map written by all 8192 threads, each finding its tokens' request by a
-// binary search of the prefix in shared memory.
+// pages are pushed, after it pages are popped and lengths replaced.  A short
+// slot map is written by the same 8192 threads, each finding its tokens'
+// request by a binary search of the prefix in shared memory; a long one by a
+// second kernel over the whole GPU, from the tables and lengths that the first
+// has left (512,000 slots: 18 us in the cluster, 6 us so; at 16,384 the second
+// launch costs what it saves).
 #include <cstdint>
 
 #include "mla_device.cuh"
@@ -19,6 +22,7 @@ namespace {
 
 constexpr int kCtas = 8;
 constexpr int kPlanThreads = 1024;
+constexpr int kLongMap = 16384;  // slots from which a kernel of its own writes the map
 
 struct Sums {
   int64_t tokens, take, give;
@@ -56,11 +60,74 @@ __device__ __forceinline__ Sums block_scan(Sums v, Sums* warp_sums, Sums& total)
 
 __device__ __forceinline__ int32_t pages_of(uint32_t tokens) { return static_cast<int32_t>((tokens + 63u) >> 6); }
 
+// The last request that starts at or before token i < prefix[batch].
+__device__ __forceinline__ int request_of(const int32_t* prefix, int batch, int32_t i) {
+  int lo = 0, hi = batch;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (prefix[mid] <= i)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ void store_four(int32_t* slots, int32_t* positions, int64_t i0, int max_new,
+                                           const int32_t (&slot)[4], const int32_t (&pos)[4]) {
+  if (i0 + 4 <= max_new && ((reinterpret_cast<uintptr_t>(slots) | reinterpret_cast<uintptr_t>(positions)) & 15u) == 0) {
+    *reinterpret_cast<int4*>(slots + i0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+    *reinterpret_cast<int4*>(positions + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (i0 + k < max_new) {
+        slots[i0 + k] = slot[k];
+        positions[i0 + k] = pos[k];
+      }
+    }
+  }
+}
+
+// The slot map of a plan that has been made: request r's new tokens stand at
+// the end of its new length, and its row holds every page.
+__global__ void __launch_bounds__(256) slot_map_kernel(const int32_t* __restrict__ cu_new,
+                                                       const int32_t* __restrict__ seq_lens, int batch,
+                                                       const int32_t* __restrict__ block_table, int max_pages,
+                                                       int num_pages, int32_t* __restrict__ slots,
+                                                       int32_t* __restrict__ positions, int max_new, int32_t* d_error) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int32_t tokens = cu_new[batch];
+  const int64_t i0 = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (i0 >= max_new) return;
+  int32_t slot[4], pos[4];
+  bool bad_page = false;
+  int r = i0 < tokens ? request_of(cu_new, batch, static_cast<int32_t>(i0)) : 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int64_t i = i0 + k;
+    slot[k] = -1;
+    pos[k] = 0;
+    if (i < tokens) {
+      while (i >= cu_new[r + 1]) ++r;
+      const int32_t p = seq_lens[r] - (cu_new[r + 1] - static_cast<int32_t>(i));
+      const int32_t page = block_table[static_cast<int64_t>(r) * max_pages + (p >> 6)];
+      const bool good = page >= 0 && page < num_pages;
+      bad_page |= !good;
+      slot[k] = good ? page * 64 + (p & 63) : -1;
+      pos[k] = p;
+    }
+  }
+  store_four(slots, positions, i0, max_new, slot, pos);
+  if (bad_page && d_error) atomicOr(d_error, MLA_DEVERR_BAD_INDEX);
+}
+
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kPlanThreads)
     page_plan_kernel(const int32_t* cached_lens, const int32_t* __restrict__ new_lens, int batch,
                      int32_t* __restrict__ block_table, int max_pages, int32_t* free_pages, int num_pages,
                      const int32_t* num_free, int32_t* seq_lens, int32_t* num_free_out, int32_t* __restrict__ cu_new,
-                     int32_t* __restrict__ slots, int32_t* __restrict__ positions, int max_new, int32_t* d_error) {
+                     int32_t* __restrict__ slots, int32_t* __restrict__ positions, int max_new, int map_len,
+                     int32_t* d_error) {
   extern __shared__ int32_t sm[];
   int32_t* s_cu = sm;                    // [batch + 1] first new token
   int32_t* s_take = s_cu + batch + 1;    // [batch + 1] pages taken before this request
@@ -152,21 +219,10 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kPlanThreads)
     if (why && d_error) atomicOr(d_error, why);
   }
 
-  // Slots and positions, four tokens to a thread.
-  for (int64_t i0 = static_cast<int64_t>(gtid) * 4; i0 < max_new; i0 += static_cast<int64_t>(kAll) * 4) {
+  // Slots and positions, four tokens to a thread (none here when the map is long).
+  for (int64_t i0 = static_cast<int64_t>(gtid) * 4; i0 < map_len; i0 += static_cast<int64_t>(kAll) * 4) {
     int32_t slot[4], pos[4];
-    int r = 0;
-    if (i0 < tokens) {  // the last request that starts at or before i0
-      int lo = 0, hi = batch;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (s_cu[mid] <= i0)
-          lo = mid;
-        else
-          hi = mid;
-      }
-      r = lo;
-    }
+    int r = i0 < tokens ? request_of(s_cu, batch, static_cast<int32_t>(i0)) : 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int64_t i = i0 + k;
@@ -184,18 +240,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kPlanThreads)
         pos[k] = p;
       }
     }
-    if (i0 + 4 <= max_new && ((reinterpret_cast<uintptr_t>(slots) | reinterpret_cast<uintptr_t>(positions)) & 15u) == 0) {
-      *reinterpret_cast<int4*>(slots + i0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
-      *reinterpret_cast<int4*>(positions + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (i0 + k < max_new) {
-          slots[i0 + k] = slot[k];
-          positions[i0 + k] = pos[k];
-        }
-      }
-    }
+    store_four(slots, positions, i0, max_new, slot, pos);
   }
   if (bad_page && d_error) atomicOr(d_error, MLA_DEVERR_BAD_INDEX);
 }
@@ -211,10 +256,24 @@ cudaError_t launch_page_plan(const int32_t* cached_lens, const int32_t* new_lens
   const cudaError_t e = max_dynamic_smem_once(configured, reinterpret_cast<const void*>(page_plan_kernel), kMost);
   if (e != cudaSuccess) return e;
   const size_t smem = (4 * static_cast<size_t>(batch) + 3) * sizeof(int32_t);
-  page_plan_kernel<<<kCtas, kPlanThreads, smem, stream>>>(cached_lens, new_lens, batch, block_table, max_pages,
-                                                          free_pages, num_pages, num_free, seq_lens, num_free_out,
-                                                          cu_new, slots, positions, max_new, d_error);
-  return cudaGetLastError();
+  const bool long_map = max_new > kLongMap;
+  page_plan_kernel<<<kCtas, kPlanThreads, smem, stream>>>(
+      cached_lens, new_lens, batch, block_table, max_pages, free_pages, num_pages, num_free, seq_lens, num_free_out,
+      cu_new, slots, positions, max_new, long_map ? 0 : max_new, d_error);
+  cudaError_t launched = cudaGetLastError();
+  if (launched != cudaSuccess || !long_map) return launched;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(max_new) + 1023) / 1024));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, slot_map_kernel, static_cast<const int32_t*>(cu_new),
+                            static_cast<const int32_t*>(seq_lens), batch, static_cast<const int32_t*>(block_table),
+                            max_pages, num_pages, slots, positions, max_new, d_error);
 }
 
 }  // namespace mla

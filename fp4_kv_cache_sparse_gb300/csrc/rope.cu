@@ -23,6 +23,7 @@ namespace mla {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kAtOnce = 2;  // heads whose loads are in flight together
 
 template <typename T>
 __device__ __forceinline__ float to_f32(T v);
@@ -43,7 +44,7 @@ __device__ __forceinline__ __nv_bfloat16 from_f32(float v) { return __float2bflo
 
 // VE consecutive elements: one 16-byte access, or element by element.
 template <typename T, int VE>
-struct Piece {
+struct alignas(VE * sizeof(T) == 16 ? 16 : sizeof(T)) Piece {
   T v[VE];
   __device__ __forceinline__ void load(const T* p) {
     if constexpr (VE * sizeof(T) == 16) {
@@ -65,8 +66,8 @@ struct Piece {
 
 struct RopeGeometry {
   int rot_cols;    // columns of a head that turn
-  int cols;        // all columns of a head (rot_cols when in place)
-  int runs;        // head runs of a token
+  uint32_t cols;   // all columns of a head (rot_cols when in place)
+  uint32_t runs;   // head runs of a token
   int heads_per;   // heads of a run
   int64_t units;   // n * runs
 };
@@ -78,28 +79,54 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, 
   const int pairs = table.rope_dim / 2;
   for (int j = threadIdx.x; j < pairs; j += kRopeThreads) step[j] = table.step[j];
   __syncthreads();
-  constexpr int kPairs = kHalf ? VE : VE / 2;                // pairs of a column
-  constexpr int kCopy = VE * sizeof(T) == 16 ? VE : 1;       // elements of a copied column
+  constexpr int kPairs = kHalf ? VE : VE / 2;           // pairs of a column
+  constexpr int kCopy = VE * sizeof(T) == 16 ? VE : 1;  // elements of a copied column
+  constexpr int kParts = kHalf ? 2 : 1;                 // pieces of a column
   const int64_t items = g.units * g.cols;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kRopeThreads;
   for (int64_t it = static_cast<int64_t>(blockIdx.x) * kRopeThreads + threadIdx.x; it < items; it += stride) {
-    const int64_t unit = it / g.cols;
-    const int col = static_cast<int>(it - unit * g.cols);
-    const int64_t token = unit / g.runs;
-    const int h0 = static_cast<int>(unit - token * g.runs) * g.heads_per;
-    const int h1 = min(p.heads, h0 + g.heads_per);
+    int64_t token;
+    int col, run;
+    if (items < (int64_t(1) << 31)) {
+      const uint32_t unit = static_cast<uint32_t>(it) / g.cols, t = unit / g.runs;
+      col = static_cast<uint32_t>(it) - unit * g.cols;
+      run = unit - t * g.runs;
+      token = t;
+    } else {
+      const int64_t unit = it / g.cols;
+      col = static_cast<int>(it - unit * g.cols);
+      token = unit / g.runs;
+      run = static_cast<int>(unit - token * g.runs);
+    }
+    const int h0 = run * g.heads_per;
+    int left = min(p.heads - h0, g.heads_per);
     const T* x = static_cast<const T*>(p.x) + token * p.x_row + h0 * p.x_head;
     T* y = static_cast<T*>(p.y) + token * p.y_row + h0 * p.y_head;
     if (col >= g.rot_cols) {  // a piece that is only copied
       int e = (col - g.rot_cols) * kCopy;
       if (e >= p.offset) e += table.rope_dim;
-      for (int h = h0; h < h1; ++h, x += p.x_head, y += p.y_head) {
+      for (; left > 0; --left, x += p.x_head, y += p.y_head) {
         Piece<T, kCopy> v;
         v.load(x + e);
         v.store(y + e);
       }
       continue;
     }
+    x += p.offset + col * VE;
+    y += p.offset + col * VE;
+    // The first heads are on their way while the sines are computed, the next
+    // ones while these are turned.
+    Piece<T, VE> next[kAtOnce][kParts];
+    const auto fetch = [&](const T* from, int n) {
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        if (u < n) {
+          next[u][0].load(from + u * p.x_head);
+          if constexpr (kHalf) next[u][1].load(from + u * p.x_head + pairs);
+        }
+      }
+    };
+    fetch(x, left);
     const int64_t pos = p.positions[token];
     float cs[kPairs], sn[kPairs];
 #pragma unroll
@@ -111,30 +138,38 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, 
       cs[k] = c * table.factor;
       sn[k] = (p.conjugate ? -s : s) * table.factor;
     }
-    const int e = p.offset + col * VE;
-    for (int h = h0; h < h1; ++h, x += p.x_head, y += p.y_head) {
-      if constexpr (kHalf) {
-        Piece<T, VE> a, b;
-        a.load(x + e);
-        b.load(x + e + pairs);
+    for (; left > 0; left -= kAtOnce, y += kAtOnce * p.y_head) {
+      Piece<T, VE> now[kAtOnce][kParts];
 #pragma unroll
-        for (int k = 0; k < VE; ++k) {
-          const float u = to_f32(a.v[k]), w = to_f32(b.v[k]);
-          a.v[k] = from_f32<T>(fmaf(u, cs[k], -w * sn[k]));
-          b.v[k] = from_f32<T>(fmaf(w, cs[k], u * sn[k]));
-        }
-        a.store(y + e);
-        b.store(y + e + pairs);
-      } else {
-        Piece<T, VE> a;
-        a.load(x + e);
+      for (int u = 0; u < kAtOnce; ++u) {
 #pragma unroll
-        for (int k = 0; k < kPairs; ++k) {
-          const float u = to_f32(a.v[2 * k]), w = to_f32(a.v[2 * k + 1]);
-          a.v[2 * k] = from_f32<T>(fmaf(u, cs[k], -w * sn[k]));
-          a.v[2 * k + 1] = from_f32<T>(fmaf(w, cs[k], u * sn[k]));
+        for (int q = 0; q < kParts; ++q) now[u][q] = next[u][q];
+      }
+      x += kAtOnce * p.x_head;
+      fetch(x, left - kAtOnce);
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        if (u >= left) break;
+        if constexpr (kHalf) {
+          Piece<T, VE> &a = now[u][0], &b = now[u][1];
+#pragma unroll
+          for (int k = 0; k < VE; ++k) {
+            const float v = to_f32(a.v[k]), w = to_f32(b.v[k]);
+            a.v[k] = from_f32<T>(fmaf(v, cs[k], -w * sn[k]));
+            b.v[k] = from_f32<T>(fmaf(w, cs[k], v * sn[k]));
+          }
+          a.store(y + u * p.y_head);
+          b.store(y + u * p.y_head + pairs);
+        } else {
+          Piece<T, VE>& a = now[u][0];
+#pragma unroll
+          for (int k = 0; k < kPairs; ++k) {
+            const float v = to_f32(a.v[2 * k]), w = to_f32(a.v[2 * k + 1]);
+            a.v[2 * k] = from_f32<T>(fmaf(v, cs[k], -w * sn[k]));
+            a.v[2 * k + 1] = from_f32<T>(fmaf(w, cs[k], v * sn[k]));
+          }
+          a.store(y + u * p.y_head);
         }
-        a.store(y + e);
       }
     }
   }
