@@ -140,6 +140,7 @@ struct PagedParams {
   int32_t* d_error;            // nullable
   int batch, s, h, rows;       // rows = s * h query rows of a sequence
   int max_pages, window, sinks;
+  bool info_by_unit;           // ws_info has an entry for each unit, not for each part
   int64_t num_pages;
   float scale_log2;            // sm_scale * log2(e)
 };

@@ -105,6 +105,18 @@ struct PSmem {
                        bSFree = bSFull + 2, bPFull = bSFree + 2, bPFree = bPFull + 2, bQFull = bPFree + 2,
                        bOFree = bQFull + 1, bDrain = bOFree + 1, bQRaw = bDrain + 1, bInfo = bQRaw + 1;
   static_assert(bInfo + kInfoRing == kNumBars, "barriers");
+  // How many arrivals complete a phase of barrier i.
+  __device__ static int arrivals(int i) {
+    if (i >= bRawFree && i < bKFull) return kDecodeWarps / 2 + kDecodeWarps;  // half of the K warps, all V warps
+    if (i >= bKFull && i < bKFree) return 4;
+    if (i >= bVFull && i < bVFree) return kDecodeWarps / 4;
+    if (i >= bSFree && i < bPFull) return kSoftmaxWarps;
+    if (i >= bPFull && i < bPFree) return kSoftmaxWarps / 2;  // P^T goes by halves of the tile's tokens
+    if (i >= bPFree && i < bQFull) return kValueWarps;
+    if (i == bQFull || i == bOFree) return kSoftmaxWarps;
+    if (i == bDrain) return 1 + kValueWarps;
+    return 1;
+  }
   // Tensor memory columns: O^T quarters, S^T buffers, K quarters.
   static constexpr int cO = 0, cS = 4 * NR, cK = 6 * NR;
   static_assert(cK + kKRing * 64 <= 512, "tensor memory");
@@ -444,32 +456,12 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
   const int lane = tid & 31;
   const int part = blockIdx.x;
 
+  if (tid < L::kNumBars) mbar_init(&bars[tid], L::arrivals(tid));
   if (tid == 0) {
-    for (int i = 0; i < L::kRaw; ++i) {
-      mbar_init(&bars[L::bRawFull + i], 1);
-      mbar_init(&bars[L::bRawFree + i], L::kDecodeWarps / 2 + L::kDecodeWarps);  // half of the K warps, all V warps
-    }
-    for (int i = 0; i < L::kKRing; ++i) {
-      mbar_init(&bars[L::bKFull + i], 4);
-      mbar_init(&bars[L::bKFree + i], 1);
-    }
-    for (int i = 0; i < L::kVRing; ++i) {
-      mbar_init(&bars[L::bVFull + i], L::kDecodeWarps / 4);
-      mbar_init(&bars[L::bVFree + i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars[L::bSFull + i], 1);
-      mbar_init(&bars[L::bSFree + i], kSoftmaxWarps);
-      mbar_init(&bars[L::bPFull + i], kSoftmaxWarps / 2);  // P^T by halves of the tile's tokens
-      mbar_init(&bars[L::bPFree + i], L::kValueWarps);
-    }
-    mbar_init(&bars[L::bQFull], kSoftmaxWarps);
-    mbar_init(&bars[L::bOFree], kSoftmaxWarps);
-    mbar_init(&bars[L::bDrain], 1 + L::kValueWarps);
-    mbar_init(&bars[L::bQRaw], 1);
-    for (int i = 0; i < kInfoRing; ++i) mbar_init(&bars[L::bInfo + i], 1);
     *abort_flag = 0;
     cut[2] = 0;
+  }
+  if (tid < L::kNumBars) {
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
   }
@@ -539,7 +531,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
   const uint32_t items = static_cast<uint32_t>(cut[2]);
 
   if (items == 0) {
-    if (tid == 0) p.ws_info[part * 4] = -1;
+    if (tid == 0 && !p.info_by_unit) p.ws_info[part * 4] = -1;
   } else {
 
     if (warp == kLoadWarp) {
@@ -599,12 +591,17 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
           }
           if (++slot == L::kRaw) slot = 0, parity ^= 1;
         }
-        if (n + 1 == items && lane == 0) {
-          // A unit that begins in this part and is cut by its end is merged on
-          // this part's behalf: {unit, last part with a piece of it}.
-          const bool merges = k + 1 < unit.tiles && !(mid && u == u_first);
-          p.ws_info[part * 4] = merges ? u : -1;
-          p.ws_info[part * 4 + 1] = part + (cut[3] - 1 + unit.tiles - k - 1) / cut[3];
+        if ((word & (kCloses | kFromStart)) == (kCloses | kFromStart) && lane == 0) {
+          // What the merge does about this unit, which begins here: nothing, or
+          // join the pieces of parts `part` .. last when this part's end cuts it.
+          const bool merges = k + 1 < unit.tiles;
+          const int last = part + (cut[3] - 1 + unit.tiles - k - 1) / cut[3];
+          if (p.info_by_unit)
+            *reinterpret_cast<int4*>(p.ws_info + u * 4) = make_int4(merges ? u : -1, part, last, 0);
+          else if (n + 1 == items)
+            *reinterpret_cast<int4*>(p.ws_info + part * 4) = make_int4(merges ? u : -1, part, last, 0);
+        } else if (n + 1 == items && lane == 0 && !p.info_by_unit) {
+          p.ws_info[part * 4] = -1;
         }
         if (++k == unit.tiles && n + 1 < items) {
           k = 0;
@@ -1090,59 +1087,115 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
 }
 
 // Merge of a unit cut by parts: pieces with normalised outputs o_i and
-// log-sum-exps L_i give L = ln sum exp L_i and sum exp(L_i - L) o_i.  One warp
-// per row, a block of four rows per part and row group.
-__global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p, const int groups, const int nr) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int part = blockIdx.x, lane = threadIdx.x & 31;
-  const int r = static_cast<int>(blockIdx.y) * 4 + (threadIdx.x >> 5);
-  const int u = p.ws_info[part * 4];
-  if (u < 0) return;
-  const int last = p.ws_info[part * 4 + 1];
-  const int b = u / groups, row0 = (u - b * groups) * nr;
-  if (r >= nr || row0 + r >= p.rows) return;
-  // Piece 0 is this part's slot 2 part + 1, piece i part + i's slot 2 (part + i).
-  const int pieces = last - part + 1;
-  const auto prow = [&](int i) { return (static_cast<int64_t>(part + i) * 2 + (i == 0 ? 1 : 0)) * nr + r; };
-  float m = -INFINITY;
-  for (int i = lane; i < pieces; i += 32) m = fmaxf(m, p.ws_lse[prow(i)]);
+// log-sum-exps L_i give L = ln sum exp L_i and sum exp(L_i - L) o_i.  An entry
+// of the info table (a part's last unit, or a unit) names the parts that hold
+// pieces.  Per row kThreads threads, each with 512 / kThreads dims: a warp where
+// units have two or three pieces (blocks of four rows: many rows, each a short
+// chain of loads), four groups of 128 threads that share a row's pieces where
+// few units are cut into many.
+struct Pieces {
+  int part, count, r, nr;
+  // Piece 0 is the first part's slot 2 part + 1, piece i part + i's slot 2 (part + i).
+  __device__ __forceinline__ int64_t row(int i) const {
+    return (static_cast<int64_t>(part + i) * 2 + (i == 0 ? 1 : 0)) * nr + r;
+  }
+};
+// The pieces' largest log-sum-exp (0 if all are empty) and the sum of their weights.
+__device__ __forceinline__ float piece_weights(const PagedParams& p, const Pieces& q, float& m) {
+  const int lane = threadIdx.x & 31;
+  m = -INFINITY;
+  for (int i = lane; i < q.count; i += 32) m = fmaxf(m, p.ws_lse[q.row(i)]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  const float mu = m == -INFINITY ? 0.f : m;
+  if (m == -INFINITY) m = 0.f;
   float z = 0.f;
-  for (int i = lane; i < pieces; i += 32) z += expf(p.ws_lse[prow(i)] - mu);
+  for (int i = lane; i < q.count; i += 32) z += expf(p.ws_lse[q.row(i)] - m);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
+  return z;
+}
+__device__ __forceinline__ void add_piece(float4& acc, float w, const float4& v) {
+  acc.x = fmaf(w, v.x, acc.x);
+  acc.y = fmaf(w, v.y, acc.y);
+  acc.z = fmaf(w, v.z, acc.z);
+  acc.w = fmaf(w, v.w, acc.w);
+}
+__device__ __forceinline__ uint2 four_bf16(const float4& v) {
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
+
+__global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p, const int groups, const int nr) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4 entry = *reinterpret_cast<const int4*>(p.ws_info + blockIdx.x * 4);
+  const int lane = threadIdx.x & 31;
+  const int r = static_cast<int>(blockIdx.y) * 4 + (threadIdx.x >> 5);
+  if (entry.x < 0) return;
+  const int b = entry.x / groups, row0 = (entry.x - b * groups) * nr;
+  if (row0 + r >= p.rows) return;
+  const Pieces q{entry.y, entry.z - entry.y + 1, r, nr};
+  float m;
+  const float z = piece_weights(p, q, m);
   const float inv = z > 0.f ? 1.f / z : 0.f;
   float4 acc[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = 0; i < pieces; ++i) {
-    const int64_t pr = prow(i);
-    const float wgt = expf(p.ws_lse[pr] - mu) * inv;
+#pragma unroll 2
+  for (int i = 0; i < q.count; ++i) {
+    const int64_t pr = q.row(i);
     const float4* src = reinterpret_cast<const float4*>(p.ws_o + pr * kD);
+    float4 v[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float4 v = src[k * 32 + lane];
-      acc[k].x = fmaf(wgt, v.x, acc[k].x);
-      acc[k].y = fmaf(wgt, v.y, acc[k].y);
-      acc[k].z = fmaf(wgt, v.z, acc[k].z);
-      acc[k].w = fmaf(wgt, v.w, acc[k].w);
-    }
+    for (int k = 0; k < 4; ++k) v[k] = src[k * 32 + lane];
+    const float w = expf(p.ws_lse[pr] - m) * inv;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) add_piece(acc[k], w, v[k]);
   }
   const int64_t row = static_cast<int64_t>(b) * p.rows + row0 + r;
   uint2* dst = reinterpret_cast<uint2*>(p.out + row * kD);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(acc[k].x, acc[k].y), c = __floats2bfloat162_rn(acc[k].z, acc[k].w);
-    dst[k * 32 + lane] =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&c));
-  }
+  for (int k = 0; k < 4; ++k) dst[k * 32 + lane] = four_bf16(acc[k]);
   if (lane == 0) p.lse[row] = z > 0.f ? m + logf(z) : -INFINITY;
 }
 
+__global__ void __launch_bounds__(512) paged_merge_many_kernel(const PagedParams p, const int groups, const int nr) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  __shared__ float4 sums[3][128];
+  const int4 entry = *reinterpret_cast<const int4*>(p.ws_info + blockIdx.x * 4);
+  const int r = blockIdx.y, group = threadIdx.x >> 7, tid = threadIdx.x & 127;
+  if (entry.x < 0) return;
+  const int b = entry.x / groups, row0 = (entry.x - b * groups) * nr;
+  if (row0 + r >= p.rows) return;
+  const Pieces q{entry.y, entry.z - entry.y + 1, r, nr};
+  float m;
+  const float z = piece_weights(p, q, m);
+  const float inv = z > 0.f ? 1.f / z : 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = group; i < q.count; i += 16) {  // four of the group's pieces in flight
+    float4 v[4];
+    float w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t pr = q.row(min(i + 4 * j, q.count - 1));
+      v[j] = *reinterpret_cast<const float4*>(p.ws_o + pr * kD + tid * 4);
+      w[j] = i + 4 * j < q.count ? p.ws_lse[pr] : -INFINITY;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) add_piece(acc, expf(w[j] - m) * inv, v[j]);
+  }
+  if (group > 0) sums[group - 1][tid] = acc;
+  __syncthreads();
+  if (group > 0) return;
+#pragma unroll
+  for (int g = 0; g < 3; ++g) add_piece(acc, 1.f, sums[g][tid]);
+  const int64_t row = static_cast<int64_t>(b) * p.rows + row0 + r;
+  *reinterpret_cast<uint2*>(p.out + row * kD + tid * 4) = four_bf16(acc);
+  if (tid == 0) p.lse[row] = z > 0.f ? m + logf(z) : -INFINITY;
+}
+
 template <int NR>
-cudaError_t launch(const PagedParams& p, const PagedPlan& plan, cudaStream_t stream) {
+cudaError_t launch(PagedParams p, const PagedPlan& plan, cudaStream_t stream) {
+  p.info_by_unit = static_cast<int64_t>(p.batch) * plan.groups <= plan.num_parts;
   static std::atomic<uint64_t> configured{0};
   cudaError_t e = max_dynamic_smem_once(configured, reinterpret_cast<const void*>(paged_decode_kernel<NR>),
                                         PSmem<NR>::kAlloc);
@@ -1174,10 +1227,13 @@ cudaError_t launch(const PagedParams& p, const PagedPlan& plan, cudaStream_t str
   cfg.dynamicSmemBytes = PSmem<NR>::kAlloc;
   e = cudaLaunchKernelEx(&cfg, paged_decode_kernel<NR>, p, plan.groups, q_map);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>(plan.num_parts), NR / 4);
-  cfg.blockDim = dim3(128);
+  // Units that are few against the parts are cut into many pieces.
+  const int units = p.batch * plan.groups;
+  const bool many = units * 4 <= plan.num_parts;
+  cfg.gridDim = dim3(static_cast<unsigned>(p.info_by_unit ? units : plan.num_parts), many ? NR : NR / 4);
+  cfg.blockDim = dim3(many ? 512 : 128);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, paged_merge_kernel, p, plan.groups, NR);
+  return cudaLaunchKernelEx(&cfg, many ? paged_merge_many_kernel : paged_merge_kernel, p, plan.groups, NR);
 }
 
 }  // namespace
