@@ -57,8 +57,6 @@ namespace mla {
 namespace {
 
 constexpr int kPageBytes = kPage * kRecFp4;
-constexpr int kVUnitTokens = 64;
-constexpr int kVUnitBytes = kVUnitTokens * 128 * 2;  // 64 tokens x 128 dims of V, two chunks of 64 dims
 constexpr int kInfoRing = 8;
 constexpr uint64_t kPagedWaitNs = 2000000000ull;  // 2 s per wait
 constexpr int kUnitCost = 2;                 // what a unit's Q and epilogue take, in tiles
@@ -78,12 +76,18 @@ struct PSmem {
   static constexpr int kScoreWarp = kLoadWarp + 1, kValueWarp0 = kScoreWarp + 1;
   static constexpr int kValueWarps = 2;
   static constexpr int kThreads = (kValueWarp0 + kValueWarps) * 32;
-  // Rings: raw pages, K quarters in tensor memory, V units.  A page lives
-  // from its load to the end of its V decode, about ten thousand cycles, so
-  // the more of them fit the better.
-  static constexpr int kRaw = NR == 64 ? 4 : (NR == 32 ? 6 : 7);
+  // Rings: raw pages, K quarters in tensor memory, a V unit (kVTokens x 128
+  // dims, two chunks of 64 dims) for each dim quarter.  A page lives from its
+  // load to the end of its V decode, about ten thousand cycles.  With 64 rows
+  // Q leaves so little that V units of half the size, and six pages instead of
+  // four, gain more than their barriers cost (4096-token windows of 64 x 64
+  // rows: 109.6 us against 114.7); with 16 they only cost (16 heads over 64k
+  // tokens: 280 us against 225).
+  static constexpr int kVTokens = NR == 64 ? 32 : 64;
+  static constexpr int kVUnitBytes = kVTokens * 128 * 2;
+  static constexpr int kRaw = NR == 16 ? 7 : 6;
   static constexpr int kKRing = NR == 64 ? 2 : 4;
-  static constexpr int kVRing = 4;  // one for each V warp
+  static constexpr int kVRing = 4;
   static constexpr int kQBytes = NR * kD * 2;
   static constexpr int kPBytes = kTile * NR * 2;
   static constexpr int kQOff = 0;
@@ -675,10 +679,10 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
       const int qq = (warp - kVWarp0) & 3;
       const int piece = (lane & 1) | ((lane >> 2) & 2);         // 32-dim piece of the quarter
       const int tok = ((lane >> 1) & 3) | ((lane >> 2) & 4);    // token within eight
-      const int first = ((warp - kVWarp0) >> 2) * 32 + tok;     // this lane's first record of a page
+      const int first = ((warp - kVWarp0) >> 2) * (L::kVTokens / kShare) + tok;  // this lane's first record of a unit
       const uint32_t rows = smem_u32(sRaw) + first * kRecFp4 + qq * 64 + piece * 16;
       const int scales = 256 - qq * 56 - piece * 14;            // from there to the scales
-      const uint32_t dst = smem_u32(sV) + qq * kVUnitBytes + (piece >> 1) * (kVUnitTokens * 128) + first * 128;
+      const uint32_t dst = smem_u32(sV) + qq * L::kVUnitBytes + (piece >> 1) * (L::kVTokens * 128) + first * 128;
       // The lane's first 16-byte unit of a 128-byte row, swizzled; unit j is at this ^ 16 j.
       const uint32_t unit0 = dst + (((piece & 1) * 4) ^ tok) * 16;
       int slot = 0;
@@ -690,31 +694,34 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
           wait_for(&bars[L::bRawFull + slot], raw_parity, abort_flag, p.d_error);
           const int have = ((info[n % kInfoRing].x >> (8 * half)) & 0xFF) - first;  // rows of this lane below it are there
           const uint32_t src = rows + slot * kPageBytes;
+          constexpr int kSteps = L::kVTokens / kShare / 8, kAtOnce = kSteps < 4 ? kSteps : 4, kUnits = kPage / L::kVTokens;
 #pragma unroll 1
-          for (int i0 = 0; i0 < 8 / kShare; i0 += 4) {
-            uint4 data[4];
-            uint32_t sc[4];
+          for (int w = 0; w < kUnits; ++w) {
+#pragma unroll 1
+            for (int i0 = 0; i0 < kSteps; i0 += kAtOnce) {
+              uint4 data[kAtOnce];
+              uint32_t sc[kAtOnce];
+              const uint32_t from = src + (w * L::kVTokens + i0 * 8) * kRecFp4;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              data[i] = lds128(src + (i0 + i) * 8 * kRecFp4);
-              sc[i] = lds16(src + scales + (i0 + i) * 8 * kRecFp4);
+              for (int i = 0; i < kAtOnce; ++i) {
+                data[i] = lds128(from + i * 8 * kRecFp4);
+                sc[i] = lds16(from + scales + i * 8 * kRecFp4);
+              }
+              if (i0 == 0) wait_for(&bars[L::bVFree + qq], kUnits == 2 ? w ^ 1 : half ^ 1, abort_flag, p.d_error);
+#pragma unroll
+              for (int i = 0; i < kAtOnce; ++i) {
+                uint32_t o[16];
+                decode32(data[i], w * L::kVTokens + (i0 + i) * 8 < have ? sc[i] : 0u, o);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  sts128((unit0 ^ (16 * j)) + (i0 + i) * 1024, o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+              }
             }
-            if (i0 == 0) wait_for(&bars[L::bVFree + qq], half ^ 1, abort_flag, p.d_error);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t o[16];
-              decode32(data[i], (i0 + i) * 8 < have ? sc[i] : 0u, o);
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                sts128((unit0 ^ (16 * j)) + (i0 + i) * 1024, o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[L::bVFull + qq]);
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&bars[L::bVFull + qq]);
-            mbar_arrive(&bars[L::bRawFree + slot]);
-          }
+          if (lane == 0) mbar_arrive(&bars[L::bRawFree + slot]);
           if (++slot == L::kRaw) slot = 0, raw_parity ^= 1;
         }
       }
@@ -757,7 +764,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
       constexpr uint32_t idesc = idesc_f16(128, NR, true, true);
       constexpr uint32_t p_sbo = 8 * 2 * NR;  // eight rows of P^T
       constexpr uint32_t p_swz = NR == 64 ? kSwizzle128 : (NR == 32 ? kSwizzle64 : kSwizzle32);
-      const uint64_t v_desc = make_smem_desc(smem_u32(sV), kVUnitTokens * 128, 1024, kSwizzle128);
+      const uint64_t v_desc = make_smem_desc(smem_u32(sV), L::kVTokens * 128, 1024, kSwizzle128);
       const uint64_t p_desc = make_smem_desc(smem_u32(sP), 16 * p_sbo, p_sbo, p_swz);
       const uint32_t v_lo = static_cast<uint32_t>(v_desc), p_lo = static_cast<uint32_t>(p_desc);
       const uint32_t v_hi = static_cast<uint32_t>(v_desc >> 32), p_hi = static_cast<uint32_t>(p_desc >> 32);
@@ -775,16 +782,18 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
               o_parity ^= 1;
             }
           }
-          const uint32_t b = p_lo + ((half * 8 * p_sbo) >> 4);
+          constexpr int kUnits = kPage / L::kVTokens;
 #pragma unroll 1
-          for (int qq = q0; qq < q0 + kMine; ++qq) {
-            wait_for(&bars[L::bVFull + qq], half, abort_flag, p.d_error);
+          for (int w = 0; w < kUnits * kMine; ++w) {
+            const int qq = q0 + w % kMine, at = half * kUnits + w / kMine;
+            wait_for(&bars[L::bVFull + qq], at & 1, abort_flag, p.d_error);
             tc_fence_after();
-            const uint32_t d = tmem + L::cO + qq * NR, a = v_lo + ((qq * kVUnitBytes) >> 4);
+            const uint32_t d = tmem + L::cO + qq * NR, a = v_lo + ((qq * L::kVUnitBytes) >> 4);
+            const uint32_t b = p_lo + ((at * (L::kVTokens / 8) * p_sbo) >> 4);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < L::kVTokens / 16; ++j)
               mma_f16_ss(d, a + ((j * 2048) >> 4), v_hi, b + ((j * 2 * p_sbo) >> 4), p_hi, idesc,
-                         !(opens && half == 0 && j == 0));
+                         !(opens && at == 0 && j == 0));
             commit_one(&bars[L::bVFree + qq]);
           }
           commit_one(&bars[L::bPFree + half]);
