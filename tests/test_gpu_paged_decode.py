@@ -17,13 +17,13 @@ import fp4_kv_cache_sparse_gb300 as mla
 pytestmark = pytest.mark.gpu
 
 DEV = torch.device("cuda", 0)
-E2M1 = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6, -0.0, -0.5, -1, -1.5, -2, -3, -4, -6], dtype=torch.float64, device=DEV)
+E2M1 = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6, -0.0, -0.5, -1, -1.5, -2, -3, -4, -6], dtype=torch.float64)
 
 
 def decode_records(rec):
     n = rec.shape[0]
     code = torch.stack([rec[:, :256] & 15, rec[:, :256] >> 4], 2).reshape(n, 512).long()
-    return E2M1[code] * rec[:, 256:].contiguous().view(torch.float8_e4m3fn).double().repeat_interleave(16, 1)
+    return E2M1.to(code.device)[code] * rec[:, 256:].contiguous().view(torch.float8_e4m3fn).double().repeat_interleave(16, 1)
 
 
 def random_records(n, g, top=0x3C):
