@@ -116,7 +116,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.mla_rope_table.argtypes = [P, I32, I32, D, I32, D, D, D, D, D]
     lib.mla_rope_table_from_freqs.argtypes = [P, I32, I32, P, D]
     lib.mla_rope.argtypes = [I32, P, I64, I64, P, I64, I64, I64, I32, I32, I32, P, P, I32, P]
-    lib.mla_rms_norm_fp8.argtypes = [I32, P, I64, P, I64, P, F, P, I64, P, I64, P, I64, I64, I32, P]
+    lib.mla_rms_norm_fp8.argtypes = [I32, P, I64, P, I64, P, F, P, I64, P, I64, P, I64, I64, I32, P, P]
     lib.mla_paged_decode_plan.argtypes = [P, I32, ctypes.POINTER(I32), ctypes.POINTER(SZ)]
     lib.mla_paged_decode_fp4.argtypes = [P, P, P, P, P, I32, P, SZ, P, P, P, P]
     lib.mla_status_string.argtypes = [ctypes.c_int]
@@ -437,7 +437,8 @@ def _rows(t, dev, dtype, what, shape):
     return t.data_ptr(), s0 if shape[0] > 1 else shape[1]
 
 
-def rms_norm_fp8(x, weight, eps: float, codes, scales, residual=None, residual_out=None, stream=None) -> None:
+def rms_norm_fp8(x, weight, eps: float, codes, scales, residual=None, residual_out=None, error=None,
+                 stream=None) -> None:
     """codes, scales = FP8 blocks of (x + residual) / rms * weight, and the sum
     itself, rounded, into residual_out (mla_rms_norm_fp8).  x, residual,
     residual_out [n, d], weight [d] of one type (bf16, fp16, fp32); codes
@@ -458,7 +459,7 @@ def rms_norm_fp8(x, weight, eps: float, codes, scales, residual=None, residual_o
     if n == 0 and d % 32 == 0 and d > 0:
         return
     _call(lib.mla_rms_norm_fp8, "mla_rms_norm_fp8", dev, stream, dtype, px, sx, pr, sr, pw, eps, po, so, pc, sc, ps, ss,
-          n, d)
+          n, d, _arg(error, dev, torch.int32, "error"))
 
 
 def paged_decode_plan(problem: PagedProblem, num_sms: int = 0):

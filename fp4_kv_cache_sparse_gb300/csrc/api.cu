@@ -467,7 +467,7 @@ mla_status_t mla_rope(int32_t dtype, const void* x, int64_t x_row_stride, int64_
 mla_status_t mla_rms_norm_fp8(int32_t dtype, const void* x, int64_t x_stride, const void* residual,
                               int64_t residual_stride, const void* weight, float eps, void* residual_out,
                               int64_t residual_out_stride, void* codes, int64_t codes_stride, void* scales,
-                              int64_t scales_stride, int64_t n, int32_t dim, mla_stream_t stream) {
+                              int64_t scales_stride, int64_t n, int32_t dim, int32_t* d_error, mla_stream_t stream) {
   const int bytes = element_bytes(dtype);
   if (bytes == 0 || n < 0 || dim < 1 || !std::isfinite(eps) || eps < 0.f) return MLA_ERR_INVALID_ARG;
   if (dim % 32 != 0 || dim > 16384 || n >= (int64_t(1) << 31)) return MLA_ERR_UNSUPPORTED;
@@ -496,6 +496,7 @@ mla_status_t mla_rms_norm_fp8(int32_t dtype, const void* x, int64_t x_stride, co
   p.n = n;
   p.dim = dim;
   p.eps = eps;
+  p.d_error = d_error;
   if (launch_rms_norm_fp8(dtype, p, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return MLA_ERR_CUDA;
   return MLA_OK;
 }

@@ -123,6 +123,7 @@ struct NormParams {
   int64_t x_row, residual_row, residual_out_row, codes_row, scales_row, n;
   int dim;
   float eps;
+  int32_t* d_error;      // nullable
 };
 cudaError_t launch_rms_norm_fp8(int dtype, const NormParams& p, cudaStream_t stream);
 

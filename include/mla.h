@@ -393,12 +393,14 @@ mla_status_t mla_rope(int32_t dtype, const void* x, int64_t x_row_stride, int64_
  *             row 16-byte aligned (weight [dim], 16-byte aligned).
  *   codes     uint8, rows 8-byte aligned; scales uint8 [n][dim / 32].
  *   dim       a multiple of 32, at most 16384 (MLA_ERR_UNSUPPORTED otherwise).
+ *   d_error   device int32 or NULL; bits are OR-ed into it (MLA_DEVERR_TIMEOUT
+ *             when a row's copy did not arrive: that row is not written).
  * Infinities and NaN in a row make that row's codes undefined; no other row.
  */
 mla_status_t mla_rms_norm_fp8(int32_t dtype, const void* x, int64_t x_stride, const void* residual,
                               int64_t residual_stride, const void* weight, float eps, void* residual_out,
                               int64_t residual_out_stride, void* codes, int64_t codes_stride, void* scales,
-                              int64_t scales_stride, int64_t n, int32_t dim, mla_stream_t stream);
+                              int64_t scales_stride, int64_t n, int32_t dim, int32_t* d_error, mla_stream_t stream);
 
 /*
  * Attention over the pages of a cache held in 4 bits: every query token sees

@@ -148,7 +148,7 @@ def test_rope_refuses_a_table_that_is_none(lib):
 
 def _norm(lib, dtype=0, x=A, xs=512, res=None, rs=512, w=A, eps=1e-6, out=None, os_=512, codes=A, cs=528, scales=A,
           ss=528, n=4, d=512):
-    return lib.mla_rms_norm_fp8(dtype, x, xs, res, rs, w, eps, out, os_, codes, cs, scales, ss, n, d, None)
+    return lib.mla_rms_norm_fp8(dtype, x, xs, res, rs, w, eps, out, os_, codes, cs, scales, ss, n, d, None, None)
 
 
 @pytest.mark.parametrize("kw,status", [
