@@ -41,7 +41,8 @@ struct Eight<float> {
     b = *reinterpret_cast<const float4*>(p + 4);
   }
   __device__ __forceinline__ void get(float2 (&f)[4]) const {
-    f[0] = make_float2(a.x, a.y), f[1] = make_float2(a.z, a.w), f[2] = make_float2(b.x, b.y), f[3] = make_float2(b.z, b.w);
+    f[0] = make_float2(a.x, a.y), f[1] = make_float2(a.z, a.w);
+    f[2] = make_float2(b.x, b.y), f[3] = make_float2(b.z, b.w);
   }
   __device__ __forceinline__ void put(const float2 (&f)[4]) {
     a = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
@@ -181,7 +182,8 @@ __global__ void __launch_bounds__(threads_of<kTeam>(), resident_of<kTeam>())
                    : "memory");
     };
     copy(mine + slot * stage_bytes, static_cast<const T*>(p.x) + r * p.x_row);
-    if constexpr (kRes) copy(mine + slot * stage_bytes + row_bytes, static_cast<const T*>(p.residual) + r * p.residual_row);
+    if constexpr (kRes)
+      copy(mine + slot * stage_bytes + row_bytes, static_cast<const T*>(p.residual) + r * p.residual_row);
   };
   for (int i = 0; i < stages; ++i) request(row + i * stride, i);
   Eight<T> w[2] = {};
@@ -336,6 +338,7 @@ cudaError_t launch(const NormParams& p, cudaStream_t stream) {
 
 template <typename T>
 cudaError_t launch_typed(const NormParams& p, cudaStream_t stream) {
+  // (200,000 x 512: 56.3 us with a warp a row, 87.1 with two.)
   if (p.dim <= 512) return launch<T, 32>(p, stream);
   if (p.dim <= 1024) return launch<T, 64>(p, stream);
   if (p.dim <= 2048) return launch<T, 128>(p, stream);

@@ -9,8 +9,10 @@
 // slot map is written by the same 8192 threads, each finding its tokens'
 // request by a binary search of the prefix in shared memory; a long one by a
 // second kernel over the whole GPU, from the tables and lengths that the first
-// has left (512,000 slots: 18 us in the cluster, 6 us so; at 16,384 the second
-// launch costs what it saves).
+// has left (1000 requests: 512,000 slots 27.3 us in the cluster, 12.6 us so;
+// 64,000 slots 10.7 against 12.3).  One decode step of 256 requests takes 5.7
+// us: latency alone, a launch, three dependent trips to memory and three
+// barriers.
 #include <cstdint>
 
 #include "mla_device.cuh"
@@ -22,7 +24,7 @@ namespace {
 
 constexpr int kCtas = 8;
 constexpr int kPlanThreads = 1024;
-constexpr int kLongMap = 16384;  // slots from which a kernel of its own writes the map
+constexpr int kLongMap = 96 * 1024;  // slots from which a kernel of its own writes the map
 
 struct Sums {
   int64_t tokens, take, give;

@@ -12,31 +12,47 @@
 // tiles of the sinks and of the window only).  All units in order, each a
 // fixed cost and then its items, are cut into gridDim.x runs of equal cost, one
 // per CTA (one CTA per SM); the lengths are on the device, so every CTA derives
-// the cut itself by a scan over the units.
-// A unit cut by a run's end leaves normalised fp32 partials, merged by a
-// second kernel.
+// the cut itself by a scan over the units.  A unit cut by a run's end leaves
+// normalised fp32 partials, merged by a second kernel.
 //
-// One CTA, 18 warps (26 with 64 rows):
-//   loader (1 warp)    each tile's two pages by bulk copies (records are
-//                      contiguous in a page) into a ring of raw FP4 tiles.
-//   K warps (4)        raw FP4 -> f16 into tensor memory, lane = token: the A
-//                      operand of S^T = K Q^T, a 128-dim quarter at a time.
-//   V warps (4)        raw FP4 -> f16 into shared memory (128-byte swizzle),
-//                      in units of 64 tokens x 128 dims: the MN-major A
-//                      operand of O^T += V^T P^T.
-//   issuer (1 warp)    all tensor-core work; S^T of the next tile goes before
-//                      O^T of this one, so the softmax runs beside O^T.
-//   softmax (8 warps)  thread = token x half of the rows: scale, mask, lazy
-//                      running maximum, P^T to shared memory, row sums in
-//                      registers; at a unit's end the epilogue, before it
-//                      the next unit's Q.
+// One CTA, 20 warps with 32 rows, 28 with 16 or 64:
+//   softmax (8; 16 with 64 rows)  thread = token x some of the rows: scale,
+//                      mask, lazy running maximum, P^T to shared memory, row
+//                      sums in registers; at a unit's end the epilogue, before
+//                      it the next unit's Q.
+//   K decode (4; 8 with 16 rows)  raw FP4 -> f16 into tensor memory, lane =
+//                      token: the A operand of S^T = K Q^T, a 128-dim quarter
+//                      at a time.
+//   V decode (4; 8 with 16 rows)  raw FP4 -> f16 into shared memory (128-byte
+//                      swizzle), a dim quarter each, in units of 64 tokens (32
+//                      with 64 rows): the MN-major A operand of
+//                      O^T += V^T P^T.
+//   loader (1)         each tile's two pages by bulk copies (records are
+//                      contiguous in a page) into a ring of raw pages.
+//   score issuer (1)   S^T, two tiles ahead of
+//   value issuers (2)  O^T, two dim quarters each: with one, what it waits for
+//                      holds up the other quarters (64 heads over up to 8k
+//                      tokens 78 us against 70, 16 over 64k 264 against 223).
+// Every role's loop is kept rolled and short: the roles together have to stay
+// in the instruction cache (issue loops unrolled over a tile: 16 heads over
+// 64k tokens 450 us against 273).
+//
 // A tile is decoded twice (K to tensor memory, V to shared memory) because
 // that is cheaper than the shared memory it saves: one f16 tile is 128 KB,
 // and kept from S^T to O^T it would leave room for nothing beside it; raw it
-// is 36 KB, so two or three tiles are in flight and neither copy of a quarter
-// lives longer than the product that reads it.  With K in tensor memory
-// shared memory carries 128 KB of V in and out per tile and the small
-// operands, which is what bounds the kernel.
+// is 36 KB, so two to four tiles are in flight and neither copy of a quarter
+// lives longer than the product that reads it.
+//
+// What bounds it.  A tile moves through shared memory 128 KB of V written and
+// 128 KB read, the raw tile written once and read twice (108 KB), and Q once
+// and P four times as B operands: 400 KB with 16 rows, 510 KB with 64, that is
+// 3100 and 4000 cycles at 128 bytes a cycle; measured are 3800 and 5500 in the
+// middle of a run (the tensor core itself needs 512 and 2050).  So 32 x 16
+// heads over 64k tokens take 224 us (604 MB, 40 % of a copy's bandwidth), 64 x
+// 64 heads over up to 8k tokens 65 us (38.7 GFLOP, 31 % of the bf16 rate), 32
+// x 2 x 128 heads with a window of 4096 109 us (34 %).  One tile alone takes 8.5 us, 2.5 of
+// them until the cut is known, 4 until the first scores are there, and a merge
+// 3 us more.
 //
 // Numbers.  e2m1 x e4m3 has at most 6 significant bits and lies in f16's
 // range, so K and V are exact in f16.  Q (bf16) is scaled by a power of two
@@ -59,18 +75,24 @@ namespace {
 constexpr int kPageBytes = kPage * kRecFp4;
 constexpr int kInfoRing = 8;
 constexpr uint64_t kPagedWaitNs = 2000000000ull;  // 2 s per wait
-constexpr int kUnitCost = 2;                 // what a unit's Q and epilogue take, in tiles
-constexpr float kSlack = 8.f;                // the running maximum may lag by 2^8
+// What a unit's Q and epilogue take, in tiles (104 sequences of 288 tokens, 64
+// heads: 23.2 us, 27.6 with nothing; 64 of up to 8k: 70.7, 76.8).
+constexpr int kUnitCost = 2;
+// The running maximum may lag by 2^8: O is rescaled seldom (64 x 64 heads over
+// up to 8k tokens: 70 us, with a maximum that follows every tile 84).
+constexpr float kSlack = 8.f;
 constexpr float kPBias = 7.f;                // P of the maximum is 2^7
 constexpr float kNoMax = -3.0e38f;           // running maximum before any visible token
 
 template <int NR>
 struct PSmem {
-  // A softmax thread holds NR / kSides rows: exponents and sums stay in registers.
+  // A softmax thread holds NR / kSides rows: exponents and sums stay in
+  // registers (64 x 64 heads over up to 8k tokens: 70 us, with two sides 80).
   static constexpr int kSides = NR == 64 ? 4 : 2;
   static constexpr int kSoftmaxWarps = 4 * kSides;
-  // Decode warps of each kind: eight hide more latency, but with more rows the
-  // softmax needs more registers than 28 warps leave it.
+  // Decode warps of each kind: eight hide more latency (16 heads over 64k
+  // tokens: 223 us against 253), but with more rows the softmax needs more
+  // registers than that many warps leave it.
   static constexpr int kDecodeWarps = NR == 16 ? 8 : 4;
   static constexpr int kKWarp0 = kSoftmaxWarps, kVWarp0 = kKWarp0 + kDecodeWarps, kLoadWarp = kVWarp0 + kDecodeWarps;
   static constexpr int kScoreWarp = kLoadWarp + 1, kValueWarp0 = kScoreWarp + 1;
@@ -313,7 +335,10 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
 // Shared memory by 32-bit address.
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
   return v;
 }
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
@@ -630,7 +655,8 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
       // Four warps, one for each quadrant of tensor memory lanes, decode a
       // 128-dim quarter; of eight, two teams take quarters in turn.  (What
       // stands in rows past the visible tokens only makes masked scores.)
-      constexpr int kTeams = L::kDecodeWarps / 4, kHalves = kTeams == 2 ? 1 : 2;  // (unrolled: two warps cover less latency)
+      constexpr int kTeams = L::kDecodeWarps / 4;
+      constexpr int kHalves = kTeams == 2 ? 1 : 2;  // unrolled where one team has to cover its own latency
       const int quad = warp & 3, team = (warp - kKWarp0) >> 2;
       const uint32_t tK = tmem + (static_cast<uint32_t>(quad * 32) << 16) + L::cK;
       const uint32_t rows = smem_u32(sRaw) + ((quad & 1) * 32 + lane) * kRecFp4;
@@ -694,7 +720,8 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
           wait_for(&bars[L::bRawFull + slot], raw_parity, abort_flag, p.d_error);
           const int have = ((info[n % kInfoRing].x >> (8 * half)) & 0xFF) - first;  // rows of this lane below it are there
           const uint32_t src = rows + slot * kPageBytes;
-          constexpr int kSteps = L::kVTokens / kShare / 8, kAtOnce = kSteps < 4 ? kSteps : 4, kUnits = kPage / L::kVTokens;
+          constexpr int kSteps = L::kVTokens / kShare / 8, kAtOnce = kSteps < 4 ? kSteps : 4;
+          constexpr int kUnits = kPage / L::kVTokens;
 #pragma unroll 1
           for (int w = 0; w < kUnits; ++w) {
 #pragma unroll 1
@@ -1098,10 +1125,9 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
 // Merge of a unit cut by parts: pieces with normalised outputs o_i and
 // log-sum-exps L_i give L = ln sum exp L_i and sum exp(L_i - L) o_i.  An entry
 // of the info table (a part's last unit, or a unit) names the parts that hold
-// pieces.  Per row kThreads threads, each with 512 / kThreads dims: a warp where
-// units have two or three pieces (blocks of four rows: many rows, each a short
-// chain of loads), four groups of 128 threads that share a row's pieces where
-// few units are cut into many.
+// pieces.  A row is joined by a warp where units have a few pieces (many rows,
+// each a short chain of loads, so blocks of four), by four groups of 128
+// threads that share its pieces where few units are cut into many.
 struct Pieces {
   int part, count, r, nr;
   // Piece 0 is the first part's slot 2 part + 1, piece i part + i's slot 2 (part + i).
@@ -1236,9 +1262,11 @@ cudaError_t launch(PagedParams p, const PagedPlan& plan, cudaStream_t stream) {
   cfg.dynamicSmemBytes = PSmem<NR>::kAlloc;
   e = cudaLaunchKernelEx(&cfg, paged_decode_kernel<NR>, p, plan.groups, q_map);
   if (e != cudaSuccess) return e;
-  // Units that are few against the parts are cut into many pieces.
+  // Units that are few against the parts are cut into many pieces (one
+  // sequence of 64k tokens, 16 heads: 26 us so, 61 by single warps; 64 x 64
+  // heads at 8k, in three pieces: 89 against 70).
   const int units = p.batch * plan.groups;
-  const bool many = units * 4 <= plan.num_parts;
+  const bool many = units * 6 <= plan.num_parts;
   cfg.gridDim = dim3(static_cast<unsigned>(p.info_by_unit ? units : plan.num_parts), many ? NR : NR / 4);
   cfg.blockDim = dim3(many ? 512 : 128);
   cfg.dynamicSmemBytes = 0;
