@@ -24,7 +24,7 @@ namespace mla {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;  // (8000 tokens x 32 heads of 128 dims: 26.7 us, 28.7 with 256)
 // Heads whose loads are in flight together (8000 tokens x 32 heads of 128 dims:
 // 25.6 us with one, 23.3 with two, 25.2 with four).
 constexpr int kAtOnce = 2;
@@ -187,16 +187,17 @@ cudaError_t launch(const RopeParams& p, const mla_rope_table_t& table, cudaStrea
   g.rot_cols = table.rope_dim / (kHalf ? 2 * VE : VE);
   g.cols = g.rot_cols + (p.x == p.y ? 0 : (p.head_dim - table.rope_dim) / (VE * sizeof(T) == 16 ? VE : 1));
   // Long head runs spread a column's sines over more heads, short ones keep
-  // every SM busy when there are few tokens.  The 64-dim tails of 128 heads:
-  // 256 tokens 3.4 us in runs of 8, 5.1 head by head; 32 tokens 3.1 against 2.4.
+  // every SM busy when there are few tokens.  The 64-dim tails of 128 heads in
+  // runs of 8 and head by head: 1024 tokens 5.6 and 9.2 us, 32 tokens 3.1 and
+  // 2.4; of 256 tokens, not in L2, 10.3 in runs of 8 and 8.2 in runs of 4.
   g.heads_per = 8;
   while (g.heads_per > 1 &&
-         p.n * ((p.heads + g.heads_per - 1) / g.heads_per) * g.cols < static_cast<int64_t>(sms) * 192)
+         p.n * ((p.heads + g.heads_per - 1) / g.heads_per) * g.cols < static_cast<int64_t>(sms) * 384)
     g.heads_per /= 2;
   g.runs = (p.heads + g.heads_per - 1) / g.heads_per;
   g.units = p.n * g.runs;
   int64_t blocks = (g.units * g.cols + kRopeThreads - 1) / kRopeThreads;
-  const int64_t cap = static_cast<int64_t>(sms) * 32;
+  const int64_t cap = static_cast<int64_t>(sms) * 64;
   if (blocks > cap) blocks = cap;
   rope_kernel<T, VE, kHalf><<<static_cast<unsigned>(blocks), kRopeThreads, 0, stream>>>(p, g, table);
   return cudaGetLastError();
