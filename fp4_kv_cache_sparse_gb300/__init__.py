@@ -443,7 +443,8 @@ def rms_norm_fp8(x, weight, eps: float, codes, scales, residual=None, residual_o
     itself, rounded, into residual_out (mla_rms_norm_fp8).  x, residual,
     residual_out [n, d], weight [d] of one type (bf16, fp16, fp32); codes
     uint8 [n, d] (E4M3FN) and scales uint8 [n, d / 32] (e8m0); any row
-    strides, so records[:, :512] and records[:, 512:] of 528-byte rows serve."""
+    strides, so records[:, :512] and records[:, 512:] of 528-byte rows serve.
+    error: optional int32 [1] error word."""
     lib = load()
     dev = _device_of(x, "rms_norm_fp8")
     dtype = _DTYPES.get(x.dtype)

@@ -1,10 +1,12 @@
 /*
  * mla.h -- C ABI of the GB300 (sm_103a) token-sparse MLA decode library.
  *
- * One operation, in three calls: the tile-scheduler metadata (computed once
- * before a decode loop), the sparse decode step itself, and the merge of
- * split-KV partial results.  Sources for what is computed (page title,
- * section):
+ * The sparse decode, in three calls: the tile-scheduler metadata (computed
+ * once before a decode loop), the decode step itself, and the merge of
+ * split-KV partial results.  Beside it the operators that a serving step over
+ * a paged FP4 cache needs: the cache writer, page and slot planning, rotary
+ * positions, the residual norm with its FP8 cast, and attention over the pages.
+ * Sources for what the sparse decode computes (page title, section):
  *   "flops/flashmla-decode-fp8-fp4-kv" -- "Arithmetic intensity" (the 528-byte
  *       FP8 and 288-byte FP4 token records, scales inlined in each record) and
  *       "Workarounds" (indices tensor (batch, seq_len_q, topk) of
@@ -19,9 +21,9 @@
  * Conventions for every call:
  *   - Pointers named d_* and every tensor argument are DEVICE pointers; the
  *     problem descriptor and the *_out arguments are HOST pointers.
- *   - All tensors are dense, row-major, contiguous, owned by the caller; the
- *     library allocates nothing and keeps no state between calls except a
- *     per-device cache of the SM count.
+ *   - All tensors are dense, row-major, contiguous (but where a call takes
+ *     strides), owned by the caller; the library allocates nothing and keeps no
+ *     state between calls except a per-device cache of the SM count.
  *   - Work is enqueued on `stream` (a cudaStream_t; NULL = legacy default
  *     stream) and returns without synchronising the host.
  *   - The return status reports argument validation and launch errors only;
@@ -45,7 +47,7 @@ typedef enum {
   MLA_OK = 0,
   MLA_ERR_INVALID_ARG = 1,   /* null/misaligned pointer, bad size, inconsistent metadata size */
   MLA_ERR_UNSUPPORTED = 2,   /* a legal problem outside what the kernels implement */
-  MLA_ERR_WORKSPACE = 3,     /* workspace smaller than mla_get_metadata reported */
+  MLA_ERR_WORKSPACE = 3,     /* workspace smaller than the plan or metadata call reported */
   MLA_ERR_CUDA = 4,          /* a CUDA runtime call or a launch failed */
   MLA_ERR_TIMEOUT = 5        /* reserved for host-side waits; device timeouts use MLA_DEVERR_TIMEOUT */
 } mla_status_t;
