@@ -368,9 +368,13 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 }
 
 // 32 consecutive dims of a record: 16 data bytes and their two scale bytes
-// (sc, low byte first) -> 16 f16x2, exact.
+// (sc, low byte first) -> 16 f16x2, exact.  As a value a NaN scale counts as
+// 448: a row that does not see the token multiplies it by 0, one that does
+// has a NaN weight from the key.
+template <bool kValue>
 __device__ __forceinline__ void decode32(const uint4& data, uint32_t sc, uint32_t (&o)[16]) {
-  const uint32_t s2 = e4m3x2_to_f16x2(sc);
+  uint32_t s2 = e4m3x2_to_f16x2(sc);
+  if constexpr (kValue) asm("min.f16x2 %0, %0, %1;" : "+r"(s2) : "r"(0x5F005F00u));
   const uint32_t s0 = __byte_perm(s2, s2, 0x1010), s1 = __byte_perm(s2, s2, 0x3232);
   const uint32_t w[4] = {data.x, data.y, data.z, data.w};
 #pragma unroll
@@ -680,10 +684,10 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
           for (int hh = 0; hh < 2; ++hh) {
             const uint32_t s = hh ? sc.y : sc.x;
             uint32_t o[16];
-            decode32(data[0], s & 0xFFFFu, o);
+            decode32<false>(data[0], s & 0xFFFFu, o);
             tmem_st16(t + hh * 32, o);
             if (hh == 0) data[0] = lds128(src + 32);
-            decode32(data[1], s >> 16, o);
+            decode32<false>(data[1], s >> 16, o);
             tmem_st16(t + hh * 32 + 16, o);
             if (hh == 0) data[1] = lds128(src + 48);
           }
@@ -738,7 +742,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
 #pragma unroll
               for (int i = 0; i < kAtOnce; ++i) {
                 uint32_t o[16];
-                decode32(data[i], w * L::kVTokens + (i0 + i) * 8 < have ? sc[i] : 0u, o);
+                decode32<true>(data[i], w * L::kVTokens + (i0 + i) * 8 < have ? sc[i] : 0u, o);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                   sts128((unit0 ^ (16 * j)) + (i0 + i) * 1024, o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);

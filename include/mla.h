@@ -434,8 +434,11 @@ mla_status_t mla_paged_decode_plan(const mla_paged_problem_t* problem, int32_t n
  * A query token that sees nothing (an empty sequence, p < 0) gets +0 and -inf.
  *   q            bf16 [batch][s][h_q][512], 16-byte aligned, finite.
  *   kv           uint8 [num_pages][64][288] FP4 records, 16-byte aligned.
- *                Records past a sequence's end are never used, whatever bytes they hold.
- *   block_table  int32 [batch][max_pages]: page ids; entries past ceil(len / 64) are not read.
+ *                Records that no query token of a sequence sees are never used, whatever
+ *                bytes they hold; a NaN scale in one makes the rows that see it
+ *                undefined, no other.
+ *   block_table  int32 [batch][max_pages]: page ids; entries past ceil(len / 64), and
+ *                those of pages that window and sinks leave out, are not read.
  *                The tokens of a page id outside [0, num_pages) are skipped
  *                and flagged (MLA_DEVERR_BAD_INDEX).
  *   seq_lens     int32 [batch] (device), the query tokens included; negative or past

@@ -86,6 +86,8 @@ class Case:
                 ok = ok.repeat_interleave(64)[:n]
             j = torch.arange(n, device=DEV)
             for i in range(self.s):
+                if skip is not None and i in skip:
+                    continue
                 at = n - self.s + i
                 see = (j <= at) & ((j > at - window) | (j < sinks) if window else torch.ones_like(j, dtype=torch.bool))
                 if n:
@@ -299,6 +301,66 @@ def test_two_decoders_at_once():
     torch.cuda.synchronize()
     c.check(*oc)
     d.check(*od)
+
+
+@pytest.mark.parametrize("s,h", [(1, 16), (3, 24), (2, 10)])
+def test_nan_records_that_no_row_sees(s, h):
+    """A page may hold anything between the sinks and the window: 0 times NaN must not reach a sum."""
+    c = Case([400, 130, 1000, 64], s, h, seed=17)
+    for b, n in enumerate(c.lens):
+        flat = torch.arange(n, device=DEV)
+        hidden = flat[(flat >= 4) & (flat <= n - s - 100)]
+        pages = c.table[b, hidden // 64].long()
+        c.kv[pages, hidden % 64] = 0xFF
+    out, lse, err = c.run(window=100, sinks=4)
+    assert err == 0
+    c.check(out, lse, 100, 4)
+
+
+@pytest.mark.parametrize("h", [5, 16, 40])
+def test_nan_spoils_only_the_rows_that_see_it(h):
+    c = Case([200, 65], 3, h, seed=18)
+    for b, n in enumerate(c.lens):                   # the last token: seen by the last query token alone
+        c.kv[int(c.table[b, (n - 1) // 64]), (n - 1) % 64] = 0xFF
+    out, lse, err = c.run()
+    assert err == 0
+    c.check(out, lse, skip={2})
+
+
+def test_infinite_query_spoils_only_its_row():
+    c = Case([300, 65], 2, 20, seed=19)
+    good = c.run()
+    q = c.q.clone()
+    c.q[0, 1, 3] = float("inf")
+    out, lse, err = c.run()
+    assert err == 0
+    c.q = q
+    out[0, 1, 3], lse[0, 1, 3] = good[0][0, 1, 3], good[1][0, 1, 3]
+    c.check(out, lse)
+
+
+def test_captured_behind_a_join_and_a_memset():
+    c = Case([700, 65], 1, 32, seed=20)
+    dec = mla.PagedFP4Decoder(c.problem(), DEV)
+    dec(c.q, c.kv, c.table, c.seq)
+    out, lse = torch.empty_like(c.q), torch.empty(2, 1, 32, device=DEV)
+    q, seq = torch.zeros_like(c.q), torch.zeros_like(c.seq)
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            q.copy_(c.q)
+        seq.copy_(c.seq)
+        torch.cuda.current_stream().wait_stream(side)
+        dec(q, c.kv, c.table, seq, out, lse)         # behind two branches
+        out.zero_()
+        dec(q, c.kv, c.table, seq, out, lse)         # behind a memset
+    for _ in range(3):
+        q.fill_(float("nan"))
+        out.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        c.check(out, lse)
 
 
 def test_binding_refusals():
