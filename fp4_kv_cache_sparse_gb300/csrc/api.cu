@@ -115,7 +115,8 @@ mla_status_t validate_paged(const mla_paged_problem_t* p) {
       static_cast<int64_t>(p->batch) * p->max_pages >= most)
     return MLA_ERR_UNSUPPORTED;
   const int64_t units = p->batch * ((rows + 15) / 16);
-  if (units * ((p->max_pages + 1) / 2 + 4) >= most) return MLA_ERR_UNSUPPORTED;  // tiles and a unit's own cost
+  // Tiles and a unit's own cost, rounded up to whole parts.
+  if (units * ((p->max_pages + 1) / 2 + 4) >= most - (1 << 16)) return MLA_ERR_UNSUPPORTED;
   return MLA_OK;
 }
 

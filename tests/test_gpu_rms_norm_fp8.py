@@ -138,7 +138,9 @@ def test_cache_records_strided_inputs_and_in_place_residual():
 def test_records_dequantize_as_the_cache_reads_them():
     x, _, w = inputs(64, 512, torch.bfloat16, seed=8, spread=0.5)
     rec = torch.empty(64, 528, dtype=torch.uint8, device=DEV)
-    mla.rms_norm_fp8(x, w, 1e-6, rec[:, :512], rec[:, 512:])
+    error = torch.zeros(1, dtype=torch.int32, device=DEV)
+    mla.rms_norm_fp8(x, w, 1e-6, rec[:, :512], rec[:, 512:], error=error)
+    assert int(error) == 0
     got = mla.dequantize(rec).double()
     v = x.double()
     v = v / torch.sqrt(v.square().mean(-1, keepdim=True) + 1e-6) * w.double()
