@@ -112,7 +112,7 @@ mla_status_t validate_paged(const mla_paged_problem_t* p) {
   // Positions, rows and tiles are counted in 32 bits.
   const int64_t most = int64_t(1) << 31, rows = static_cast<int64_t>(p->seq_len_q) * p->h_q;
   if (static_cast<int64_t>(p->max_pages) * MLA_PAGE_SIZE >= most - 256 || rows * p->batch >= most ||
-      static_cast<int64_t>(p->batch) * p->max_pages >= most)
+      static_cast<int64_t>(p->batch) * p->max_pages >= most || p->num_pages >= most / MLA_PAGE_SIZE)
     return MLA_ERR_UNSUPPORTED;
   const int64_t units = p->batch * ((rows + 15) / 16);
   // Tiles and a unit's own cost, rounded up to whole parts.

@@ -179,7 +179,8 @@ def test_paged_problem_layout_matches_header():
 
 @pytest.mark.parametrize("kw,status", [
     (dict(batch=0), INVALID), (dict(seq_len_q=0), INVALID), (dict(h_q=0), INVALID), (dict(max_pages=0), INVALID),
-    (dict(num_pages=0), INVALID), (dict(window=-1), INVALID), (dict(sinks=-1), INVALID),
+    (dict(num_pages=0), INVALID), (dict(num_pages=1 << 25), UNSUPPORTED),
+    (dict(window=-1), INVALID), (dict(sinks=-1), INVALID),
     (dict(sm_scale=float("inf")), INVALID), (dict(kv_format=mla.KV_NONE), INVALID),
     (dict(kv_format=mla.KV_FP8_528), UNSUPPORTED), (dict(kv_format=mla.KV_BF16), UNSUPPORTED),
     (dict(head_dim=576), UNSUPPORTED), (dict(page_size=32), UNSUPPORTED), (dict(h_q=129), UNSUPPORTED),
