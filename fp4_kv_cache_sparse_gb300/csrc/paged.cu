@@ -27,8 +27,8 @@
 //                      swizzle), a dim quarter each, in units of 64 tokens (32
 //                      with 64 rows): the MN-major A operand of
 //                      O^T += V^T P^T.
-//   loader (1)         each tile's two pages by bulk copies (records are
-//                      contiguous in a page) into a ring of raw pages.
+//   loader (1)         each tile's two pages by tensor copies into a ring of
+//                      raw pages, swizzled.
 //   score issuer (1)   S^T, two tiles ahead of
 //   value issuers (2)  O^T, two dim quarters each: with one, what it waits for
 //                      holds up the other quarters (64 heads over up to 8k
@@ -43,16 +43,17 @@
 // is 36 KB, so two to four tiles are in flight and neither copy of a quarter
 // lives longer than the product that reads it.
 //
-// What bounds it.  A tile moves through shared memory 128 KB of V written and
-// 128 KB read, the raw tile written once and read twice (108 KB), and Q once
-// and P four times as B operands: 400 KB with 16 rows, 510 KB with 64, that is
-// 3100 and 4000 cycles at 128 bytes a cycle; measured are 3800 and 5500 in the
-// middle of a run (the tensor core itself needs 512 and 2050).  So 32 x 16
-// heads over 64k tokens take 224 us (604 MB, 40 % of a copy's bandwidth), 64 x
-// 64 heads over up to 8k tokens 65 us (38.7 GFLOP, 31 % of the bf16 rate), 32
-// x 2 x 128 heads with a window of 4096 109 us (34 %).  One tile alone takes 8.5 us, 2.5 of
-// them until the cut is known, 4 until the first scores are there, and a merge
-// 3 us more.
+// What bounds it: shared memory.  A tile's 128 KB of V are written and read,
+// the raw tile is written once and read twice (108 KB), Q is read once and P
+// four times as B operands.  With 16 rows that and the small operands are 3860
+// accesses of 128 bytes a tile (2580 by the warps, 1280 by the tensor core),
+// with 64 rows 5520 (3470 and 2050), in 4250 and 6130 cycles: nine tenths of
+// what shared memory can do, and the tensor core is busy for 510 and 2050 of
+// them.  So 32 x 16 heads over 64k tokens take 221 us (604 MB, 40 % of a copy's
+// bandwidth), 64 x 64 heads over 4k to 8k tokens 66 us (38.7 GFLOP, 31 % of the
+// bf16 rate), 32 x 2 x 128 heads with a window of 4096 108 us (35 %).  One tile
+// alone takes 8.5 us, 2.5 of them until the cut is known, 4 until the first
+// scores are there, and a merge 3 us more.
 //
 // Numbers.  e2m1 x e4m3 has at most 6 significant bits and lies in f16's
 // range, so K and V are exact in f16.  Q (bf16) is scaled by a power of two
