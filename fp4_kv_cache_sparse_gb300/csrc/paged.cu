@@ -1300,7 +1300,23 @@ cudaError_t launch(PagedParams p, const PagedPlan& plan, cudaStream_t stream) {
 PagedPlan paged_plan(const mla_paged_problem_t* p, int num_parts) {
   PagedPlan pl{};
   const int64_t rows = static_cast<int64_t>(p->seq_len_q) * p->h_q;
-  pl.nr = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
+  // Rows of a unit: as few as hold them all, for a tile's decode is most of its
+  // cost (32 sequences of 8k tokens, 24 heads: 46.8 us by 32, 55.6 by 64, 65.8
+  // by 16; 64 heads: 57.4 by 64, 79.5 by 32; 32 of 64k, 16 heads: 222 by 16, 270
+  // by 32).  Where the lengths that the table and the window allow leave no
+  // part more than three or four tiles even so, as few as that takes: the start
+  // and the end of a unit are then most of its cost, and shorter (7 x 3 x 24
+  // heads, window 1000: 18.8 us by 16, 21.3 by 64; 16 of 1000 tokens, 64 heads:
+  // 20.4 by 32, 26.3 by 64; 2 of 446, 128 heads: 13.9 by 16, 18.4 by 64).
+  int64_t tiles = (p->max_pages + 1) / 2;
+  if (p->window > 0) {
+    const int64_t seen = (static_cast<int64_t>(p->window) + p->seq_len_q) / kTile + 2 + (p->sinks + kTile - 1ll) / kTile;
+    if (seen < tiles) tiles = seen;
+  }
+  const auto fits = [&](int nr) {
+    return rows <= nr || 2ll * p->batch * ((rows + nr - 1) / nr) * (tiles + kUnitCost) <= int64_t(7) * num_parts;
+  };
+  pl.nr = fits(16) ? 16 : (fits(32) ? 32 : 64);
   pl.groups = static_cast<int>((rows + pl.nr - 1) / pl.nr);
   pl.num_parts = num_parts;
   pl.ws_o_bytes = static_cast<size_t>(num_parts) * 2 * pl.nr * MLA_HEAD_DIM * sizeof(float);

@@ -115,9 +115,10 @@ LENGTHS = [0, 1, 2, 63, 64, 65, 127, 128, 129, 191, 200, 256, 257, 1000]
 
 @pytest.mark.parametrize("s,h", [(1, 16), (1, 1), (1, 64), (1, 128), (2, 128), (3, 24), (5, 7), (1, 33), (1, 17), (4, 16),
                                  (7, 100)])
-def test_matches_64_bits_at_every_length(s, h):
+@pytest.mark.parametrize("num_sms", [0, 20])         # (units have fewer rows where parts are plenty)
+def test_matches_64_bits_at_every_length(s, h, num_sms):
     c = Case(LENGTHS, s, h, seed=s * 200 + h)
-    out, lse, err = c.run()
+    out, lse, err = c.run(num_sms=num_sms)
     assert err == 0
     c.check(out, lse)
 
@@ -125,9 +126,10 @@ def test_matches_64_bits_at_every_length(s, h):
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (2, 4), (64, 0), (63, 64), (65, 130), (100, 4), (128, 128),
                                           (300, 5), (5000, 3), (0, 9), (200, 2000), (7, 129)])
 @pytest.mark.parametrize("s,h", [(1, 16), (3, 24), (2, 64)])
-def test_windows_and_sinks(window, sinks, s, h):
+@pytest.mark.parametrize("num_sms", [0, 20])
+def test_windows_and_sinks(window, sinks, s, h, num_sms):
     c = Case([0, 1, 5, 64, 129, 400, 777, 1025], s, h, seed=window + 7 * sinks)
-    out, lse, err = c.run(window=window, sinks=sinks)
+    out, lse, err = c.run(num_sms=num_sms, window=window, sinks=sinks)
     assert err == 0
     c.check(out, lse, window, sinks)
 
