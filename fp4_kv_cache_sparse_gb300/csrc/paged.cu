@@ -84,6 +84,8 @@ constexpr uint64_t kPagedWaitNs = 2000000000ull;  // 2 s per wait
 // What a unit's Q and epilogue take, in tiles (104 sequences of 288 tokens, 64
 // heads: 23.2 us, 27.6 with nothing; 64 of up to 8k: 70.7, 76.8).
 constexpr int kUnitCost = 2;
+// What the partials and the merge of cut units take, in tiles.
+constexpr int kMergeCost = 3;
 // The running maximum may lag by 2^8: O is rescaled seldom (64 x 64 heads over
 // up to 8k tokens: 70 us, with a maximum that follows every tile 84).
 constexpr float kSlack = 8.f;
@@ -128,7 +130,7 @@ struct PSmem {
   // float mb[NR], alpha[NR], scale[NR], linv[NR]; int hi[NR], lo[NR]; float red[4][NR]
   static constexpr int kInfoOff = kColOff + 10 * NR * 4;
   static constexpr int kMiscOff = kInfoOff + kInfoRing * 16;
-  static constexpr int kEnd = kMiscOff + 256;
+  static constexpr int kEnd = kMiscOff + 288;
   static constexpr int kAlloc = kEnd + 1024;
   static_assert(kAlloc <= 232448, "shared memory of one CTA");
   // Barrier indices.
@@ -483,7 +485,8 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
   // This part's run: first unit, its item that the run begins with, items; and the cost of every run.
   int* cut = reinterpret_cast<int*>(smem + L::kMiscOff + 8);
-  int* warp_sum = reinterpret_cast<int*>(smem + L::kMiscOff + 32);  // [warps]
+  int* warp_sum = reinterpret_cast<int*>(smem + L::kMiscOff + 32);    // [warps]
+  int* warp_most = reinterpret_cast<int*>(smem + L::kMiscOff + 160);  // [warps]
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
@@ -509,10 +512,12 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
   const int units = p.batch * groups;
   const int per = (units + kPagedThreads - 1) / kPagedThreads;
   const int u_a = min(units, tid * per), u_b = min(units, u_a + per);
-  int mine = 0;
+  int mine = 0, most = 0;
   for (int u = u_a; u < u_b; ++u) {
     bool bad;
-    mine += unit_of<NR>(p, groups, u, bad).tiles + kUnitCost;
+    const int cost = unit_of<NR>(p, groups, u, bad).tiles + kUnitCost;
+    mine += cost;
+    most = max(most, cost);
     if (bad && part == 0 && p.d_error) atomicOr(p.d_error, MLA_DEVERR_BAD_LENGTH);
   }
   int incl = mine;
@@ -521,18 +526,27 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
     const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
     if (lane >= o) incl += v;
   }
-  if (lane == 31) warp_sum[warp] = incl;
+  most = __reduce_max_sync(0xFFFFFFFFu, most);
+  if (lane == 31) warp_sum[warp] = incl, warp_most[warp] = most;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  int before = 0, total = 0;
-  for (int w = 0; w < kPagedThreads / 32; ++w) {
-    const int v = warp_sum[w];
-    if (w < warp) before += v;
-    total += v;
-  }
+  const bool is_warp = lane < kPagedThreads / 32;
+  const int sum = is_warp ? warp_sum[lane] : 0;
+  const int total = __reduce_add_sync(0xFFFFFFFFu, sum), before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? sum : 0);
+  most = __reduce_max_sync(0xFFFFFFFFu, is_warp ? warp_most[lane] : 0);
   {
     const int share = (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+    // Short units of about one length, no more than parts: one a part, for
+    // cutting them would cost more than it spreads.
+    const bool whole = units <= static_cast<int>(gridDim.x) && most <= share + kMergeCost;
+    if (whole && tid == 0 && part < units) {
+      bool bad;
+      cut[0] = part;
+      cut[1] = 0;
+      cut[2] = unit_of<NR>(p, groups, part, bad).tiles;
+      cut[3] = share;
+    }
     const int64_t from = static_cast<int64_t>(part) * share;
     const int g0 = static_cast<int>(min(from, static_cast<int64_t>(total)));
     const int g1 = static_cast<int>(min(from + share, static_cast<int64_t>(total)));
@@ -540,7 +554,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
     // in the unit whose last tile lies at or past g0; the thread that summed
     // that unit counts the run's tiles.
     const int excl = before + incl - mine;
-    if (g0 < g1 && excl <= g0 && g0 < excl + mine) {
+    if (!whole && g0 < g1 && excl <= g0 && g0 < excl + mine) {
       int at = excl, u = u_a;
       bool bad;
       int tiles = unit_of<NR>(p, groups, u, bad).tiles;
