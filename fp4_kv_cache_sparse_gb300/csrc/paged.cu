@@ -11,8 +11,9 @@
 // sequence; its items are the 128-token tiles that some row of it sees (the
 // tiles of the sinks and of the window only).  All units in order, each a
 // fixed cost and then its items, are cut into gridDim.x runs of equal cost, one
-// per CTA (one CTA per SM); the lengths are on the device, so every CTA derives
-// the cut itself by a scan over the units.  A unit cut by a run's end leaves
+// per CTA (one CTA per SM), or go whole to one CTA each where they are few and
+// short; the lengths are on the device, so every CTA derives the cut itself by a
+// scan over the units.  A unit cut by a run's end leaves
 // normalised fp32 partials, merged by a second kernel.
 //
 // One CTA, 20 warps with 32 rows, 28 with 16 or 64:
@@ -52,8 +53,8 @@
 // them.  So 32 x 16 heads over 64k tokens take 221 us (604 MB, 40 % of a copy's
 // bandwidth), 64 x 64 heads over 4k to 8k tokens 66 us (38.7 GFLOP, 31 % of the
 // bf16 rate), 32 x 2 x 128 heads with a window of 4096 108 us (35 %).  One tile
-// alone takes 8.5 us, 2.5 of them until the cut is known, 4 until the first
-// scores are there, and a merge 3 us more.
+// alone takes 8 us, 2 of them until the cut is known, 4 until the first scores
+// are there, and a merge 3 us more.
 //
 // Numbers.  e2m1 x e4m3 has at most 6 significant bits and lies in f16's
 // range, so K and V are exact in f16.  Q (bf16) is scaled by a power of two
@@ -81,10 +82,11 @@ constexpr int kPageBytes = kPage * kRecFp4;
 constexpr int kHalfBytes = kPage * 128;
 constexpr int kInfoRing = 8;
 constexpr uint64_t kPagedWaitNs = 2000000000ull;  // 2 s per wait
-// What a unit's Q and epilogue take, in tiles (104 sequences of 288 tokens, 64
-// heads: 23.2 us, 27.6 with nothing; 64 of up to 8k: 70.7, 76.8).
+// What a unit's Q and epilogue take, in tiles (64 sequences of up to 8k tokens,
+// 64 heads: 70.7 us, with nothing 76.8).
 constexpr int kUnitCost = 2;
-// What the partials and the merge of cut units take, in tiles.
+// What the partials and the merge of cut units take, in tiles (100 sequences of
+// 700 tokens, 64 heads: 29.7 us whole, 32.3 cut; 54 of 350, 22 heads: 16.8, 18.2).
 constexpr int kMergeCost = 3;
 // The running maximum may lag by 2^8: O is rescaled seldom (64 x 64 heads over
 // up to 8k tokens: 70 us, with a maximum that follows every tile 84).
@@ -130,7 +132,7 @@ struct PSmem {
   // float mb[NR], alpha[NR], scale[NR], linv[NR]; int hi[NR], lo[NR]; float red[4][NR]
   static constexpr int kInfoOff = kColOff + 10 * NR * 4;
   static constexpr int kMiscOff = kInfoOff + kInfoRing * 16;
-  static constexpr int kEnd = kMiscOff + 288;
+  static constexpr int kEnd = kMiscOff + 336;
   static constexpr int kAlloc = kEnd + 1024;
   static_assert(kAlloc <= 232448, "shared memory of one CTA");
   // Barrier indices.
@@ -487,6 +489,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
   int* cut = reinterpret_cast<int*>(smem + L::kMiscOff + 8);
   int* warp_sum = reinterpret_cast<int*>(smem + L::kMiscOff + 32);    // [warps]
   int* warp_most = reinterpret_cast<int*>(smem + L::kMiscOff + 160);  // [warps]
+  Unit* first_unit = reinterpret_cast<Unit*>(smem + L::kMiscOff + 288);  // the run's first
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
@@ -508,14 +511,24 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
   // beside the end of the stream's previous kernel, nothing after it does.
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
+        // A unit's Q arrives by TMA as bf16, K-major with 128-byte swizzle ...
+        const auto request_q = [&](int u) {
+          const int b = u / groups, y = b * p.rows + (u - b * groups) * NR;
+          expect_tx(&bars[L::bQRaw], L::kQBytes);
+  #pragma unroll 1
+          for (int c = 0; c < 8; ++c) tma_load_2d(sQ + c * (NR * 128), &q_map, c * 64, y, &bars[L::bQRaw]);
+        };
+
   // The cut: items of all units, this part's run, and the unit it begins in.
   const int units = p.batch * groups;
   const int per = (units + kPagedThreads - 1) / kPagedThreads;
   const int u_a = min(units, tid * per), u_b = min(units, u_a + per);
   int mine = 0, most = 0;
+  Unit unit{};  // this thread's last, which is its only one unless units are very many
   for (int u = u_a; u < u_b; ++u) {
     bool bad;
-    const int cost = unit_of<NR>(p, groups, u, bad).tiles + kUnitCost;
+    unit = unit_of<NR>(p, groups, u, bad);
+    const int cost = unit.tiles + kUnitCost;
     mine += cost;
     most = max(most, cost);
     if (bad && part == 0 && p.d_error) atomicOr(p.d_error, MLA_DEVERR_BAD_LENGTH);
@@ -540,13 +553,6 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
     // Short units of about one length, no more than parts: one a part, for
     // cutting them would cost more than it spreads.
     const bool whole = units <= static_cast<int>(gridDim.x) && most <= share + kMergeCost;
-    if (whole && tid == 0 && part < units) {
-      bool bad;
-      cut[0] = part;
-      cut[1] = 0;
-      cut[2] = unit_of<NR>(p, groups, part, bad).tiles;
-      cut[3] = share;
-    }
     const int64_t from = static_cast<int64_t>(part) * share;
     const int g0 = static_cast<int>(min(from, static_cast<int64_t>(total)));
     const int g1 = static_cast<int>(min(from + share, static_cast<int64_t>(total)));
@@ -554,24 +560,30 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
     // in the unit whose last tile lies at or past g0; the thread that summed
     // that unit counts the run's tiles.
     const int excl = before + incl - mine;
-    if (!whole && g0 < g1 && excl <= g0 && g0 < excl + mine) {
-      int at = excl, u = u_a;
+    if (whole ? u_a <= part && part < u_b : g0 < g1 && excl <= g0 && g0 < excl + mine) {
+      int at = excl, u = whole ? part : u_a;
       bool bad;
-      int tiles = unit_of<NR>(p, groups, u, bad).tiles;
-      while (at + kUnitCost + tiles <= g0) {
-        at += kUnitCost + tiles;
-        tiles = unit_of<NR>(p, groups, ++u, bad).tiles;
+      if (per > 1) unit = unit_of<NR>(p, groups, u, bad);
+      while (!whole && at + kUnitCost + unit.tiles <= g0) {
+        at += kUnitCost + unit.tiles;
+        unit = unit_of<NR>(p, groups, ++u, bad);
       }
-      const int k = max(g0 - at - kUnitCost, 0);
+      const int k = whole ? 0 : max(g0 - at - kUnitCost, 0);
+      int count = unit.tiles;
+      *first_unit = unit;
       cut[0] = u;
       cut[1] = k;
-      int count = max(min(at + kUnitCost + tiles, g1) - (at + kUnitCost + k), 0);
-      for (at += kUnitCost + tiles; at + kUnitCost < g1; at += kUnitCost + tiles) {
-        tiles = unit_of<NR>(p, groups, ++u, bad).tiles;
-        count += min(at + kUnitCost + tiles, g1) - (at + kUnitCost);
+      cut[3] = share;
+      if (!whole) {
+        int tiles = unit.tiles, next = u;
+        count = max(min(at + kUnitCost + tiles, g1) - (at + kUnitCost + k), 0);
+        for (at += kUnitCost + tiles; at + kUnitCost < g1; at += kUnitCost + tiles) {
+          tiles = unit_of<NR>(p, groups, ++next, bad).tiles;
+          count += min(at + kUnitCost + tiles, g1) - (at + kUnitCost);
+        }
       }
       cut[2] = count;
-      cut[3] = share;
+      if (count > 0) request_q(u);
     }
   }
   __syncthreads();
@@ -589,7 +601,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
       const bool mid = k > 0;  // the run begins inside its first unit
       const int u_first = u;
       bool bad_len;
-      Unit unit = unit_of<NR>(p, groups, u, bad_len);
+      Unit unit = *first_unit;
       int slot = 0;
       uint32_t parity = 1;
       for (uint32_t n = 0; n < items; ++n) {
@@ -860,20 +872,13 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
       const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
       const uint32_t tS = tmem + lanes + L::cS + c0, tO = tmem + lanes + L::cO;
 
-      // A unit's Q arrives by TMA as bf16, K-major with 128-byte swizzle ...
-      const auto request_q = [&](int u) {
-        const int b = u / groups, y = b * p.rows + (u - b * groups) * NR;
-        expect_tx(&bars[L::bQRaw], L::kQBytes);
-#pragma unroll 1
-        for (int c = 0; c < 8; ++c) tma_load_2d(sQ + c * (NR * 128), &q_map, c * 64, y, &bars[L::bQRaw]);
-      };
-      // ... and becomes scaled f16 in place, a row per warp at a time (lane =
+      // A unit's Q becomes scaled f16 in place, a row per warp at a time (lane =
       // 16 dims); rows past the unit's become zeros.
       uint32_t q_parity = 0;
-      const auto convert_q = [&](int u) {
+      const auto convert_q = [&](int u, bool first) {
         constexpr int kRowsAtOnce = NR == 16 ? 2 : 1;  // (registers)
         bool bad_len;
-        const Unit t = unit_of<NR>(p, groups, u, bad_len);
+        const Unit t = first ? *first_unit : unit_of<NR>(p, groups, u, bad_len);
         wait_for(&bars[L::bQRaw], q_parity, abort_flag, p.d_error);
         q_parity ^= 1;
         uint8_t* base = sQ + (lane >> 2) * (NR * 128);
@@ -934,8 +939,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
         }
       };
 
-      if (tid == 0) request_q(cut[0]);
-      convert_q(cut[0]);
+      convert_q(cut[0], true);
       float l[NC];
 #pragma unroll 1
       for (uint32_t n = 0; n < items; ++n) {
@@ -1091,7 +1095,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
         }
         named_bar_sync(1, kSoftmaxThreads);
         // The next unit's Q goes in while the last product runs (this piece's scores are all done).
-        if (n + 1 < items) convert_q(min(u + 1, units - 1));
+        if (n + 1 < items) convert_q(min(u + 1, units - 1), false);
         wait_for(&bars[L::bPFree + 1], n & 1, abort_flag, p.d_error);
         tc_fence_after();
         // Lane = dim, columns = rows.
