@@ -457,10 +457,9 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 // ------------------------------------------------------------------ the kernel
 
 template <int NR>
-__global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(const PagedParams p, const int groups,
-                                                                                const __grid_constant__ CUtensorMap q_map,
-                                                                                const __grid_constant__ CUtensorMap data_map,
-                                                                                const __grid_constant__ CUtensorMap scale_map) {
+__global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
+    paged_decode_kernel(const PagedParams p, const int groups, const __grid_constant__ CUtensorMap q_map,
+                        const __grid_constant__ CUtensorMap data_map, const __grid_constant__ CUtensorMap scale_map) {
   using L = PSmem<NR>;
   constexpr int NC = NR / L::kSides;    // rows of a softmax thread
   constexpr bool kKeep = NR == 16;
@@ -742,7 +741,8 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1) paged_decode_kernel(co
       const int qq = (warp - kVWarp0) & 3;
       const int tok = lane & 7, piece = lane >> 3;
       const int first = ((warp - kVWarp0) >> 2) * (L::kVTokens / kShare) + tok;  // this lane's first record of a unit
-      const uint32_t rows = smem_u32(sRaw) + (qq >> 1) * kHalfBytes + first * 128 + ((((qq & 1) * 4 + piece) ^ tok) * 16);
+      const uint32_t rows =
+          smem_u32(sRaw) + (qq >> 1) * kHalfBytes + first * 128 + ((((qq & 1) * 4 + piece) ^ tok) * 16);
       const uint32_t scales = smem_u32(sRaw) + 2 * kHalfBytes + first * 32 + ((qq * 8 + piece * 2) ^ ((tok & 4) * 4));
       const uint32_t dst = smem_u32(sV) + qq * L::kVUnitBytes + (piece >> 1) * (L::kVTokens * 128) + first * 128;
       // The lane's first 16-byte unit of a 128-byte row, swizzled; unit j is at this ^ 16 j.
@@ -1283,8 +1283,8 @@ cudaError_t launch(PagedParams p, const PagedPlan& plan, cudaStream_t stream) {
   if (enc(&data_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(p.kv), kv_dims, kv_strides, data_box, estr,
           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
-      enc(&scale_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(p.kv), kv_dims, kv_strides, scale_box, estr,
-          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+      enc(&scale_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(p.kv), kv_dims, kv_strides, scale_box,
+          estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
   // Both kernels are programmatic dependents: each may be scheduled while the
@@ -1328,7 +1328,7 @@ PagedPlan paged_plan(const mla_paged_problem_t* p, int num_parts) {
   // 20.4 by 32, 26.3 by 64; 2 of 446, 128 heads: 13.9 by 16, 18.4 by 64).
   int64_t tiles = (p->max_pages + 1) / 2;
   if (p->window > 0) {
-    const int64_t seen = (static_cast<int64_t>(p->window) + p->seq_len_q) / kTile + 2 + (p->sinks + kTile - 1ll) / kTile;
+    const int64_t seen = (int64_t(p->window) + p->seq_len_q) / kTile + 2 + (p->sinks + kTile - 1ll) / kTile;
     if (seen < tiles) tiles = seen;
   }
   const auto fits = [&](int nr) {
