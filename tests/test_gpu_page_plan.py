@@ -180,3 +180,22 @@ def test_slots_at_odd_addresses():
     want = reference(cached, new, table, list(free), nf, total + 3, num_pages)
     assert slots.tolist() == want[3] and pos.tolist() == want[4]
     assert big[0, 0] == -9 and torch.all(big[0, total + 4:] == -9) and torch.all(big[1, :3] == -9)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_long_maps(in_place):
+    """Maps long enough for a kernel of their own: whole, refused, and with a bad page in the stack."""
+    cached, new, table, free, nf, num_pages = make(20, 40, 300, lambda r: r.choice([-1, 0, 1, 9000, 16000]),
+                                                   cached_of=lambda: 70)
+    total = sum(max(n, 0) for n in new)
+    assert total > 98304
+    for max_new in (total, total + 7):
+        got, err = run(cached, new, table, list(free), nf, max_new, in_place)
+        assert err == 0 and list(got) == list(reference(cached, new, table, list(free), nf, max_new, num_pages))
+    got, err = run(cached, new, table, list(free), nf, total - 1, in_place)
+    assert err == mla.DEVERR_NO_ROOM and got[2] == [0] * 41 and got[5] == table and got[6] == free
+    assert got[0] == cached and got[1] == nf and got[3] == [-1] * (total - 1) and got[4] == [0] * (total - 1)
+    free[nf - 5] = num_pages
+    got, err = run(cached, new, table, list(free), nf, total, in_place)
+    want = reference(cached, new, table, list(free), nf, total, num_pages)
+    assert err == mla.DEVERR_BAD_INDEX and got[3] == want[3] and got[4] == want[4] and -1 in got[3]

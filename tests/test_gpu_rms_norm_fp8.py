@@ -176,3 +176,17 @@ def test_streams_graphs_and_refusals():
         mla.rms_norm_fp8(x, w, 1e-6, codes, scales.view(torch.int8))
     with pytest.raises(mla.MLAError):
         mla.rms_norm_fp8(x[:, 1:481], w[1:481].clone(), 1e-6, codes[:, :480], scales[:, :15])   # rows off 16 bytes
+
+
+@pytest.mark.parametrize("d", [512, 8224])
+def test_offsets_beyond_32_bits(d):
+    """Rows whose element offsets pass 2^31 (4.8 GB of bf16, of which little is touched)."""
+    wide = torch.empty(600, 1 << 22, dtype=torch.bfloat16, device=DEV)
+    x, r, w = inputs(600, d, torch.bfloat16, seed=22)
+    a, b = wide[:, 64:64 + d], wide[:, 1 << 20:(1 << 20) + d]
+    a.copy_(x)
+    b.copy_(r)
+    codes = torch.empty(600, d, dtype=torch.uint8, device=DEV)
+    scales = torch.empty(600, d // 32, dtype=torch.uint8, device=DEV)
+    mla.rms_norm_fp8(a, w, 1e-6, codes, scales, residual=b, residual_out=b)
+    verify(x, r, w, 1e-6, codes, scales, b)

@@ -177,3 +177,14 @@ def test_empty_and_refused():
         mla.rope(x[:, :1].expand(4, 2, 64), pos, table)     # heads that share memory, in place
     with pytest.raises(ValueError):
         mla.rope(x.double(), pos, table)
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
+def test_offsets_beyond_32_bits(interleaved):
+    """Rows whose element offsets pass 2^31 (4.8 GB of bf16, of which little is touched)."""
+    wide = torch.empty(600, 1 << 22, dtype=torch.bfloat16, device=DEV)
+    x, pos = inputs(600, 3, 64, torch.bfloat16, seed=21)
+    view = wide.as_strided((600, 3, 64), (1 << 22, 128, 1))
+    view.copy_(x)
+    table = mla.RopeTable(64, interleaved=interleaved)
+    check(mla.rope(view, pos, table), *reference(x, pos, table, interleaved))
