@@ -154,6 +154,18 @@ def test_many_query_tokens_of_one_sequence():
     c.check(out, lse, 33, 2)
 
 
+@pytest.mark.parametrize("b,h", [(1000, 16), (950, 32), (500, 128)])
+@pytest.mark.parametrize("num_sms", [0, 7, 1500])
+def test_more_units_than_threads(b, h, num_sms):
+    """Units that the threads of a block share several to one; with 1500 parts, one unit to a part."""
+    lens = [(37 * r) % 140 if r % 5 else 0 for r in range(b)]
+    lens[b // 2] = 900
+    c = Case(lens, 1, h, seed=b)
+    out, lse, err = c.run(num_sms=num_sms)
+    assert err == 0
+    c.check(out, lse)
+
+
 def test_one_long_sequence_is_split_and_merged():
     c = Case([20011], 1, 16, seed=8)
     out, lse, err = c.run()
