@@ -16,15 +16,15 @@
 // scan over the units.  A unit cut by a run's end leaves
 // normalised fp32 partials, merged by a second kernel.
 //
-// One CTA, 20 warps with 32 rows, 28 with 16 or 64:
+// One CTA, 28 warps:
 //   softmax (8; 16 with 64 rows)  thread = token x some of the rows: scale,
 //                      mask, lazy running maximum, P^T to shared memory, row
 //                      sums in registers; at a unit's end the epilogue, before
 //                      it the next unit's Q.
-//   K decode (4; 8 with 16 rows)  raw FP4 -> f16 into tensor memory, lane =
+//   K decode (8; 4 with 64 rows)  raw FP4 -> f16 into tensor memory, lane =
 //                      token: the A operand of S^T = K Q^T, a 128-dim quarter
 //                      at a time.
-//   V decode (4; 8 with 16 rows)  raw FP4 -> f16 into shared memory (128-byte
+//   V decode (8; 4 with 64 rows)  raw FP4 -> f16 into shared memory (128-byte
 //                      swizzle), a dim quarter each, in units of 64 tokens (32
 //                      with 64 rows): the MN-major A operand of
 //                      O^T += V^T P^T.
@@ -101,9 +101,9 @@ struct PSmem {
   static constexpr int kSides = NR == 64 ? 4 : 2;
   static constexpr int kSoftmaxWarps = 4 * kSides;
   // Decode warps of each kind: eight hide more latency (16 heads over 64k
-  // tokens: 223 us against 253), but with more rows the softmax needs more
-  // registers than that many warps leave it.
-  static constexpr int kDecodeWarps = NR == 16 ? 8 : 4;
+  // tokens: 223 us against 253; 32 over 16k: 74.5 against 80.3), but with 64
+  // rows the softmax has twice the warps and no registers are left for more.
+  static constexpr int kDecodeWarps = NR == 64 ? 4 : 8;
   static constexpr int kKWarp0 = kSoftmaxWarps, kVWarp0 = kKWarp0 + kDecodeWarps, kLoadWarp = kVWarp0 + kDecodeWarps;
   static constexpr int kScoreWarp = kLoadWarp + 1, kValueWarp0 = kScoreWarp + 1;
   static constexpr int kValueWarps = 2;
@@ -224,7 +224,7 @@ __device__ __forceinline__ bool token_there(int info, int row) {
 
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
-  static_assert(N == 8 || N == 16 || N == 32, "columns");
+  static_assert(N == 8 || N == 16, "columns");
   if constexpr (N == 8) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
@@ -232,20 +232,8 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
         : "r"(taddr)
         : "memory");
-  } else if constexpr (N == 16) {
-    tmem_ld16(taddr, r);
   } else {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,"
-        "%29,%30,%31}, [%32];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr)
-        : "memory");
+    tmem_ld16(taddr, r);
   }
 }
 
@@ -463,7 +451,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
   using L = PSmem<NR>;
   constexpr int NC = NR / L::kSides;    // rows of a softmax thread
   constexpr bool kKeep = NR == 16;
-  constexpr int HC = NR == 16 ? 8 : 16;  // of which it works on so many at a time
+  constexpr int HC = NR == 64 ? 16 : 8;  // of which it works on so many at a time (registers)
   constexpr int kPagedThreads = L::kThreads, kSoftmaxWarps = L::kSoftmaxWarps;
   constexpr int kKWarp0 = L::kKWarp0, kVWarp0 = L::kVWarp0, kLoadWarp = L::kLoadWarp;
   constexpr int kScoreWarp = L::kScoreWarp, kValueWarp0 = L::kValueWarp0;
@@ -987,7 +975,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
         }
         if (any_of(2, kSoftmaxThreads, top > kSlack + kPBias)) {
           // Exact maxima of the tile's rows.
-#pragma unroll
+#pragma unroll 1
           for (int h = 0; h < NC; h += HC) {
             float y[HC];
             exponents(s_col, h, y, false);
@@ -1099,7 +1087,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
         wait_for(&bars[L::bPFree + 1], n & 1, abort_flag, p.d_error);
         tc_fence_after();
         // Lane = dim, columns = rows.
-        constexpr int EC = NR == 32 ? 32 : 16;  // columns at a time (registers)
+        constexpr int EC = 16;  // columns at a time (registers)
 #pragma unroll 1
         for (int i = side; i < 4 * (NR / EC); i += L::kSides) {
           const int qq = i / (NR / EC), cc = (i % (NR / EC)) * EC;
@@ -1319,7 +1307,7 @@ PagedPlan paged_plan(const mla_paged_problem_t* p, int num_parts) {
   PagedPlan pl{};
   const int64_t rows = static_cast<int64_t>(p->seq_len_q) * p->h_q;
   // Rows of a unit: as few as hold them all, for a tile's decode is most of its
-  // cost (32 sequences of 8k tokens, 24 heads: 46.8 us by 32, 55.6 by 64, 65.8
+  // cost (32 sequences of 8k tokens, 24 heads: 43.5 us by 32, 55.6 by 64, 65.8
   // by 16; 64 heads: 57.4 by 64, 79.5 by 32; 32 of 64k, 16 heads: 222 by 16, 270
   // by 32).  Where the lengths that the table and the window allow leave no
   // part more than three or four tiles even so, as few as that takes: the start
