@@ -60,9 +60,9 @@
 // range, so K and V are exact in f16.  Q (bf16) is scaled by a power of two
 // per row to put its largest value in [2^14, 2^15) and is then exact in f16
 // down to 2^-28 of that; below, 2^-39 of the row's largest value is lost.  P
-// is f16 with the maximum at 2^7 (at most 2^15 with the lazy maximum's slack
-// of 2^8): 11 bits, where bf16 has 8, and weights down to 2^-31 of the
-// largest still count.  Sums, maxima and O are fp32.
+// is f16 with the maximum at 2^5 (at most 2^15 with the lazy maximum's slack
+// of 2^10): 11 bits down to 2^-19 of the largest weight, where bf16 has 8, and
+// weights down to 2^-29 of it still count.  Sums, maxima and O are fp32.
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -88,10 +88,11 @@ constexpr int kUnitCost = 2;
 // What the partials and the merge of cut units take, in tiles (100 sequences of
 // 700 tokens, 64 heads: 29.7 us whole, 32.3 cut; 54 of 350, 22 heads: 16.8, 18.2).
 constexpr int kMergeCost = 3;
-// The running maximum may lag by 2^8: O is rescaled seldom (64 x 64 heads over
-// up to 8k tokens: 70 us, with a maximum that follows every tile 84).
-constexpr float kSlack = 8.f;
-constexpr float kPBias = 7.f;                // P of the maximum is 2^7
+// The running maximum may lag by 2^10: O is rescaled seldom (32 x 2 x 128 heads,
+// window 4096: 104.9 us, 109.3 with 2^8; with none 64 x 64 heads took 84 us
+// instead of 70).  P has room for that and for 5 bits above 1.
+constexpr float kSlack = 10.f;
+constexpr float kPBias = 5.f;                // P of the maximum is 2^5
 constexpr float kNoMax = -3.0e38f;           // running maximum before any visible token
 
 template <int NR>
@@ -462,7 +463,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
   uint8_t* sP = smem + L::kPOff;
   uint8_t* sRaw = smem + L::kRawOff;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
-  float* c_mb = reinterpret_cast<float*>(smem + L::kColOff);  // m - 7
+  float* c_mb = reinterpret_cast<float*>(smem + L::kColOff);  // m - kPBias
   float* c_alpha = c_mb + NR;
   float* c_scale = c_alpha + NR;
   float* c_linv = c_scale + NR;
@@ -679,7 +680,6 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
       // 128-dim quarter; of eight, two teams take quarters in turn.  (What
       // stands in rows past the visible tokens only makes masked scores.)
       constexpr int kTeams = L::kDecodeWarps / 4;
-      constexpr int kHalves = kTeams == 2 ? 1 : 2;  // unrolled where one team has to cover its own latency
       const int quad = warp & 3, team = (warp - kKWarp0) >> 2;
       const uint32_t tK = tmem + (static_cast<uint32_t>(quad * 32) << 16) + L::cK;
       const int row = (quad & 1) * 32 + lane;  // of the page
@@ -701,7 +701,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
           wait_for(&bars[L::bKFree + ks], parity ^ 1, abort_flag, p.d_error);
           tc_fence_after();
           const uint32_t t = tK + ks * 64;
-#pragma unroll kHalves
+#pragma unroll 1
           for (int hh = 0; hh < 2; ++hh) {
             const uint32_t s = hh ? sc.y : sc.x;
             uint32_t o[16];
@@ -911,7 +911,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
         named_bar_sync(1, kSoftmaxThreads);  // the row arrays are complete
       };
       // This thread's exponents of rows h .. h + HC - 1 in an item, scale *
-      // score - (m - 7), or its scaled scores themselves (against_max false).
+      // score - (m - kPBias), or its scaled scores themselves (against_max false).
       const auto exponents = [&](uint32_t s_col, int h, float (&y)[HC], bool against_max) {
         uint32_t r[HC];
         tmem_ld<HC>(s_col + h, r);
