@@ -51,8 +51,8 @@
 // with 64 rows 5520 (3470 and 2050), in 4250 and 6130 cycles: nine tenths of
 // what shared memory can do, and the tensor core is busy for 510 and 2050 of
 // them.  So 32 x 16 heads over 64k tokens take 221 us (604 MB, 40 % of a copy's
-// bandwidth), 64 x 64 heads over 4k to 8k tokens 66 us (38.7 GFLOP, 31 % of the
-// bf16 rate), 32 x 2 x 128 heads with a window of 4096 108 us (35 %).  One tile
+// bandwidth), 64 x 64 heads over 4k to 8k tokens 64 us (38.7 GFLOP, 32 % of the
+// bf16 rate), 32 x 2 x 128 heads with a window of 4096 107 us (35 %).  One tile
 // alone takes 8 us, 2 of them until the cut is known, 4 until the first scores
 // are there, and a merge 3 us more.
 //
