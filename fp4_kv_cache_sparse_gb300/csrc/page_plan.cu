@@ -9,8 +9,8 @@
 // slot map is written by the same 8192 threads, each finding its tokens'
 // request by a binary search of the prefix in shared memory; a long one by a
 // second kernel over the whole GPU, from the tables and lengths that the first
-// has left (1000 requests: 512,000 slots 27.3 us in the cluster, 12.6 us so;
-// 64,000 slots 10.7 against 12.3).  One decode step of 256 requests takes 5.7
+// has left (1000 requests: 512,000 slots 24.6 us in the cluster, 10.4 us so;
+// 64,000 slots 8.5 against 10.3).  One decode step of 256 requests takes 5.5
 // us: latency alone, a launch, three dependent trips to memory and three
 // barriers.
 #include <cstdint>
@@ -187,30 +187,40 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kPlanThreads)
   }
   __syncthreads();
 
-  const int warp = rank * (kPlanThreads / 32) + (tid >> 5), lane = tid & 31;
-  constexpr int kWarps = kCtas * kPlanThreads / 32;
-  if (ok && total.give > 0) {
-    for (int r = warp; r < batch; r += kWarps) {
-      const int32_t g0 = s_give[r], n = s_give[r + 1] - g0;
-      for (int k = lane; k < n; k += 32) free_pages[nf + g0 + k] = block_table[static_cast<int64_t>(r) * max_pages + k];
+  // A warp to each request where that takes one round of a few pages; else a
+  // thread to each page, its request found by a search (256 requests of one
+  // token: 5.5 us by warps, 5.8 by pages; 1000 of up to 512 tokens: 12.7 and 10.3;
+  // 4 of 50,000: 9.9 and 6.1; 500 of which 250 end: 11.3 and 12.4).
+  const int gtid = rank * kPlanThreads + tid, lane = tid & 31, warp = gtid >> 5;
+  constexpr int kAll = kCtas * kPlanThreads;
+  const bool by_warp = batch <= kAll / 32 && s_give[batch] + s_take[batch] <= 32 * batch;
+  if (by_warp) {
+    if (warp < batch) {
+      const int32_t g0 = s_give[warp], n = s_give[warp + 1] - g0;
+      for (int k = lane; k < n; k += 32)
+        free_pages[nf + g0 + k] = block_table[static_cast<int64_t>(warp) * max_pages + k];
+    }
+  } else {
+    for (int32_t i = gtid; i < s_give[batch]; i += kAll) {
+      const int r = request_of(s_give, batch, i);
+      free_pages[nf + i] = block_table[static_cast<int64_t>(r) * max_pages + (i - s_give[r])];
     }
   }
   // Everyone has read the old lengths and the pushed pages are visible.
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 
   bool bad_page = false;
-  for (int r = warp; r < batch; r += kWarps) {
-    const int32_t t0 = s_take[r], n = s_take[r + 1] - t0;
-    const int32_t held = pages_of(s_len[r]);
-    for (int k = lane; k < n; k += 32) {
-      const int32_t page = free_pages[top - 1 - (t0 + k)];
-      const bool good = page >= 0 && page < num_pages;
-      bad_page |= !good;
-      block_table[static_cast<int64_t>(r) * max_pages + held + k] = page;
-    }
+  const auto take = [&](int r, int32_t i) {  // page i of all goes to request r
+    const int32_t page = free_pages[top - 1 - i];
+    bad_page |= page < 0 || page >= num_pages;
+    block_table[static_cast<int64_t>(r) * max_pages + pages_of(s_len[r]) + (i - s_take[r])] = page;
+  };
+  if (by_warp) {
+    if (warp < batch)
+      for (int32_t i = s_take[warp] + lane; i < s_take[warp + 1]; i += 32) take(warp, i);
+  } else {
+    for (int32_t i = gtid; i < s_take[batch]; i += kAll) take(request_of(s_take, batch, i), i);
   }
-  const int gtid = rank * kPlanThreads + tid;
-  constexpr int kAll = kCtas * kPlanThreads;
   for (int r = gtid; r < batch; r += kAll) {
     seq_lens[r] = ok ? (new_lens[r] < 0 ? 0 : s_len[r] + s_cu[r + 1] - s_cu[r]) : s_len[r];
     cu_new[r] = s_cu[r];
