@@ -1023,6 +1023,11 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
                 tmem_st16(tO + qq * NR + cc, o);
               }
               tmem_wait_st();
+              // A product adds to all lanes of O^T, and the first half's needs the P of two lane quadrants only: no
+              // warp hands its P over before every quadrant is rescaled.
+              tc_fence_before();
+              named_bar_sync(1, kSoftmaxThreads);
+              tc_fence_after();
             }
           }
         }

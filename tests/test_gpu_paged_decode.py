@@ -190,6 +190,28 @@ def test_maxima_that_grow_from_tile_to_tile():
         c.check(out, lse)
 
 
+@pytest.mark.parametrize("s,h", [(1, 16), (2, 16), (1, 64), (2, 64)])      # 16, 32, 64 and twice 64 rows
+def test_maxima_that_outgrow_the_slack_in_every_tile(s, h):
+    """Each tile's scores top the last one's by 12 powers of two and more, so O is rescaled in every tile of every
+    unit, between products that add to it: many units at once, the same bits from run to run."""
+    b, tiles = 40, 20
+    c = Case([tiles * 128 - 7 * r for r in range(b)], s, h, seed=21)
+    for r, n in enumerate(c.lens):
+        pages = c.table[r, : -(-n // 64)].long()
+        flat = c.kv[pages].reshape(-1, 288)
+        flat[:n, :8] = 0x77                          # sixes in dims 0 .. 15, under the next larger E4M3 scale in each tile
+        flat[:n, 256] = (0x38 + torch.arange(n, device=DEV) // 128).to(torch.uint8)
+        c.kv[pages] = flat.view(-1, 64, 288)
+    # 12 ln 2 between the scales 1 and 1.125, more between larger ones.
+    c.q[..., :16] = 12 * 0.6931471805599453 * 8 / 96 * 512 ** 0.5
+    first = c.run()
+    assert first[2] == 0
+    c.check(*first[:2])
+    for _ in range(20):
+        out, lse, err = c.run()
+        assert err == 0 and torch.equal(out, first[0]) and torch.equal(lse, first[1])
+
+
 def test_large_and_small_queries_and_scales():
     for qscale, top, sm in ((2.0 ** 20, 0x10, 2.0 ** -22), (2.0 ** -60, 0x7F, 1.0), (1e30, 0x30, 1e-31), (1.0, 0x7F, 1e-4)):
         c = Case([130, 7], 2, 18, seed=5, qscale=qscale, records=lambda n, g: random_records(n, g, top))
