@@ -10,10 +10,9 @@
 // once for sixteen values; products and sums go two values to an instruction.
 // Rows of up to 512 dims belong to a warp, longer ones to as many warps as
 // give each thread sixteen values.
-// Long rows are bound by HBM (8191 x 8192 bf16 with a residual: 83.8 us, 469
+// Long rows are bound by HBM (8191 x 8192 bf16 with a residual: 83.4 us, 471
 // MB, 83 % of a copy's bandwidth); short ones by instructions (200,000 x 512
-// fp16: 58.6 us, 311 MB, 78 %; 68.7 us with eight values a lane and scalar
-// arithmetic).
+// fp16: 60.4 us, 311 MB, 76 %).
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -90,20 +89,37 @@ struct Eight<__nv_bfloat16> : Eight16<__nv_bfloat16> {
 // pieces 0 and 2, the odd one 1 and 3: each access of the two is 32 contiguous bytes.
 __device__ __forceinline__ int first_of(int at, int i) { return (at >> 1) * 32 + i * 16 + (at & 1) * 8; }
 
-// Half a block: v holds weight * s of its 16 values, and 1 / rms is applied
-// with the block's scale.  Lanes 2 i and 2 i + 1 hold a block; both are inside
-// the row or both past it.
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+  float r;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Half a block: 16 values of s and their weights.  Lanes 2 i and 2 i + 1 hold a
+// block; both are inside the row or both past it.
+//
+// s / rms lies within sqrt(dim), so in this order only v itself can leave the
+// range of 32 bits.  (weight * s can where v does not, and so can 1 / rms with
+// the block's scale in one factor, which beside zeros gives NaN; that saved a
+// product a value, 57.8 us for 200,000 x 512.)
+template <typename T>
 __device__ __forceinline__ void store_half_block(const NormParams& p, int64_t row, int at, bool in,
-                                                 const float2 (&v)[2][4], float inv) {
+                                                 const float2 (&s)[2][4], const Eight<T> (&weight)[2], float inv) {
+  float2 v[2][4];
   float amax = 0.f;
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < 2; ++i) {
+    weight[i].get(v[i]);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) amax = fmaxf(amax, fmaxf(fabsf(v[i][k].x), fabsf(v[i][k].y)));
+    for (int k = 0; k < 4; ++k) {
+      v[i][k] = __fmul2_rn(__fmul2_rn(s[i][k], make_float2(inv, inv)), v[i][k]);
+      amax = max_abs(amax, v[i][k].x, v[i][k].y);
+    }
+  }
   amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
   if (!in) return;
-  const int e = fp8_block_exponent(amax * inv);
-  const float up = inv * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // 2^-e exactly: e is -127 .. 120
+  const int e = fp8_block_exponent(amax);
+  const float up = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // 2^-e exactly: e is -127 .. 120
   uint32_t c[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -228,14 +244,7 @@ __global__ void __launch_bounds__(threads_of<kTeam>(), resident_of<kTeam>())
     request(row + stages * stride, slot);
     if (++slot == stages) slot = 0, parity ^= 1;
     const float inv = rsqrtf(fmaf(sum, inv_dim, p.eps));
-    float2 v[2][4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      w[i].get(v[i]);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[i][k] = __fmul2_rn(v[i][k], s[i][k]);
-    }
-    store_half_block(p, row, at, live && inside, v, inv);
+    store_half_block(p, row, at, live && inside, s, w, inv);
   }
   // After a wait that gave up: what is still on its way gets another while to land.
   if (gave_up) {
@@ -291,17 +300,11 @@ __global__ void __launch_bounds__(512) rms_norm_fp8_long_kernel(const NormParams
   for (int j = 0; j < kPieces; ++j) {
     const int at = tid + j * kTeam;
     const bool in = at < p.dim / 16;
-    float2 v[2][4] = {};
+    Eight<T> w[2] = {};
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (!in) continue;
-      Eight<T> w;
-      w.load(static_cast<const T*>(p.weight) + first_of(at, i));
-      w.get(v[i]);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[i][k] = __fmul2_rn(v[i][k], s[j][i][k]);
-    }
-    store_half_block(p, row, at, in, v, inv);
+    for (int i = 0; i < 2; ++i)
+      if (in) w[i].load(static_cast<const T*>(p.weight) + first_of(at, i));
+    store_half_block(p, row, at, in, s[j], w, inv);
   }
 }
 

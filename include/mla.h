@@ -397,7 +397,9 @@ mla_status_t mla_rope(int32_t dtype, const void* x, int64_t x_row_stride, int64_
  *   dim       a multiple of 32, at most 16384 (MLA_ERR_UNSUPPORTED otherwise).
  *   d_error   device int32 or NULL; bits are OR-ed into it (MLA_DEVERR_TIMEOUT
  *             when a row's copy did not arrive: that row is not written).
- * Infinities and NaN in a row make that row's codes undefined; no other row.
+ * Infinities and NaN in a row make that row's codes undefined, and so does a
+ * mean(s^2) + eps that fp32 cannot hold (0, as of a row of zeros with eps = 0,
+ * or a sum of squares past 3.4e38); no other row.
  */
 mla_status_t mla_rms_norm_fp8(int32_t dtype, const void* x, int64_t x_stride, const void* residual,
                               int64_t residual_stride, const void* weight, float eps, void* residual_out,

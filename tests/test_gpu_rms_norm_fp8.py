@@ -107,6 +107,36 @@ def test_very_small_and_large_values():
     verify(x * 2.0 ** -120, None, w, 1.0, codes, scales, None)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d", [512, 1024, 8192, 8224])            # a warp a row, more of them, a block, the long rows
+@pytest.mark.parametrize("res", [False, True])
+def test_blocks_of_tiny_values_beside_zeros(dtype, d, res):
+    """Blocks whose values times 1 / rms are normal numbers, though 1 / rms times the block's scale is not."""
+    x = torch.full((6, d), 0.3, dtype=dtype, device=DEV)
+    x[:, 32:64] = 0.0
+    x[0, 40] = 1e-37                                  # scale clamped
+    x[1, 32:64:3] = -4e-37
+    x[2, 63] = 6e-36
+    x[3:] = 0.0
+    x[3, 37] = 1e-37                                  # the row's only value: 1 / rms is 1000
+    x[4, 33], x[4, d - 1] = 3e-35, -2e-37
+    x[5, ::2] = 7e-37
+    r = torch.zeros_like(x) if res else None
+    w = torch.linspace(0.5, 2.0, d, device=DEV).to(dtype)
+    codes, scales = run(x, r, w)
+    assert not torch.any((codes & 0x7F) == 0x7F)      # no NaN
+    assert torch.all(codes[x == 0] & 0x7F == 0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d", [512, 8224])
+def test_weights_whose_product_with_the_row_leaves_the_range(dtype, d):
+    """s w overflows or vanishes in 32 bits, s / rms w does not."""
+    x, _, w = inputs(5, d, torch.float32, seed=23, spread=0.0)
+    for rows, weights, eps in ((1e15, 1e30, 1e-6), (1e-12, 1e-30, 1e-30), (1e-15, 1e-33, 0.0)):
+        run((x * rows).to(dtype), None, (w * weights).to(dtype), eps=eps)
+
+
 def test_a_row_of_infinities_or_nan_spoils_no_other():
     x, r, w = inputs(20, 512, torch.bfloat16, seed=6)
     clean = run(x, r, w)
