@@ -50,9 +50,9 @@
 // accesses of 128 bytes a tile (2580 by the warps, 1280 by the tensor core),
 // with 64 rows 5520 (3470 and 2050), in 4250 and 6130 cycles: nine tenths of
 // what shared memory can do, and the tensor core is busy for 510 and 2050 of
-// them.  So 32 x 16 heads over 64k tokens take 221 us (604 MB, 40 % of a copy's
-// bandwidth), 64 x 64 heads over 4k to 8k tokens 64 us (38.7 GFLOP, 32 % of the
-// bf16 rate), 32 x 2 x 128 heads with a window of 4096 107 us (35 %).  One tile
+// them.  So 32 x 16 heads over 64k tokens take 222 us (604 MB, 40 % of a copy's
+// bandwidth), 64 x 64 heads over 4k to 8k tokens 63 us (38.7 GFLOP, 32 % of the
+// bf16 rate), 32 x 2 x 128 heads with a window of 4096 106 us (35 %).  One tile
 // alone takes 8 us, 2 of them until the cut is known, 4 until the first scores
 // are there, and a merge 3 us more.
 //
@@ -93,7 +93,7 @@ constexpr int kMergeCost = 3;
 // instead of 70).  P has room for that and for 5 bits above 1.
 constexpr float kSlack = 10.f;
 constexpr float kPBias = 5.f;                // P of the maximum is 2^5
-constexpr float kNoMax = -3.0e38f;           // running maximum before any visible token
+constexpr float kNoMax = -3.0e38f;           // running maximum, unscaled, before any visible token
 
 template <int NR>
 struct PSmem {
@@ -130,8 +130,8 @@ struct PSmem {
   static constexpr int kBarOff = kRawOff + kRaw * kPageBytes;
   static constexpr int kNumBars = 2 * kRaw + 2 * kKRing + 2 * kVRing + 8 + 4 + kInfoRing;
   static constexpr int kColOff = (kBarOff + kNumBars * 8 + 15) & ~15;  // per-row arrays
-  // float mb[NR], alpha[NR], scale[NR], linv[NR]; int hi[NR], lo[NR]; float red[4][NR]
-  static constexpr int kInfoOff = kColOff + 10 * NR * 4;
+  // float minus_m[NR], minus_most[NR], alpha[NR], scale[NR], linv[NR]; int hi[NR], lo[NR]; float red[4][NR]
+  static constexpr int kInfoOff = kColOff + 11 * NR * 4;
   static constexpr int kMiscOff = kInfoOff + kInfoRing * 16;
   static constexpr int kEnd = kMiscOff + 336;
   static constexpr int kAlloc = kEnd + 1024;
@@ -463,8 +463,9 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
   uint8_t* sP = smem + L::kPOff;
   uint8_t* sRaw = smem + L::kRawOff;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
-  float* c_mb = reinterpret_cast<float*>(smem + L::kColOff);  // m - kPBias
-  float* c_alpha = c_mb + NR;
+  float* c_minus_m = reinterpret_cast<float*>(smem + L::kColOff);  // minus the running maximum of the unscaled scores
+  float* c_minus_most = c_minus_m + NR;  // minus the largest score that P has room for under that maximum
+  float* c_alpha = c_minus_most + NR;
   float* c_scale = c_alpha + NR;
   float* c_linv = c_scale + NR;
   int* c_hi = reinterpret_cast<int*>(c_linv + NR);
@@ -860,6 +861,12 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
       const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
       const uint32_t tS = tmem + lanes + L::cS + c0, tO = tmem + lanes + L::cO;
 
+      // The largest score whose exponent is within the slack, rounded down: with
+      // 32 rows and more, whose exponents are computed again for P, comparing
+      // scores with it takes one sum each (32 x 2 x 128 heads, window 4096: 105.5
+      // us, 107.5 with whole exponents).
+      const auto most_under = [](float m, float scale) { return __fadd_rd(m, __fdividef(kSlack, scale)); };
+
       // A unit's Q becomes scaled f16 in place, a row per warp at a time (lane =
       // 16 dims); rows past the unit's become zeros.
       uint32_t q_parity = 0;
@@ -887,16 +894,19 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
           const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, max(two >> 16, two & 0xFFFFu)) >> 7;
           // Largest value to [2^14, 2^15); nothing to scale in a row of zeros or of infinities.
           const int e = top == 0 || top == 255 ? 0 : max(static_cast<int>(top) - 127 - 14, -100);
-          const float up = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+          // A negative scale's sign goes into Q, so that the largest product is the largest score.
+          const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 - e) << 23), p.scale_log2);
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             wv[k] = pack_f16x2(__uint_as_float(wv[k] << 16) * up, __uint_as_float(wv[k] & 0xFFFF0000u) * up);
           *pa = make_uint4(wv[0], wv[1], wv[2], wv[3]);
           *pb = make_uint4(wv[4], wv[5], wv[6], wv[7]);
           if (lane == 0) {
-            // Never 0, so that an infinite score stays infinite (scores are below 2^36).
-            const float s = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+            // Never 0 or infinite, so that no score times it is NaN (scores are below 2^36).
+            const float s = fminf(fabsf(p.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 + e) << 23), 3.0e38f);
             c_scale[r] = s == 0.f ? 1e-30f : s;
+            c_minus_m[r] = -kNoMax;
+            c_minus_most[r] = -most_under(kNoMax, c_scale[r]);
           }
         }
         fence_proxy_async_smem();
@@ -904,26 +914,29 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
         if (lane == 0) mbar_arrive(&bars[L::bQFull]);
         if (tid < NR) {
           const int hi = t.first + min(t.row0 + tid, p.rows - 1) / p.h;
-          c_mb[tid] = kNoMax;
           c_hi[tid] = hi;
           c_lo[tid] = window_start(p, hi);
         }
         named_bar_sync(1, kSoftmaxThreads);  // the row arrays are complete
       };
-      // This thread's exponents of rows h .. h + HC - 1 in an item, scale *
-      // score - (m - kPBias), or its scaled scores themselves (against_max false).
-      const auto exponents = [&](uint32_t s_col, int h, float (&y)[HC], bool against_max) {
+      // This thread's exponents of rows h .. h + HC - 1 in an item: scale *
+      // (score - m) + kPBias.  The difference comes first, as it is exact near m:
+      // scale * score rounded into m would leave the maximum's own exponent half
+      // a step of that product off, and P infinite or 0 for scores past 2^27.
+      const auto exponents = [&](uint32_t s_col, int h, float (&y)[HC]) {
         uint32_t r[HC];
         tmem_ld<HC>(s_col + h, r);
         const float4* sc4 = reinterpret_cast<const float4*>(c_scale + c0 + h);
-        const float4* mb4 = reinterpret_cast<const float4*>(c_mb + c0 + h);
+        const float4* mm4 = reinterpret_cast<const float4*>(c_minus_m + c0 + h);
+        const float2 bias = make_float2(kPBias, kPBias);
 #pragma unroll
         for (int k = 0; k < HC / 4; ++k) {
-          const float4 s = sc4[k], m = against_max ? mb4[k] : make_float4(0.f, 0.f, 0.f, 0.f);
-          y[4 * k] = fmaf(__uint_as_float(r[4 * k]), s.x, -m.x);
-          y[4 * k + 1] = fmaf(__uint_as_float(r[4 * k + 1]), s.y, -m.y);
-          y[4 * k + 2] = fmaf(__uint_as_float(r[4 * k + 2]), s.z, -m.z);
-          y[4 * k + 3] = fmaf(__uint_as_float(r[4 * k + 3]), s.w, -m.w);
+          const float4 s = sc4[k], m = mm4[k];
+          const float2 a = make_float2(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1]));
+          const float2 b = make_float2(__uint_as_float(r[4 * k + 2]), __uint_as_float(r[4 * k + 3]));
+          const float2 u = __ffma2_rn(__fadd2_rn(a, make_float2(m.x, m.y)), make_float2(s.x, s.y), bias);
+          const float2 v = __ffma2_rn(__fadd2_rn(b, make_float2(m.z, m.w)), make_float2(s.z, s.w), bias);
+          y[4 * k] = u.x, y[4 * k + 1] = u.y, y[4 * k + 2] = v.x, y[4 * k + 3] = v.y;
         }
       };
 
@@ -943,7 +956,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
         // The piece's last scores are there, so its Q has been read: the next unit's may come.
         if ((it.x & kCloses) && n + 1 < items && tid == 0) request_q(min(max(info[n % kInfoRing].z, 0) + 1, units - 1));
         if (!(it.x & kWhole)) {
-          // Scores of tokens that a row does not see become infinite, of the sign that its scale turns to minus.
+          // Scores of tokens that a row does not see become minus infinity.
           const int pos = it.y * kTile + row;
           const bool there = token_there(it.x, row), sink = pos < p.sinks;
 #pragma unroll 1
@@ -954,7 +967,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
             for (int c = 0; c < 8; ++c) {
               const int i = c0 + h + c;
               const bool see = there && pos <= c_hi[i] && (sink || pos >= c_lo[i]);
-              if (!see) r[c] = c_scale[i] > 0.f ? 0xFF800000u : 0x7F800000u;
+              if (!see) r[c] = 0xFF800000u;
             }
             tmem_st8(s_col + h, r);
           }
@@ -965,34 +978,47 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
 #pragma unroll
         for (int h = 0; h < NC; h += HC) {
           float y[HC];
-          exponents(s_col, h, y, true);
           if constexpr (kKeep) {
+            exponents(s_col, h, y);
 #pragma unroll
             for (int c = 0; c < HC; ++c) kept[h + c] = y[c];
+          } else {
+            uint32_t r[HC];
+            tmem_ld<HC>(s_col + h, r);
+            const float4* most4 = reinterpret_cast<const float4*>(c_minus_most + c0 + h);
+#pragma unroll
+            for (int k = 0; k < HC / 4; ++k) {
+              const float4 m = most4[k];
+              y[4 * k] = __uint_as_float(r[4 * k]) + m.x, y[4 * k + 1] = __uint_as_float(r[4 * k + 1]) + m.y;
+              y[4 * k + 2] = __uint_as_float(r[4 * k + 2]) + m.z, y[4 * k + 3] = __uint_as_float(r[4 * k + 3]) + m.w;
+            }
           }
 #pragma unroll
           for (int c = 0; c < HC; ++c) top = fmaxf(top, y[c]);
         }
-        if (any_of(2, kSoftmaxThreads, top > kSlack + kPBias)) {
+        if (any_of(2, kSoftmaxThreads, top > (kKeep ? kSlack + kPBias : 0.f))) {
           // Exact maxima of the tile's rows.
 #pragma unroll 1
           for (int h = 0; h < NC; h += HC) {
+            uint32_t r[HC];
             float y[HC];
-            exponents(s_col, h, y, false);
+            tmem_ld<HC>(s_col + h, r);
+#pragma unroll
+            for (int c = 0; c < HC; ++c) y[c] = __uint_as_float(r[c]);
             LaneReduce<HC, 16>::run(y, lane, OpMax());
             if (lane % (32 / HC) == 0) red[quad * NR + c0 + h + column_of<HC>(lane)] = y[0];
           }
           named_bar_sync(1, kSoftmaxThreads);
           bool moved = false;
           if (tid < NR) {
-            const float mb =
-                fmaxf(fmaxf(red[tid], red[NR + tid]), fmaxf(red[2 * NR + tid], red[3 * NR + tid])) - kPBias;
-            const float old = c_mb[tid];
+            const float m = fmaxf(fmaxf(red[tid], red[NR + tid]), fmaxf(red[2 * NR + tid], red[3 * NR + tid]));
+            const float minus_old = c_minus_m[tid], scale = c_scale[tid];
             float alpha = 1.f;
-            if (mb > old + kSlack) {
-              alpha = ex2_approx(old - mb);
-              moved = old != kNoMax;
-              c_mb[tid] = mb;
+            if (fmaf(m + minus_old, scale, kPBias) > kSlack + kPBias) {  // (its exponent, as above)
+              alpha = ex2_approx(-(m + minus_old) * scale);
+              moved = minus_old != -kNoMax;
+              c_minus_m[tid] = -m;
+              c_minus_most[tid] = -most_under(m, scale);
             }
             c_alpha[tid] = alpha;
           }
@@ -1001,7 +1027,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
 #pragma unroll
             for (int h = 0; h < NC; h += HC) {
               float y[HC];
-              exponents(s_col, h, y, true);
+              exponents(s_col, h, y);
 #pragma unroll
               for (int c = 0; c < HC; ++c) kept[h + c] = y[c];
             }
@@ -1041,7 +1067,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
 #pragma unroll
             for (int c = 0; c < HC; ++c) y[c] = kept[h + c];
           } else {
-            exponents(s_col, h, y, true);
+            exponents(s_col, h, y);
           }
           if (h + HC == NC) {
             tc_fence_before();
@@ -1080,7 +1106,8 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
         if (tid < NR) {
           const float sum = (red[tid] + red[NR + tid]) + (red[2 * NR + tid] + red[3 * NR + tid]);
           c_linv[tid] = sum > 0.f ? 1.f / sum : 0.f;
-          const float lse = sum > 0.f ? (c_mb[tid] + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+          const float lse =
+              sum > 0.f ? fmaf(-c_minus_m[tid], c_scale[tid], log2f(sum) - kPBias) * 0.6931471805599453f : -INFINITY;
           if (!whole_unit)
             p.ws_lse[prow + tid] = lse;
           else if (tid < nrows)

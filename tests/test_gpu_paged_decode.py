@@ -9,6 +9,8 @@ exponentials add 2^-22, their fp32 sums 2^-20 in all: so
 product rounded to 16 bits with at least 11 significant bits (2^-11 of
 itself), and shifts by 2 dx at most: |out error| <= (2^-11 + 2 dx + 2^-19) *
 sum_j p_j |k_j| before the output's own rounding to bf16, 2^-8 of itself."""
+import math
+
 import pytest
 import torch
 
@@ -218,6 +220,38 @@ def test_large_and_small_queries_and_scales():
         out, lse, err = c.run(sm_scale=sm)
         assert err == 0
         c.check(out, lse, sm_scale=sm)
+
+
+@pytest.mark.parametrize("bits", [16, 20, 23, 25, 26, 27, 28, 29, 31, 40, 100])
+@pytest.mark.parametrize("s,h", [(1, 16), (2, 16), (1, 64)])
+def test_scores_far_past_what_a_softmax_tells_apart(s, h, bits):
+    """Finite queries whose scores reach 2^bits: lse still follows the largest score, out is some average of the
+    records, and the largest score's own record (its values have 6 bits, so bf16 holds them) where it leads by more
+    than the scores' error on either side."""
+    c = Case([700, 128, 1, 2000, 65] * 8, s, h, seed=bits)
+    c.q = (c.q.float() * 2.0 ** (bits - 2)).to(torch.bfloat16)
+    out, lse, err = c.run()
+    assert err == 0 and bool(torch.isfinite(out).all())
+    alone = 0
+    for b, n in enumerate(c.lens):
+        k = decode_records(c.kv[c.table[b, : -(-n // 64)].long()].reshape(-1, 288)[:n])
+        for i in range(s):
+            at = n - s + i
+            if at < 0:
+                continue
+            ks, q = k[: at + 1], c.q[b, i].double()
+            x = q @ ks.T * 512 ** -0.5
+            dx = 64 * 2.0 ** -23 * (q.abs() @ ks.abs().T * 512 ** -0.5).amax(-1)
+            want = torch.logsumexp(x, -1)
+            assert torch.all((lse[b, i].double() - want).abs() <= dx + 2.0 ** -20 * (1 + want.abs()))
+            assert torch.all(out[b, i].double().abs() <= ks.abs().amax(0) * (1 + 2.0 ** -7))
+            top, arg = x.topk(min(2, at + 1), dim=-1)
+            ahead = top[:, 0] - top[:, -1] > 2 * dx + 64 if at else torch.ones(h, dtype=torch.bool, device=DEV)
+            # Its weight is 1 within 2^-11, less than half a step of bf16; the others' are below e^-64 each.
+            err = (out[b, i].double() - ks[arg[:, 0]]).abs()[ahead]
+            assert torch.all(err <= n * math.exp(-64) * ks.abs().max()), float(err.max())
+            alone += int(ahead.sum())
+    assert alone > len(c.lens) * s * h / (8 if bits > 20 else 40)
 
 
 def test_a_peak_and_a_long_tail():
