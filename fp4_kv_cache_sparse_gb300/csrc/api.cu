@@ -99,12 +99,14 @@ bool uses_pair_kernel(const mla_problem_t* problem) { return problem->h_q == 128
 
 int element_bytes(int32_t dtype) { return dtype == MLA_FP32 ? 4 : (dtype == MLA_BF16 || dtype == MLA_FP16 ? 2 : 0); }
 
+constexpr float kLog2e = 1.4426950408889634f;
+
 bool aligned_to(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
 mla_status_t validate_paged(const mla_paged_problem_t* p) {
   if (p == nullptr) return MLA_ERR_INVALID_ARG;
   if (p->batch < 1 || p->seq_len_q < 1 || p->h_q < 1 || p->max_pages < 1 || p->num_pages < 1 || p->window < 0 ||
-      p->sinks < 0 || !std::isfinite(p->sm_scale))
+      p->sinks < 0 || !std::isfinite(p->sm_scale * kLog2e))
     return MLA_ERR_INVALID_ARG;
   if (p->kv_format == MLA_KV_FP8_528 || p->kv_format == MLA_KV_BF16) return MLA_ERR_UNSUPPORTED;
   if (p->kv_format != MLA_KV_FP4_288) return MLA_ERR_INVALID_ARG;
@@ -553,7 +555,7 @@ mla_status_t mla_paged_decode_fp4(const mla_paged_problem_t* problem, const void
   p.window = problem->window;
   p.sinks = problem->sinks;
   p.num_pages = problem->num_pages;
-  p.scale_log2 = problem->sm_scale * 1.4426950408889634f;
+  p.scale_log2 = problem->sm_scale * kLog2e;
   if (launch_paged_decode(p, pl, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return MLA_ERR_CUDA;
   return MLA_OK;
 }

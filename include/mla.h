@@ -421,7 +421,7 @@ typedef struct {
   int32_t sinks;        /* the first tokens of a sequence, seen whatever the window */
   int64_t num_pages;    /* pages in the pool (bounds check of the block table) */
   int32_t kv_format;    /* must be MLA_KV_FP4_288 */
-  float sm_scale;       /* softmax scale applied to q.k */
+  float sm_scale;       /* softmax scale applied to q.k, finite in units of ln 2 too (|sm_scale| < 2.35e38) */
 } mla_paged_problem_t;
 
 /* Host-only planning: the part count (num_sms = 0 asks the current device) and the workspace bytes. */

@@ -193,6 +193,15 @@ def test_paged_problem_refusals(lib, kw, status):
     assert lib.mla_paged_decode_fp4(ctypes.addressof(p), A, A, A, A, 152, A, 1 << 40, A, A, None, None) == status
 
 
+@pytest.mark.parametrize("sm_scale", [2.4e38, -3.4e38])
+def test_paged_problem_refuses_a_scale_that_overflows_in_units_of_ln_2(lib, sm_scale):
+    prob = mla.PagedProblem.make(4, 1, 16, 10, 100, sm_scale=sm_scale)
+    parts, ws = ctypes.c_int32(), ctypes.c_size_t()
+    assert lib.mla_paged_decode_plan(ctypes.byref(prob), 152, ctypes.byref(parts), ctypes.byref(ws)) == INVALID
+    prob.sm_scale = math.copysign(2.3e38, sm_scale)
+    assert lib.mla_paged_decode_plan(ctypes.byref(prob), 152, ctypes.byref(parts), ctypes.byref(ws)) == 0
+
+
 def test_paged_decode_argument_checks_before_any_launch(lib):
     p = _problem()
     parts, ws = mla.paged_decode_plan(p, 152)
