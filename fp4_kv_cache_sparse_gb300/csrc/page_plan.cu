@@ -194,22 +194,26 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kPlanThreads)
   const int gtid = rank * kPlanThreads + tid, lane = tid & 31, warp = gtid >> 5;
   constexpr int kAll = kCtas * kPlanThreads;
   const bool by_warp = batch <= kAll / 32 && s_give[batch] + s_take[batch] <= 32 * batch;
+  bool bad_page = false;
+  const auto give = [&](int r, int32_t i, int32_t k) {  // page i of all comes back: entry k of request r's row
+    const int32_t page = block_table[static_cast<int64_t>(r) * max_pages + k];
+    bad_page |= page < 0 || page >= num_pages;
+    free_pages[nf + i] = page;
+  };
   if (by_warp) {
     if (warp < batch) {
       const int32_t g0 = s_give[warp], n = s_give[warp + 1] - g0;
-      for (int k = lane; k < n; k += 32)
-        free_pages[nf + g0 + k] = block_table[static_cast<int64_t>(warp) * max_pages + k];
+      for (int k = lane; k < n; k += 32) give(warp, g0 + k, k);
     }
   } else {
     for (int32_t i = gtid; i < s_give[batch]; i += kAll) {
       const int r = request_of(s_give, batch, i);
-      free_pages[nf + i] = block_table[static_cast<int64_t>(r) * max_pages + (i - s_give[r])];
+      give(r, i, i - s_give[r]);
     }
   }
   // Everyone has read the old lengths and the pushed pages are visible.
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 
-  bool bad_page = false;
   const auto take = [&](int r, int32_t i) {  // page i of all goes to request r
     const int32_t page = free_pages[top - 1 - i];
     bad_page |= page < 0 || page >= num_pages;

@@ -314,7 +314,8 @@ mla_status_t mla_kv_write(int32_t kv_format, const void* latents, const int32_t*
  * 64 * max_pages (MLA_DEVERR_BAD_LENGTH), when pages or slots do not suffice
  * (MLA_DEVERR_NO_ROOM), or when num_free lies outside [0, num_pages] or more
  * pages come back than the stack holds (MLA_DEVERR_BAD_METADATA).  A page id
- * outside [0, num_pages) gives its tokens slot -1 and MLA_DEVERR_BAD_INDEX.
+ * outside [0, num_pages) gives its tokens slot -1 and MLA_DEVERR_BAD_INDEX; one
+ * that an ended request gives back is flagged likewise and goes onto the stack.
  * batch is at most 8192 and num_pages * 64 below 2^31 (MLA_ERR_UNSUPPORTED).
  * Apart from the two pairs named, no buffer may overlap another.
  */

@@ -147,6 +147,22 @@ def test_bad_page_ids_are_skipped_and_flagged():
     assert got[3] == [-1, -1, -1, -1] and got[4] == [64, 10, 11, 0] and got[0] == [65, 12]
 
 
+@pytest.mark.parametrize("b", [3, 300])               # a warp to a request, a thread to a page
+def test_bad_page_ids_given_back_are_flagged(b):
+    """An ended request's row with ids outside the pool: they return to the stack, which keeps its count, and the call
+    says so."""
+    cached, new = [200] + [64] * (b - 1), [-1] + [0] * (b - 1)
+    pages = b + 10
+    for bad in (-3, pages, 2 ** 31 - 1):
+        table = [[0, bad, 2, 3]] + [[4 + r, -1, -1, -1] for r in range(b - 1)]
+        got, err = run(cached, new, table, [7] * pages, 1, 5)
+        assert err == mla.DEVERR_BAD_INDEX
+        assert got[0] == [0] + [64] * (b - 1) and got[1] == 5 and got[6][:5] == [7, 0, bad, 2, 3] and got[3] == [-1] * 5
+    # What lies past the held pages is not looked at.
+    got, err = run([64] + cached[1:], new, [[0, -3, -3, -3]] + table[1:], [7] * pages, 1, 5)
+    assert err == 0 and got[1] == 2
+
+
 def test_replayed_graph_advances_the_state_in_place():
     """Captured once, replayed: lengths, stack and tables go on from step to step."""
     cached, new, table, free, nf, num_pages = make(5, 33, 4, lambda r: 1, spare=200, cached_of=lambda: 40)
