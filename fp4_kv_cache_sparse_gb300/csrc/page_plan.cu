@@ -162,7 +162,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kPlanThreads)
   bad = __syncthreads_or(bad);
   int32_t why = 0;
   if (bad) why |= MLA_DEVERR_BAD_LENGTH;
-  if (nf < 0 || nf > num_pages || total.give > num_pages - nf) why |= MLA_DEVERR_BAD_METADATA;
+  if (nf < 0 || nf > num_pages || (!bad && total.give > num_pages - nf)) why |= MLA_DEVERR_BAD_METADATA;
   if (!why && (total.tokens > max_new || total.take > nf + total.give)) why |= MLA_DEVERR_NO_ROOM;
   const bool ok = why == 0;
   const int32_t top = ok ? nf + static_cast<int32_t>(total.give) : nf;

@@ -141,6 +141,14 @@ def test_refuses_as_a_whole(case, bit, in_place):
     assert got == (cached, nf, [0, 0, 0, 0], [-1] * max_new, [0] * max_new, table, free)
 
 
+@pytest.mark.parametrize("cached,new", [(-100, -1), (2 ** 31 - 1, -1), (-2 ** 31, 0)])
+def test_a_bad_length_is_flagged_as_that_alone(cached, new):
+    """Sums over bad lengths say nothing about the stack."""
+    got, err = run([cached, 10], [new, 1], [[0, -1], [1, -1]], [2, 3, 0, 0], 2, 3)
+    assert err == mla.DEVERR_BAD_LENGTH
+    assert got == ([cached, 10], 2, [0, 0, 0], [-1] * 3, [0] * 3, [[0, -1], [1, -1]], [2, 3, 0, 0])
+
+
 def test_bad_page_ids_are_skipped_and_flagged():
     got, err = run([64, 10], [1, 2], [[0, -1], [9, -1]], [100, 0, 0, 0, 0], 1, 4)
     assert err == mla.DEVERR_BAD_INDEX
