@@ -92,11 +92,12 @@ __device__ __forceinline__ void store_four(int32_t* slots, int32_t* positions, i
 }
 
 // The slot map of a plan that has been made: request r's new tokens stand at
-// the end of its new length, and its row holds every page.
-__global__ void __launch_bounds__(256) slot_map_kernel(const int32_t* __restrict__ cu_new,
-                                                       const int32_t* __restrict__ seq_lens, int batch,
-                                                       const int32_t* __restrict__ block_table, int max_pages,
-                                                       int num_pages, int32_t* __restrict__ slots,
+// the end of its new length, and its row holds every page.  (No __restrict__ on
+// what the plan writes: this kernel starts while that one ends, and a
+// non-coherent load may be moved above the wait.)
+__global__ void __launch_bounds__(256) slot_map_kernel(const int32_t* cu_new, const int32_t* seq_lens, int batch,
+                                                       const int32_t* block_table, int max_pages, int num_pages,
+                                                       int32_t* __restrict__ slots,
                                                        int32_t* __restrict__ positions, int max_new, int32_t* d_error) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int32_t tokens = cu_new[batch];

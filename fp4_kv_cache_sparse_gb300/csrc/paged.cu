@@ -172,8 +172,16 @@ struct Unit {
   int tiles;            // at least 1 (a unit that sees nothing still writes its rows)
 };
 
+// A coherent load that stays behind griddepcontrol.wait: what the stream's
+// previous kernel may still be writing when this one starts.
+__device__ __forceinline__ int load_i32(const int32_t* p) {
+  int v;
+  asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
 __device__ __forceinline__ int checked_len(const PagedParams& p, int b, bool& bad) {
-  const int len = __ldg(p.seq_lens + b);
+  const int len = load_i32(p.seq_lens + b);
   bad = len < 0 || len > p.max_pages * kPage;
   return bad ? 0 : len;
 }
@@ -498,6 +506,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
 
   // Launched as a programmatic dependent: what comes before this line runs
   // beside the end of the stream's previous kernel, nothing after it does.
+  // (That kernel may write the lengths and tables, hence load_i32.)
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
         // A unit's Q arrives by TMA as bf16, K-major with 128-byte swizzle ...
@@ -605,7 +614,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
           const int pos = tile * kTile + lane * kPage;
           const bool seen = pos < end && (pos + kPage > unit.start || pos < p.sinks);
           if (seen) {
-            const int page = __ldg(p.block_table + static_cast<int64_t>(unit.b) * p.max_pages + tile * 2 + lane);
+            const int page = load_i32(p.block_table + static_cast<int64_t>(unit.b) * p.max_pages + tile * 2 + lane);
             if (page >= 0 && page < p.num_pages) {
               tokens = min(kPage, end - pos);
               first_row = page * kPage;
