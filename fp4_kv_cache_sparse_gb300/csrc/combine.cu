@@ -39,8 +39,8 @@ __device__ __forceinline__ float warp_sum(float v) {
 // The merged output of one (query token, head) row: lane l ends with dims
 // 128 k + 4 l .. 128 k + 4 l + 3 in acc[4 k .. 4 k + 3]; returns the row's
 // log-sum-exp (natural log; -inf when every split is empty, acc all zero).
-__device__ __forceinline__ float merge_row(const float* __restrict__ o_part, const float* __restrict__ lse_part,
-                                           int s0, int n, int h, int h_q, int lane, float (&acc)[16]) {
+__device__ __forceinline__ float merge_row(const float* o_part, const float* lse_part, int s0, int n, int h, int h_q,
+                                           int lane, float (&acc)[16]) {
   const float* lrow = lse_part + static_cast<int64_t>(s0) * h_q + h;
   // Max and sum over the splits, lanes striding over them.
   float mx = -INFINITY;
@@ -99,7 +99,7 @@ __device__ __forceinline__ float merge_row(const float* __restrict__ o_part, con
 // once); -1 when the part has nothing to merge.  Otherwise one warp per
 // (query token, head) row, every token visited.
 template <bool kByPart>
-__device__ __forceinline__ int64_t merge_row_of(const int32_t* __restrict__ sched, int T, int h_q, int& h) {
+__device__ __forceinline__ int64_t merge_row_of(const int32_t* sched, int T, int h_q, int& h) {
   const int warp = threadIdx.x >> 5;
   if constexpr (!kByPart) {
     const int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
@@ -120,8 +120,8 @@ __device__ __forceinline__ int64_t merge_row_of(const int32_t* __restrict__ sche
 // that the two overlap.  Returns false (nothing done) when there are more
 // splits than the staging holds.
 constexpr int kStageSplits = 2;
-__device__ __forceinline__ bool merge_rows_staged(const float* __restrict__ o_part, const float* __restrict__ lse_part,
-                                                  int s0, int n, int h0, int h_q, float (&acc)[16], float& L) {
+__device__ __forceinline__ bool merge_rows_staged(const float* o_part, const float* lse_part, int s0, int n,
+                                                  int h0, int h_q, float (&acc)[16], float& L) {
   __shared__ alignas(128) float stage[kStageSplits][kWarps * 512];
   __shared__ alignas(8) uint64_t bar;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -189,15 +189,15 @@ __device__ __forceinline__ bool merge_rows_staged(const float* __restrict__ o_pa
 }
 
 template <bool kByPart>
-__global__ void __launch_bounds__(kWarps * 32, 7) combine_kernel(const int32_t* __restrict__ num_splits,
-                                                             const float* __restrict__ o_part,
-                                                             const float* __restrict__ lse_part,
+__global__ void __launch_bounds__(kWarps * 32, 7) combine_kernel(const int32_t* num_splits,
+                                                             const float* o_part, const float* lse_part,
                                                              uint16_t* __restrict__ out, float* __restrict__ lse,
                                                              int nq, int h_q, int skip_single,
-                                                             const int32_t* __restrict__ sched, int T) {
+                                                             const int32_t* sched, int T) {
   // Launched as a programmatic dependent of the decode kernel: wait until
   // that grid has completed and its partials are visible (returns at once
-  // for an ordinary launch).
+  // for an ordinary launch).  No input is __restrict__: a non-coherent load
+  // may be moved above the wait.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
   int h;
@@ -237,14 +237,12 @@ __global__ void __launch_bounds__(kWarps * 32, 7) combine_kernel(const int32_t* 
 // 32-dim block (eight lanes) is cast to E4M3FN under its e8m0 scale, giving
 // a 528-byte record per row in the cache's own format.
 template <bool kByPart>
-__global__ void __launch_bounds__(kWarps * 32, 4) rope_fp8_kernel(const int32_t* __restrict__ num_splits,
-                                                              const float* __restrict__ o_part,
-                                                              const float* __restrict__ lse_part,
-                                                              const int32_t* __restrict__ positions,
+__global__ void __launch_bounds__(kWarps * 32, 4) rope_fp8_kernel(const int32_t* num_splits,
+                                                              const float* o_part, const float* lse_part,
+                                                              const int32_t* positions,
                                                               const RopeFreqs freqs, uint8_t* __restrict__ out,
                                                               float* __restrict__ lse, int nq, int h_q,
-                                                              int skip_single, const int32_t* __restrict__ sched,
-                                                              int T) {
+                                                              int skip_single, const int32_t* sched, int T) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
   int h;

@@ -38,6 +38,7 @@ def dependent_kernels(text):
 @pytest.mark.parametrize("name,kernels", [
     ("paged.cu", {"paged_decode_kernel", "paged_merge_kernel", "paged_merge_many_kernel"}),
     ("page_plan.cu", {"slot_map_kernel"}),
+    ("combine.cu", {"combine_kernel", "rope_fp8_kernel"}),
 ])
 def test_dependent_kernels_read_by_plain_loads(name, kernels):
     text = source(name)
