@@ -77,6 +77,42 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
+// The same wait for a whole warp, whose waits are many and nearly all short:
+// the clock is read only now and then.  After limit_ns, or once another warp
+// of the CTA has given up, it goes on with the abort flag set, so that every
+// warp still reaches the kernel's end.
+__device__ __forceinline__ void mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                               int32_t* d_error, uint64_t limit_ns) {
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+    if ((i & 63) == 0) {
+      const uint64_t t = global_timer_ns();
+      if (t0 == 0) t0 = t;
+      const bool late = t - t0 > limit_ns;
+      if (late || *abort_flag) {
+        *abort_flag = 1;
+        if (late && d_error) atomicOr(d_error, MLA_DEVERR_TIMEOUT);
+        break;
+      }
+    }
+  }
+  __syncwarp();
+}
+
+// The wait before a CTA ends, for what must not outlive it (copies into its
+// shared memory, products in its tensor memory): it heeds no abort flag, but
+// has a bound of its own.
+__device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity, int32_t* d_error, uint64_t limit_ns) {
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (global_timer_ns() - t0 > limit_ns) {
+      if (d_error) atomicOr(d_error, MLA_DEVERR_TIMEOUT);
+      break;
+    }
+  }
+}
+
 // Make this thread's generic-proxy shared-memory writes visible to the
 // async proxy (the tensor core reads its operands through it).
 __device__ __forceinline__ void fence_proxy_async_smem() {

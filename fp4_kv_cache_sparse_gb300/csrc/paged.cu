@@ -246,39 +246,8 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
   }
 }
 
-// Bounded wait of a whole warp on an mbarrier phase; the clock is read only
-// now and then, as nearly all waits are short.  After kPagedWaitNs, or once
-// another warp of the CTA has given up, it goes on with the abort flag set, so
-// that every warp still reaches the kernel's end.
 __device__ __forceinline__ void wait_for(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* d_error) {
-  uint64_t t0 = 0;
-#pragma unroll 1
-  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
-    if ((i & 63) == 0) {
-      const uint64_t t = global_timer_ns();
-      if (t0 == 0) t0 = t;
-      const bool late = t - t0 > kPagedWaitNs;
-      if (late || *abort_flag) {
-        *abort_flag = 1;
-        if (late && d_error) atomicOr(d_error, MLA_DEVERR_TIMEOUT);
-        break;
-      }
-    }
-  }
-  __syncwarp();
-}
-
-// The wait for the tensor core's end before tensor memory goes away: it does
-// not heed the abort flag, but has its own bound.
-__device__ __forceinline__ void wait_drain(uint64_t* bar, int32_t* d_error) {
-  const uint64_t t0 = global_timer_ns();
-  while (!mbar_try_wait(bar, 0)) {
-    if (global_timer_ns() - t0 > kPagedWaitNs) {
-      if (d_error) atomicOr(d_error, MLA_DEVERR_TIMEOUT);
-      break;
-    }
-  }
-  __syncwarp();
+  mbar_wait_warp(bar, parity, abort_flag, d_error, kPagedWaitNs);
 }
 
 // One elected lane of a converged warp issues; A in tensor memory or in
@@ -482,7 +451,8 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
   int4* info = reinterpret_cast<int4*>(smem + L::kInfoOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
-  // This part's run: first unit, its item that the run begins with, items; and the cost of every run.
+  // This part's run: first unit, its item that the run begins with, items; the
+  // cost of every run; the phase of the last copy of Q asked for.
   int* cut = reinterpret_cast<int*>(smem + L::kMiscOff + 8);
   int* warp_sum = reinterpret_cast<int*>(smem + L::kMiscOff + 32);    // [warps]
   int* warp_most = reinterpret_cast<int*>(smem + L::kMiscOff + 160);  // [warps]
@@ -497,6 +467,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
   if (tid == 0) {
     *abort_flag = 0;
     cut[2] = 0;
+    cut[4] = 0;
   }
   if (tid < L::kNumBars) {
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -601,7 +572,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
       bool bad_len;
       Unit unit = *first_unit;
       int slot = 0;
-      uint32_t parity = 1;
+      uint32_t parity = 1, asked = 0;  // pages asked for
       for (uint32_t n = 0; n < items; ++n) {
         const int tile = tile_of(unit, k);
         const int end = unit.p_hi + 1;
@@ -642,7 +613,10 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
             info[n % kInfoRing] = make_int4(word, tile, u, 0);
             mbar_arrive(&bars[L::bInfo + n % kInfoRing]);
           }
-          if (lane == j) {
+          // After a wait that gave up nothing more is asked for.
+          const bool ask = !__any_sync(0xFFFFFFFFu, *abort_flag);
+          if (ask) ++asked;
+          if (lane == j && ask) {
             uint64_t* bar = &bars[L::bRawFull + slot];
             uint8_t* dst = sRaw + slot * kPageBytes;
             expect_tx(bar, tokens > 0 ? kPageBytes : 0);
@@ -677,13 +651,8 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
         }
       }
       // Every copy has landed before the CTA may end (they have, unless a wait gave up).
-      const uint32_t pages = 2 * items;
-      for (uint32_t i = pages > L::kRaw ? pages - L::kRaw : 0; i < pages; ++i) {
-        const uint64_t t0 = global_timer_ns();
-        while (!mbar_try_wait(&bars[L::bRawFull + i % L::kRaw], (i / L::kRaw) & 1) &&
-               global_timer_ns() - t0 < kPagedWaitNs) {
-        }
-      }
+      for (uint32_t i = asked > L::kRaw ? asked - L::kRaw : 0; i < asked; ++i)
+        mbar_drain(&bars[L::bRawFull + i % L::kRaw], (i / L::kRaw) & 1, p.d_error, kPagedWaitNs);
     } else if (warp >= kKWarp0 && warp < kVWarp0) {
       // ---------------------------------------------------------------- K: lane = token
       // Four warps, one for each quadrant of tensor memory lanes, decode a
@@ -815,7 +784,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
         commit_one(&bars[L::bSFull + (n & 1)]);
       }
       commit_one(&bars[L::bDrain]);
-      wait_drain(&bars[L::bDrain], p.d_error);
+      mbar_drain(&bars[L::bDrain], 0, p.d_error, kPagedWaitNs);
     } else if (warp >= kValueWarp0) {
       // ---------------------------------------------------------------- O^T += V^T P^T
       // Two warps, two dim quarters each: what waiting for one costs the other issues through.
@@ -860,7 +829,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
         }
       }
       commit_one(&bars[L::bDrain]);
-      wait_drain(&bars[L::bDrain], p.d_error);
+      mbar_drain(&bars[L::bDrain], 0, p.d_error, kPagedWaitNs);
     } else if (warp < kSoftmaxWarps) {
       // ---------------------------------------------------------------- softmax
       constexpr int kSoftmaxThreads = kSoftmaxWarps * 32;
@@ -963,7 +932,11 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
         tc_fence_after();
         const uint32_t s_col = tS + (n & 1) * NR;
         // The piece's last scores are there, so its Q has been read: the next unit's may come.
-        if ((it.x & kCloses) && n + 1 < items && tid == 0) request_q(min(max(info[n % kInfoRing].z, 0) + 1, units - 1));
+        // (None after a wait that gave up: the last one asked for has to have landed at the end.)
+        if ((it.x & kCloses) && n + 1 < items && tid == 0 && !*abort_flag) {
+          request_q(min(max(info[n % kInfoRing].z, 0) + 1, units - 1));
+          cut[4] ^= 1;
+        }
         if (!(it.x & kWhole)) {
           // Scores of tokens that a row does not see become minus infinity.
           const int pos = it.y * kTile + row;
@@ -1172,6 +1145,8 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  // (Q's copies have landed long ago, unless a wait gave up.)
+  if (tid == 0 && items > 0) mbar_drain(&bars[L::bQRaw], cut[4], p.d_error, kPagedWaitNs);
   if (warp == kValueWarp0) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
