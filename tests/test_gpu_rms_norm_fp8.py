@@ -137,6 +137,26 @@ def test_weights_whose_product_with_the_row_leaves_the_range(dtype, d):
         run((x * rows).to(dtype), None, (w * weights).to(dtype), eps=eps)
 
 
+@pytest.mark.parametrize("dtype,d", [(torch.float32, 12800), (torch.float32, 12832), (torch.float32, 16384),
+                                     (torch.bfloat16, 16384)])
+def test_rows_around_the_longest_that_are_copied_ahead(dtype, d):
+    """Two rows with their residuals just fit into a block's shared memory, or just do not: several rows a block, blocks of
+    tiny values and of zeros among them."""
+    x, r, w = inputs(400, d, dtype, seed=d)
+    run(x, r, w)
+    r[3::5], x[3::5] = 0.0, 0.0
+    x[3::5, 70] = 1e-37
+    x[8::5, :64] = 0.0
+    run(x, r, w)
+    run(x, None, w)
+    clean = run(x, r, w)
+    x[7, 5] = float("nan")
+    codes, scales = torch.empty_like(clean[0]), torch.empty_like(clean[1])
+    mla.rms_norm_fp8(x, w, 1e-6, codes, scales, residual=r)
+    keep = [i for i in range(400) if i != 7]
+    assert torch.equal(codes[keep], clean[0][keep]) and torch.equal(scales[keep], clean[1][keep])
+
+
 def test_a_row_of_infinities_or_nan_spoils_no_other():
     x, r, w = inputs(20, 512, torch.bfloat16, seed=6)
     clean = run(x, r, w)
