@@ -341,7 +341,7 @@ cudaError_t launch(const NormParams& p, cudaStream_t stream) {
 
 template <typename T>
 cudaError_t launch_typed(const NormParams& p, cudaStream_t stream) {
-  // (200,000 x 512: 56.3 us with a warp a row, 87.1 with two.)
+  // (200,000 x 512, one call alone between two events: 63.5 us with a warp a row, 97.0 with two.)
   if (p.dim <= 512) return launch<T, 32>(p, stream);
   if (p.dim <= 1024) return launch<T, 64>(p, stream);
   if (p.dim <= 2048) return launch<T, 128>(p, stream);

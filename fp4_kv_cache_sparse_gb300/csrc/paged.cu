@@ -32,11 +32,12 @@
 //                      raw pages, swizzled.
 //   score issuer (1)   S^T, two tiles ahead of
 //   value issuers (2)  O^T, two dim quarters each: with one, what it waits for
-//                      holds up the other quarters (64 heads over up to 8k
-//                      tokens 78 us against 70, 16 over 64k 264 against 223).
+//                      holds up the other quarters (64 x 64 heads over 1k to
+//                      8k tokens 80 us against 72, 32 x 16 over 64k 266
+//                      against 227).
 // Every role's loop is kept rolled and short: the roles together have to stay
-// in the instruction cache (issue loops unrolled over a tile: 16 heads over
-// 64k tokens 450 us against 273).
+// in the instruction cache (issue loops unrolled over a tile, in an earlier
+// build: 32 x 16 heads over 64k tokens 450 us against 273).
 //
 // A tile is decoded twice (K to tensor memory, V to shared memory) because
 // that is cheaper than the shared memory it saves: one f16 tile is 128 KB,
@@ -51,10 +52,12 @@
 // with 64 rows 5520 (3470 and 2050), in 4250 and 6130 cycles: nine tenths of
 // what shared memory can do, and the tensor core is busy for 510 and 2050 of
 // them.  So 32 x 16 heads over 64k tokens take 222 us (604 MB, 40 % of a copy's
-// bandwidth), 64 x 64 heads over 4k to 8k tokens 63 us (38.7 GFLOP, 32 % of the
-// bf16 rate), 32 x 2 x 128 heads with a window of 4096 106 us (35 %).  One tile
+// bandwidth), 64 x 64 heads over 1k to 8k tokens 63 us (38.7 GFLOP, 32 % of the
+// bf16 rate), 32 x 2 x 128 heads with a window of 4096 107 us (35 %).  One tile
 // alone takes 8 us, 2 of them until the cut is known, 4 until the first scores
-// are there, and a merge 3 us more.
+// are there, and a merge 3 us more.  (Those are times of a call among others.
+// Pairs beside the rules below are one call alone between two events, L2
+// written over before it: some 5 us more.)
 //
 // Numbers.  e2m1 x e4m3 has at most 6 significant bits and lies in f16's
 // range, so K and V are exact in f16.  Q (bf16) is scaled by a power of two
@@ -77,32 +80,33 @@ namespace {
 // A page in shared memory: its rows' data bytes in two halves of 128 bytes a
 // row (128-byte swizzle), then their 32 scale bytes a row (32-byte swizzle).
 // As one copy of the records, 288 bytes apart, rows of a warp met in the same
-// banks (16 heads: 1620 cycles of loads a tile, 1200 so; 229 and 221 us over 64k tokens).
+// banks (16 heads: 1620 cycles of loads a tile, 1200 so; 32 x 16 heads over 64k
+// tokens 229 and 221 us, in the build that laid them out so).
 constexpr int kPageBytes = kPage * kRecFp4;
 constexpr int kHalfBytes = kPage * 128;
 constexpr int kInfoRing = 8;
 constexpr uint64_t kPagedWaitNs = 2000000000ull;  // 2 s per wait
-// What a unit's Q and epilogue take, in tiles (64 sequences of up to 8k tokens,
-// 64 heads: 70.7 us, with nothing 76.8).
+// What a unit's Q and epilogue take, in tiles (64 sequences of 1k to 8k tokens,
+// 64 heads: 72 us, with nothing 79).
 constexpr int kUnitCost = 2;
 // What the partials and the merge of cut units take, in tiles (100 sequences of
-// 700 tokens, 64 heads: 29.7 us whole, 32.3 cut; 54 of 350, 22 heads: 16.8, 18.2).
+// 700 tokens, 64 heads: 33.5 us whole, 37.7 cut; 54 of 350, 22 heads: 22.1, 24.0).
 constexpr int kMergeCost = 3;
 // The running maximum may lag by 2^10: O is rescaled seldom (32 x 2 x 128 heads,
-// window 4096: 104.9 us, 109.3 with 2^8; with none 64 x 64 heads took 84 us
-// instead of 70).  P has room for that and for 5 bits above 1.
+// window 4096: 107.3 us among others, 110.5 with 2^8; with none 64 x 64 heads
+// take 88 us instead of 72).  P has room for that and for 5 bits above 1.
 constexpr float kSlack = 10.f;
 constexpr float kPBias = 5.f;                // P of the maximum is 2^5
 constexpr float kNoMax = -3.0e38f;           // running maximum, unscaled, before any visible token
 
 template <int NR>
 struct PSmem {
-  // A softmax thread holds NR / kSides rows: exponents and sums stay in
-  // registers (64 x 64 heads over up to 8k tokens: 70 us, with two sides 80).
+  // A softmax thread holds NR / kSides rows: sums and P stay in registers (with
+  // two sides of 64 rows they spill: 64 x 64 heads over 1k to 8k tokens 73.7 us, 72.4 so).
   static constexpr int kSides = NR == 64 ? 4 : 2;
   static constexpr int kSoftmaxWarps = 4 * kSides;
-  // Decode warps of each kind: eight hide more latency (16 heads over 64k
-  // tokens: 223 us against 253; 32 over 16k: 74.5 against 80.3), but with 64
+  // Decode warps of each kind: eight hide more latency (32 x 16 heads
+  // over 64k tokens: 227 us against 268; 32 x 32 over 16k: 80 against 88), but with 64
   // rows the softmax has twice the warps and no registers are left for more.
   static constexpr int kDecodeWarps = NR == 64 ? 4 : 8;
   static constexpr int kKWarp0 = kSoftmaxWarps, kVWarp0 = kKWarp0 + kDecodeWarps, kLoadWarp = kVWarp0 + kDecodeWarps;
@@ -113,9 +117,9 @@ struct PSmem {
   // dims, two chunks of 64 dims) for each dim quarter.  A page lives from its
   // load to the end of its V decode, about ten thousand cycles.  With 64 rows
   // Q leaves so little that V units of half the size, and six pages instead of
-  // four, gain more than their barriers cost (4096-token windows of 64 x 64
-  // rows: 109.6 us against 114.7); with 16 they only cost (16 heads over 64k
-  // tokens: 280 us against 225).
+  // four, gain more than their barriers cost (32 x 2 x 128
+  // heads, window 4096: 111.4 us against 114.7); with 16 they only cost (32 x 16
+  // heads over 64k tokens: 282 us against 227).
   static constexpr int kVTokens = NR == 64 ? 32 : 64;
   static constexpr int kVUnitBytes = kVTokens * 128 * 2;
   static constexpr int kRaw = NR == 16 ? 7 : 6;
@@ -480,13 +484,13 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
   // (That kernel may write the lengths and tables, hence load_i32.)
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-        // A unit's Q arrives by TMA as bf16, K-major with 128-byte swizzle ...
-        const auto request_q = [&](int u) {
-          const int b = u / groups, y = b * p.rows + (u - b * groups) * NR;
-          expect_tx(&bars[L::bQRaw], L::kQBytes);
-  #pragma unroll 1
-          for (int c = 0; c < 8; ++c) tma_load_2d(sQ + c * (NR * 128), &q_map, c * 64, y, &bars[L::bQRaw]);
-        };
+  // A unit's Q arrives by TMA as bf16, K-major with 128-byte swizzle ...
+  const auto request_q = [&](int u) {
+    const int b = u / groups, y = b * p.rows + (u - b * groups) * NR;
+    expect_tx(&bars[L::bQRaw], L::kQBytes);
+#pragma unroll 1
+    for (int c = 0; c < 8; ++c) tma_load_2d(sQ + c * (NR * 128), &q_map, c * 64, y, &bars[L::bQRaw]);
+  };
 
   // The cut: items of all units, this part's run, and the unit it begins in.
   const int units = p.batch * groups;
@@ -842,7 +846,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
       // The largest score whose exponent is within the slack, rounded down: with
       // 32 rows and more, whose exponents are computed again for P, comparing
       // scores with it takes one sum each (32 x 2 x 128 heads, window 4096: 105.5
-      // us, 107.5 with whole exponents).
+      // us among others, 107.5 with whole exponents).
       const auto most_under = [](float m, float scale) { return __fadd_rd(m, __fdividef(kSlack, scale)); };
 
       // A unit's Q becomes scaled f16 in place, a row per warp at a time (lane =
@@ -1307,8 +1311,8 @@ cudaError_t launch(PagedParams p, const PagedPlan& plan, cudaStream_t stream) {
   e = cudaLaunchKernelEx(&cfg, paged_decode_kernel<NR>, p, plan.groups, q_map, data_map, scale_map);
   if (e != cudaSuccess) return e;
   // Units that are few against the parts are cut into many pieces (one
-  // sequence of 64k tokens, 16 heads: 26 us so, 61 by single warps; 64 x 64
-  // heads at 8k, in three pieces: 89 against 70).
+  // sequence of 64k tokens, 16 heads: 32 us so, 66 by single warps; 64 x 64
+  // heads over 1k to 8k, in three pieces: 89 against 72).
   const int units = p.batch * plan.groups;
   const bool many = units * 6 <= plan.num_parts;
   cfg.gridDim = dim3(static_cast<unsigned>(p.info_by_unit ? units : plan.num_parts), many ? NR : NR / 4);
@@ -1323,13 +1327,15 @@ PagedPlan paged_plan(const mla_paged_problem_t* p, int num_parts) {
   PagedPlan pl{};
   const int64_t rows = static_cast<int64_t>(p->seq_len_q) * p->h_q;
   // Rows of a unit: as few as hold them all, for a tile's decode is most of its
-  // cost (32 sequences of 8k tokens, 24 heads: 43.5 us by 32, 55.6 by 64, 65.8
-  // by 16; 64 heads: 57.4 by 64, 79.5 by 32; 32 of 64k, 16 heads: 222 by 16, 270
-  // by 32).  Where the lengths that the table and the window allow leave no
+  // cost (32 sequences of 8k tokens, 24 heads: 50 us by 32, 59 by 64, 72 by 16;
+  // 64 of 1k to 8k, 64 heads: 72 by 64, 96 by 32; 32 of 64k, 16 heads: 227 by 16,
+  // 249 by 32).  Where the lengths that the table and the window allow leave no
   // part more than three or four tiles even so, as few as that takes: the start
   // and the end of a unit are then most of its cost, and shorter (7 x 3 x 24
-  // heads, window 1000: 18.8 us by 16, 21.3 by 64; 16 of 1000 tokens, 64 heads:
-  // 20.4 by 32, 26.3 by 64; 2 of 446, 128 heads: 13.9 by 16, 18.4 by 64).
+  // heads, window 1000: 22.5 us by 16, 26.6 by 64; 16 of 1000 tokens, 64 heads:
+  // 24.6 by 32, 28.7 by 64; 2 of 446, 128 heads: 18.4 by 16, 22.3 by 64).  The
+  // lengths themselves are on the device: short sequences under a wide table
+  // without a window get what the width says.
   int64_t tiles = (p->max_pages + 1) / 2;
   if (p->window > 0) {
     const int64_t seen = (int64_t(p->window) + p->seq_len_q) / kTile + 2 + (p->sinks + kTile - 1ll) / kTile;

@@ -6,13 +6,14 @@
 // point (of which this GPU has little) and no cosine table in memory.  Its
 // upper 32 bits, as a signed fraction in [-1/2, 1/2), go through one fp32
 // sine and cosine (of pi x, so no reduction is left): the angle is off by at
-// most 2^-25 of itself.
+// most 2^-32 of a turn, for the bits cut, and 2^-24 of itself.
 //
 // A thread owns one column -- a 16-byte piece of a head (two in the half
 // layout, whose pairs lie rope_dim / 2 apart) -- of one token, computes that
 // column's sines once and applies them to a run of heads.  Bound by HBM: 8000
-// tokens x 32 heads of 128 dims out of place, fp16 (131 MB), take 24.8 us, 78 %
-// of a copy's bandwidth.
+// tokens x 32 heads of 128 dims out of place, fp16 (131 MB), take 24.5 us, 79 %
+// of a copy's bandwidth.  Heads or ranges off 16 bytes go element by element:
+// 100 dims instead of 128 take 30.8 us, twice what their bytes would.
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -24,9 +25,9 @@ namespace mla {
 
 namespace {
 
-constexpr int kRopeThreads = 128;  // (8000 tokens x 32 heads of 128 dims: 26.7 us, 28.7 with 256)
+constexpr int kRopeThreads = 128;  // (8000 tokens x 32 heads of 128 dims: 24.5 us, 25.9 with 256)
 // Heads whose loads are in flight together (8000 tokens x 32 heads of 128 dims:
-// 25.6 us with one, 23.3 with two, 25.2 with four).
+// 26.6 us with one, 24.5 with two, 23.9 with four; 256 x 128 tails 7.5, 7.8 and 8.0).
 constexpr int kAtOnce = 2;
 
 template <typename T>
@@ -188,8 +189,9 @@ cudaError_t launch(const RopeParams& p, const mla_rope_table_t& table, cudaStrea
   g.cols = g.rot_cols + (p.x == p.y ? 0 : (p.head_dim - table.rope_dim) / (VE * sizeof(T) == 16 ? VE : 1));
   // Long head runs spread a column's sines over more heads, short ones keep
   // every SM busy when there are few tokens.  The 64-dim tails of 128 heads in
-  // runs of 8 and head by head: 1024 tokens 5.6 and 9.2 us, 32 tokens 3.1 and
-  // 2.4; of 256 tokens, not in L2, 10.3 in runs of 8 and 8.2 in runs of 4.
+  // runs of 8 and head by head, one call alone between two events: 1024 tokens
+  // 12.4 and 18.9 us, 32 tokens 8.3 and 6.2; 256 tokens 10.2 in runs of 8, 8.2 in
+  // runs of 4.
   g.heads_per = 8;
   while (g.heads_per > 1 &&
          p.n * ((p.heads + g.heads_per - 1) / g.heads_per) * g.cols < static_cast<int64_t>(sms) * 384)

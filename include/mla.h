@@ -417,7 +417,8 @@ typedef struct {
   int32_t h_q;          /* query heads, 1 .. 128 */
   int32_t head_dim;     /* must be 512 */
   int32_t page_size;    /* must be 64 */
-  int32_t max_pages;    /* entries of a block table row */
+  int32_t max_pages;    /* entries of a block table row; a table no wider than the sequences need is faster
+                           for short ones, as the plan knows their lengths by it */
   int32_t window;       /* tokens seen back from the query token, itself included; 0 = all */
   int32_t sinks;        /* the first tokens of a sequence, seen whatever the window */
   int64_t num_pages;    /* pages in the pool (bounds check of the block table) */
