@@ -59,21 +59,28 @@ constexpr int kMaxDevices = 64;
 int g_sm_count[kMaxDevices] = {0};
 std::mutex g_sm_mutex;
 
+// A call that CUDA refused: its error is reported here and does not stay with
+// the thread, where the next launch's check would take it for its own.
+mla_status_t cuda_failed() {
+  (void)cudaGetLastError();
+  return MLA_ERR_CUDA;
+}
+
 mla_status_t device_sm_count(int* out) {
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return MLA_ERR_CUDA;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cuda_failed();
   if (dev >= 0 && dev < kMaxDevices) {
     std::lock_guard<std::mutex> lock(g_sm_mutex);
     if (g_sm_count[dev] == 0) {
       int n = 0;
-      if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return MLA_ERR_CUDA;
+      if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return cuda_failed();
       g_sm_count[dev] = n;
     }
     *out = g_sm_count[dev];
     return MLA_OK;
   }
   int n = 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return MLA_ERR_CUDA;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return cuda_failed();
   *out = n;
   return MLA_OK;
 }
@@ -211,7 +218,7 @@ mla_status_t decode_launch(const mla_problem_t* problem, const void* q, const vo
       default: e = launch_decode<16>(p, grid, s); break;
     }
   }
-  if (e != cudaSuccess) return MLA_ERR_CUDA;
+  if (e != cudaSuccess) return cuda_failed();
   return MLA_OK;
 }
 
@@ -250,7 +257,7 @@ mla_status_t mla_get_metadata(const mla_problem_t* problem, int32_t num_sms, int
   if (d_sched == nullptr) return MLA_OK;
   const int nq = problem->batch * problem->seq_len_q;
   if (launch_metadata(pl, nq, d_sched, d_num_splits, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
-    return MLA_ERR_CUDA;
+    return cuda_failed();
   return MLA_OK;
 }
 
@@ -274,7 +281,7 @@ mla_status_t mla_sparse_decode(const mla_problem_t* problem, const void* q, cons
     const int32_t* by_part = num_parts < p.nq ? d_sched : nullptr;
     if (launch_combine(d_num_splits, p.ws_o, p.ws_lse, p.out, lse, p.nq, problem->h_q, true, by_part, num_parts,
                        p.T, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
-      return MLA_ERR_CUDA;
+      return cuda_failed();
   }
   return MLA_OK;
 }
@@ -304,7 +311,7 @@ mla_status_t mla_sparse_decode_rope_fp8(const mla_problem_t* problem, const void
   if (launch_rope_fp8(d_num_splits, p.ws_o, p.ws_lse, positions, ro.freqs, ro.out, lse, p.nq, problem->h_q, true,
                       num_parts < p.nq ? d_sched : nullptr, num_parts, p.T,
                       reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
-    return MLA_ERR_CUDA;
+    return cuda_failed();
   return MLA_OK;
 }
 
@@ -320,7 +327,7 @@ mla_status_t mla_combine(const mla_problem_t* problem, const int32_t* d_num_spli
   const int nq = problem->batch * problem->seq_len_q;
   if (launch_combine(d_num_splits, o_partial, lse_partial, static_cast<uint16_t*>(out), lse, nq, problem->h_q,
                      false, nullptr, 0, 0, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
-    return MLA_ERR_CUDA;
+    return cuda_failed();
   return MLA_OK;
 }
 
@@ -333,7 +340,7 @@ mla_status_t mla_dequantize(int32_t kv_format, const void* records, int64_t n, v
   if (n * 32 >= (int64_t(1) << 40)) return MLA_ERR_UNSUPPORTED;
   if (launch_dequant(kv_format, static_cast<const uint8_t*>(records), n, static_cast<uint16_t*>(out),
                      reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
-    return MLA_ERR_CUDA;
+    return cuda_failed();
   return MLA_OK;
 }
 
@@ -352,7 +359,7 @@ mla_status_t mla_kv_write(int32_t kv_format, const void* latents, const int32_t*
   const int64_t pool_tokens = num_pages * MLA_PAGE_SIZE < cap ? num_pages * MLA_PAGE_SIZE : cap;
   if (launch_kv_write(kv_format, static_cast<const uint16_t*>(latents), slots, n, static_cast<uint8_t*>(pool),
                       pool_tokens, d_error, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
-    return MLA_ERR_CUDA;
+    return cuda_failed();
   return MLA_OK;
 }
 
@@ -378,7 +385,7 @@ mla_status_t mla_page_plan(const int32_t* cached_lens, const int32_t* new_lens, 
   if (launch_page_plan(cached_lens, new_lens, batch, block_table, max_pages, free_pages, num_pages, num_free, seq_lens,
                        num_free_out, cu_new, slots, positions, max_new, d_error,
                        reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
-    return MLA_ERR_CUDA;
+    return cuda_failed();
   return MLA_OK;
 }
 
@@ -463,7 +470,7 @@ mla_status_t mla_rope(int32_t dtype, const void* x, int64_t x_row_stride, int64_
   if (n >= (int64_t(1) << 31) || head_dim > (1 << 20) || heads > (1 << 20)) return MLA_ERR_UNSUPPORTED;
   const RopeParams p{x, y, x_row_stride, x_head_stride, y_row_stride, y_head_stride, n, heads, head_dim, offset,
                      positions, conjugate != 0};
-  if (launch_rope(dtype, p, *table, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return MLA_ERR_CUDA;
+  if (launch_rope(dtype, p, *table, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return cuda_failed();
   return MLA_OK;
 }
 
@@ -500,7 +507,7 @@ mla_status_t mla_rms_norm_fp8(int32_t dtype, const void* x, int64_t x_stride, co
   p.dim = dim;
   p.eps = eps;
   p.d_error = d_error;
-  if (launch_rms_norm_fp8(dtype, p, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return MLA_ERR_CUDA;
+  if (launch_rms_norm_fp8(dtype, p, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return cuda_failed();
   return MLA_OK;
 }
 
@@ -556,7 +563,7 @@ mla_status_t mla_paged_decode_fp4(const mla_paged_problem_t* problem, const void
   p.sinks = problem->sinks;
   p.num_pages = problem->num_pages;
   p.scale_log2 = problem->sm_scale * kLog2e;
-  if (launch_paged_decode(p, pl, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return MLA_ERR_CUDA;
+  if (launch_paged_decode(p, pl, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return cuda_failed();
   return MLA_OK;
 }
 

@@ -45,7 +45,10 @@ extern "C" mla_status_t mla_sparse_decode_noalloc(const mla_problem_t* problem, 
   // The same workspace size mla_get_metadata reports for this part count.
   if (mla::plan_for_parts(problem, num_parts).ws_bytes > MLA_NOALLOC_SCRATCH_BYTES) return MLA_ERR_WORKSPACE;
   void* scratch = nullptr;
-  if (cudaGetSymbolAddress(&scratch, g_decode_scratch) != cudaSuccess || scratch == nullptr) return MLA_ERR_CUDA;
+  if (cudaGetSymbolAddress(&scratch, g_decode_scratch) != cudaSuccess || scratch == nullptr) {
+    (void)cudaGetLastError();  // (reported here, not by the next launch's check)
+    return MLA_ERR_CUDA;
+  }
   return mla_sparse_decode(problem, q, kv, indices, extra_kv, extra_indices, d_sched, d_num_splits, num_parts,
                            scratch, MLA_NOALLOC_SCRATCH_BYTES, out, lse, d_error, stream);
 }
