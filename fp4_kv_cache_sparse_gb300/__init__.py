@@ -310,6 +310,8 @@ def _arg(t, dev, dtype, what, shape=None):
 
 def _call(fn, what, dev, stream, *args):
     """fn(*args, stream) on device dev."""
+    if stream is not None and getattr(stream, "device_index", dev) != dev:
+        raise ValueError(f"{what}: stream of device {stream.device_index}, tensors on device {dev}")
     raw = stream.cuda_stream if stream is not None else _raw_stream(dev)
     if dev == _current_device():
         status = fn(*args, raw)

@@ -230,6 +230,17 @@ def test_paged_plan_grows_with_parts_not_with_lengths(num_sms):
 # ---------------------------------------------------------------- binding
 
 
+def test_binding_refuses_a_stream_of_another_device():
+    class Stream:
+        device_index, cuda_stream = 1, 0
+
+    def never(*args):
+        raise AssertionError("the call must not be made")
+
+    with pytest.raises(ValueError, match="stream of device 1"):
+        mla._call(never, "mla_rope", 0, Stream())
+
+
 def test_binding_refuses_cpu_tensors():
     i = torch.zeros(4, dtype=torch.int32)
     with pytest.raises(ValueError):
