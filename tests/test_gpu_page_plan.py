@@ -193,6 +193,27 @@ def test_replayed_graph_advances_the_state_in_place():
     assert (c.tolist(), int(k), cu.tolist(), slots.tolist(), pos.tolist(), tab.tolist()) == want[:6]
 
 
+def test_replayed_graph_with_a_long_map():
+    """The map's own kernel, captured behind the plan: requests of 5000 tokens grow from replay to replay, then end."""
+    cached, new, table, free, nf, num_pages = make(6, 24, 320, lambda r: 5000, spare=7000, cached_of=lambda: 70)
+    t = lambda v: torch.tensor(v, dtype=torch.int32, device=DEV)  # noqa: E731
+    room = 24 * 5000 + 3
+    c, n, tab, f, k = t(cached), t(new), t(table), t(free), t([nf])
+    cu, slots, pos, err = t([0] * 25), torch.zeros(room, dtype=torch.int32, device=DEV), t([0] * room), t([0])
+    s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(g, stream=s):
+        mla.page_plan(c, n, tab, f, k, c, k, cu, slots, pos, error=err)
+    want = (cached, nf, None, None, None, table, list(free))
+    for step in ([5000] * 24, [5000, 0] * 12, [-1, 5000] * 12, [4999] * 24):
+        n.copy_(t(step))
+        g.replay()
+        torch.cuda.synchronize()
+        want = reference(want[0], step, want[5], want[6], want[1], room, num_pages)
+        assert want is not None and int(err) == 0
+        assert (c.tolist(), int(k), cu.tolist(), slots.tolist(), pos.tolist(), tab.tolist()) == want[:6]
+
+
 def test_slots_at_odd_addresses():
     cached, new, table, free, nf, num_pages = make(9, 7, 5, lambda r: 33, spare=10)
     t = lambda v: torch.tensor(v, dtype=torch.int32, device=DEV)  # noqa: E731

@@ -254,6 +254,17 @@ def test_scores_far_past_what_a_softmax_tells_apart(s, h, bits):
     assert alone > len(c.lens) * s * h / (8 if bits > 20 else 40)
 
 
+@pytest.mark.parametrize("sm_scale", [-0.05, -1.0, 0.0, 1e-30, -3e-38, 1e-44, 2.0])
+@pytest.mark.parametrize("s,h", [(1, 16), (3, 24), (1, 64)])
+def test_scales_of_either_sign_and_none(s, h, sm_scale):
+    """A negative scale turns the order of the scores round; one of 0 or far below any score leaves an average."""
+    c = Case([0, 1, 130, 700, 2000], s, h, seed=41)
+    for window, sinks in ((0, 0), (150, 70)):
+        out, lse, err = c.run(sm_scale=sm_scale, window=window, sinks=sinks)
+        assert err == 0
+        c.check(out, lse, window, sinks, sm_scale=sm_scale)
+
+
 def test_a_peak_and_a_long_tail():
     """One token carries most of the mass; the other 40000 each have 2^-22 of its weight, 1 % together."""
     n = 40000
