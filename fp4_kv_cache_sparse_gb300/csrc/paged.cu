@@ -47,9 +47,9 @@
 //
 // What bounds it: shared memory.  A tile's 128 KB of V are written and read,
 // the raw tile is written once and read twice (108 KB), Q is read once and P
-// four times as B operands.  With 16 rows that and the small operands are 3860
-// accesses of 128 bytes a tile (2580 by the warps, 1280 by the tensor core),
-// with 64 rows 5520 (3470 and 2050), in 4250 and 6130 cycles: nine tenths of
+// four times as B operands.  With 16 rows that and the small operands are 3820
+// accesses of 128 bytes a tile (2540 by the warps, 1280 by the tensor core),
+// with 64 rows 5270 (3220 and 2050), in 4230 and 6000 cycles: nine tenths of
 // what shared memory can do, and the tensor core is busy for 510 and 2050 of
 // them.  So 32 x 16 heads over 64k tokens take 222 us (604 MB, 40 % of a copy's
 // bandwidth), 64 x 64 heads over 1k to 8k tokens 63 us (38.7 GFLOP, 32 % of the
