@@ -391,7 +391,10 @@ mla_status_t mla_rope(int32_t dtype, const void* x, int64_t x_row_stride, int64_
  * (scale byte 127 + e; 127 for an all-zero block; e >= -127), each value
  * rounded to the nearest E4M3FN.  The norm is taken of the unrounded sum.
  * codes and scales have row strides of their own, so with dim 512, codes = r
- * and scales = r + 512 at stride 528 the rows are cache records.
+ * and scales = r + 512 at stride 528 the rows have the form of FP8 records
+ * (mla_dequantize reads them; mla_rope and mla_kv_write take 16-bit rows, so a
+ * latent is rotated and written from those).  Outputs overlap no input but as
+ * said, and not one another.
  *   x, residual, residual_out, weight  dtype; rows at element strides, each
  *             row 16-byte aligned (weight [dim], 16-byte aligned).
  *   codes     uint8, rows 8-byte aligned; scales uint8 [n][dim / 32].
