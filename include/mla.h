@@ -400,7 +400,8 @@ mla_status_t mla_rope(int32_t dtype, const void* x, int64_t x_row_stride, int64_
  *   codes     uint8, rows 8-byte aligned; scales uint8 [n][dim / 32].
  *   dim       a multiple of 32, at most 16384 (MLA_ERR_UNSUPPORTED otherwise).
  *   d_error   device int32 or NULL; bits are OR-ed into it (MLA_DEVERR_TIMEOUT
- *             when a row's copy did not arrive: that row is not written).
+ *             when a row's copy did not arrive: that row is not written, nor
+ *             are those that its block has not asked for by then).
  * Infinities and NaN in a row make that row's codes undefined, and so does a
  * mean(s^2) + eps that fp32 cannot hold (0, as of a row of zeros with eps = 0,
  * or a sum of squares past 3.4e38); no other row.
