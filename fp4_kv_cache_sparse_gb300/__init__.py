@@ -20,7 +20,7 @@ __all__ = [
     "dequantize", "kv_write",
     "SparseMLADecoder", "decode", "KV_NONE", "KV_FP8_528", "KV_FP4_288", "KV_BF16",
     "DEVERR_BAD_INDEX", "DEVERR_TIMEOUT", "DEVERR_BAD_METADATA", "DEVERR_NO_ROOM", "DEVERR_BAD_LENGTH", "SCHED_INTS",
-    "page_plan", "RopeScaling", "RopeTable", "rope", "rms_norm_fp8",
+    "page_plan", "RopeScaling", "RopeTable", "rope", "kv_append", "page_means", "rms_norm_fp8",
     "PagedProblem", "paged_decode_plan", "paged_decode_fp4", "PagedFP4Decoder",
 ]
 
@@ -34,6 +34,7 @@ HEAD_DIM = 512
 PAGE_SIZE = 64
 FP8_RECORD_BYTES = 528
 FP4_RECORD_BYTES = 288
+MEAN_BYTES = 528
 
 STATUS = {0: "MLA_OK", 1: "MLA_ERR_INVALID_ARG", 2: "MLA_ERR_UNSUPPORTED", 3: "MLA_ERR_WORKSPACE",
           4: "MLA_ERR_CUDA", 5: "MLA_ERR_TIMEOUT"}
@@ -116,6 +117,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.mla_rope_table.argtypes = [P, I32, I32, D, I32, D, D, D, D, D]
     lib.mla_rope_table_from_freqs.argtypes = [P, I32, I32, P, D]
     lib.mla_rope.argtypes = [I32, P, I64, I64, P, I64, I64, I64, I32, I32, I32, P, P, I32, P]
+    lib.mla_kv_append.argtypes = [I32, I32, P, I64, I64, P, I32, P, P, P, I64, P, P]
+    lib.mla_page_means.argtypes = [P, I64, P, I64, P, P, P]
     lib.mla_rms_norm_fp8.argtypes = [I32, P, I64, P, I64, P, F, P, I64, P, I64, P, I64, I64, I32, P, P]
     lib.mla_paged_decode_plan.argtypes = [P, I32, ctypes.POINTER(I32), ctypes.POINTER(SZ)]
     lib.mla_paged_decode_fp4.argtypes = [P, P, P, P, P, I32, P, SZ, P, P, P, P]
@@ -123,7 +126,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.mla_status_string.restype = ctypes.c_char_p
     for f in (lib.mla_get_metadata, lib.mla_sparse_decode, lib.mla_sparse_decode_rope_fp8, lib.mla_combine,
               lib.mla_dequantize, lib.mla_kv_write, lib.mla_page_plan, lib.mla_rope_table,
-              lib.mla_rope_table_from_freqs, lib.mla_rope, lib.mla_rms_norm_fp8, lib.mla_paged_decode_plan,
+              lib.mla_rope_table_from_freqs, lib.mla_rope, lib.mla_kv_append, lib.mla_page_means, lib.mla_rms_norm_fp8, lib.mla_paged_decode_plan,
               lib.mla_paged_decode_fp4):
         f.restype = ctypes.c_int
     if path == _build.LIB:
@@ -437,6 +440,64 @@ def _rows(t, dev, dtype, what, shape):
     if s1 != 1 and shape[1] > 1:
         raise ValueError(f"{what}: rows must be dense")
     return t.data_ptr(), s0 if shape[0] > 1 else shape[1]
+
+
+def _pool(pool, dev, rec, num_pages, what):
+    """Address and page count of a uint8 pool of records: [num_pages, 64, rec] or [tokens, rec], or any of that size."""
+    ptr = _arg(pool, dev, torch.uint8, "pool")
+    held = pool.numel() // (PAGE_SIZE * rec)
+    if num_pages is None:
+        num_pages = held
+    if num_pages < 0 or num_pages > held:
+        raise ValueError(f"{what}: the pool holds {held} pages of {rec}-byte records, not {num_pages}")
+    return ptr, num_pages
+
+
+def kv_append(latents, slots, pool, kv_format: int = KV_FP8_528, rope: RopeTable = None, positions=None,
+              offset: int = 448, num_pages: int = None, error=None, stream=None) -> None:
+    """New tokens into the paged pool, their rotary positions applied on the
+    way (mla_kv_append): dims offset .. offset + rope.rope_dim - 1 of each row
+    of latents [n, 512] (bf16, fp16 or fp32, any row stride of whole 16 bytes)
+    turn to positions int32 [n]; each row becomes an FP8 (528-byte) or FP4
+    (288-byte) record at its slot (page*64 + offset, -1 = skip) of the uint8
+    pool [num_pages, 64, record].  Without rope nothing turns."""
+    lib = load()
+    dev = _device_of(latents, "kv_append")
+    dtype = _DTYPES.get(latents.dtype)
+    if dtype is None or latents.dim() != 2 or latents.shape[1] != HEAD_DIM:
+        raise ValueError("kv_append: latents are [n, 512] in bfloat16, float16 or float32 "
+                         f"(got {latents.dtype}, {tuple(latents.shape)})")
+    n = latents.shape[0]
+    px, sx = _rows(latents, dev, latents.dtype, "latents", latents.shape)
+    if rope is None and positions is not None:
+        raise ValueError("kv_append: positions without a rope table")
+    if rope is not None and positions is None:
+        raise ValueError("kv_append: a rope table needs positions")
+    if kv_format not in (KV_FP8_528, KV_FP4_288):
+        raise MLAError(2 if kv_format == KV_BF16 else 1, "mla_kv_append")
+    ptr, num_pages = _pool(pool, dev, FP8_RECORD_BYTES if kv_format == KV_FP8_528 else FP4_RECORD_BYTES, num_pages,
+                           "kv_append")
+    ps = _arg(slots, dev, torch.int32, "slots", (n,))
+    pp = _arg(positions, dev, torch.int32, "positions", (n,))
+    _call(lib.mla_kv_append, "mla_kv_append", dev, stream, kv_format, dtype, px, sx, n, rope.ref if rope is not None else None,
+          offset, pp, ps, ptr, num_pages, _arg(error, dev, torch.int32, "error"))
+
+
+def page_means(pool, slots, means, num_pages: int = None, error=None, stream=None) -> None:
+    """The 8-bit means of the pages that slots (int32 [n]) complete, those with
+    a slot % 64 == 63 in the list, from the FP4 pool [num_pages, 64, 288] into
+    means uint8 [num_pages, 528] (mla_page_means): 512 int8 codes, the byte
+    127 + e of their scale, zeros."""
+    lib = load()
+    dev = _device_of(pool, "page_means")
+    ptr, num_pages = _pool(pool, dev, FP4_RECORD_BYTES, num_pages, "page_means")
+    if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
+        raise ValueError("page_means: slots are int32 [n]")
+    pm = _arg(means, dev, torch.uint8, "means")
+    if means.numel() < num_pages * MEAN_BYTES:
+        raise ValueError(f"means: expected {num_pages} records of {MEAN_BYTES} bytes")
+    _call(lib.mla_page_means, "mla_page_means", dev, stream, ptr, num_pages, _arg(slots, dev, torch.int32, "slots"),
+          slots.shape[0], pm, _arg(error, dev, torch.int32, "error"))
 
 
 def rms_norm_fp8(x, weight, eps: float, codes, scales, residual=None, residual_out=None, error=None,

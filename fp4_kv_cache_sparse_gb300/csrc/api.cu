@@ -129,6 +129,17 @@ mla_status_t validate_paged(const mla_paged_problem_t* p) {
   return MLA_OK;
 }
 
+bool rope_table_ok(const mla_rope_table_t& t) {
+  return t.rope_dim >= 2 && t.rope_dim <= MLA_ROPE_MAX_DIM && (t.rope_dim & 1) == 0 &&
+         (t.layout == MLA_ROPE_INTERLEAVED || t.layout == MLA_ROPE_HALF) && std::isfinite(t.factor);
+}
+
+// Slots of a pool that an int32 can name.
+int64_t pool_tokens(int64_t num_pages) {
+  const int64_t cap = int64_t(1) << 31;
+  return num_pages < cap / MLA_PAGE_SIZE ? num_pages * MLA_PAGE_SIZE : cap;
+}
+
 // Where the decode kernels write the fused epilogue's FP8 records of query
 // tokens that have one split.
 struct RopeOut {
@@ -450,9 +461,7 @@ mla_status_t mla_rope(int32_t dtype, const void* x, int64_t x_row_stride, int64_
                       mla_stream_t stream) {
   const int bytes = element_bytes(dtype);
   if (bytes == 0 || table == nullptr || n < 0 || heads < 1 || head_dim < 1 || offset < 0) return MLA_ERR_INVALID_ARG;
-  if (table->rope_dim < 2 || table->rope_dim > MLA_ROPE_MAX_DIM || (table->rope_dim & 1) != 0 ||
-      (table->layout != MLA_ROPE_INTERLEAVED && table->layout != MLA_ROPE_HALF) || !std::isfinite(table->factor))
-    return MLA_ERR_INVALID_ARG;
+  if (!rope_table_ok(*table)) return MLA_ERR_INVALID_ARG;
   if (static_cast<int64_t>(offset) + table->rope_dim > head_dim) return MLA_ERR_INVALID_ARG;
   if (x_row_stride < 0 || x_head_stride < 0 || y_row_stride < 0 || y_head_stride < 0) return MLA_ERR_INVALID_ARG;
   if (n == 0) return MLA_OK;
@@ -471,6 +480,56 @@ mla_status_t mla_rope(int32_t dtype, const void* x, int64_t x_row_stride, int64_
   const RopeParams p{x, y, x_row_stride, x_head_stride, y_row_stride, y_head_stride, n, heads, head_dim, offset,
                      positions, conjugate != 0};
   if (launch_rope(dtype, p, *table, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return cuda_failed();
+  return MLA_OK;
+}
+
+mla_status_t mla_kv_append(int32_t kv_format, int32_t dtype, const void* latents, int64_t row_stride, int64_t n,
+                           const mla_rope_table_t* table, int32_t offset, const int32_t* positions,
+                           const int32_t* slots, void* pool, int64_t num_pages, int32_t* d_error,
+                           mla_stream_t stream) {
+  if (kv_format != MLA_KV_FP8_528 && kv_format != MLA_KV_FP4_288)
+    return kv_format == MLA_KV_BF16 ? MLA_ERR_UNSUPPORTED : MLA_ERR_INVALID_ARG;
+  const int bytes = element_bytes(dtype);
+  if (bytes == 0 || n < 0 || num_pages < 0 || offset < 0) return MLA_ERR_INVALID_ARG;
+  if (table != nullptr) {
+    if (!rope_table_ok(*table) || static_cast<int64_t>(offset) + table->rope_dim > MLA_HEAD_DIM)
+      return MLA_ERR_INVALID_ARG;
+  }
+  if (n == 0) return MLA_OK;
+  if (latents == nullptr || slots == nullptr || pool == nullptr || (table != nullptr && positions == nullptr))
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned16(latents) || !aligned16(pool) || !aligned_to(slots, 4) || !aligned_to(positions, 4))
+    return MLA_ERR_INVALID_ARG;
+  if (row_stride < 0 || (n > 1 && row_stride > (int64_t(1) << 31))) return MLA_ERR_INVALID_ARG;
+  if (n > 1 && (row_stride * bytes) % 16 != 0) return MLA_ERR_INVALID_ARG;
+  if (n >= (int64_t(1) << 31)) return MLA_ERR_UNSUPPORTED;
+  AppendParams p{};
+  p.latents = latents;
+  p.positions = positions;
+  p.slots = slots;
+  p.pool = static_cast<uint8_t*>(pool);
+  p.row_stride = row_stride;
+  p.n = n;
+  p.pool_tokens = pool_tokens(num_pages);
+  p.offset = offset;
+  p.d_error = d_error;
+  static const mla_rope_table_t kNone{};  // no pairs
+  if (launch_kv_append(kv_format, dtype, p, table != nullptr ? *table : kNone,
+                       reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return cuda_failed();
+  return MLA_OK;
+}
+
+mla_status_t mla_page_means(const void* pool, int64_t num_pages, const int32_t* slots, int64_t n, void* means,
+                            int32_t* d_error, mla_stream_t stream) {
+  if (n < 0 || num_pages < 0) return MLA_ERR_INVALID_ARG;
+  if (n == 0) return MLA_OK;
+  if (pool == nullptr || slots == nullptr || means == nullptr) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(pool) || !aligned16(means) || !aligned_to(slots, 4)) return MLA_ERR_INVALID_ARG;
+  if (n >= (int64_t(1) << 31)) return MLA_ERR_UNSUPPORTED;
+  if (launch_page_means(static_cast<const uint8_t*>(pool), pool_tokens(num_pages), slots, n,
+                        static_cast<uint8_t*>(means), d_error, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return cuda_failed();
   return MLA_OK;
 }
 

@@ -21,6 +21,7 @@
 #include "../../include/mla.h"
 #include "mla_device.cuh"
 #include "mla_internal.h"
+#include "mla_rows.cuh"
 
 namespace mla {
 
@@ -29,27 +30,6 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kRecFp8Bytes = 528;
 constexpr int kRecFp4Bytes = 288;
-
-// Eight floats -> eight e2m1 nibbles (x[0] in the low nibble of byte 0).
-__device__ __forceinline__ uint32_t e2m1x8(const float (&x)[8]) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
-      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
-      : "=r"(r)
-      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
-  return r;
-}
-
-// E4M3FN byte -> float, exactly (through f16, which holds every e4m3 value).
-__device__ __forceinline__ float e4m3_to_float(uint32_t byte) {
-  uint32_t h2;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(byte)));
-  return __half2float(__ushort_as_half(static_cast<unsigned short>(h2 & 0xFFFFu)));
-}
 
 // 16 bf16 values of this lane (dims 16 lane .. 16 lane + 15) as floats.
 __device__ __forceinline__ void load16(const uint16_t* src, float (&x)[16]) {

@@ -112,6 +112,22 @@ struct RopeParams {
 };
 cudaError_t launch_rope(int dtype, const RopeParams& p, const mla_rope_table_t& table, cudaStream_t stream);
 
+// New tokens' latents, turned on the way into their records; row stride in elements.
+struct AppendParams {
+  const void* latents;
+  const int32_t* positions;  // null when nothing turns
+  const int32_t* slots;
+  uint8_t* pool;
+  int64_t row_stride, n, pool_tokens;
+  int offset;
+  int32_t* d_error;          // nullable
+};
+cudaError_t launch_kv_append(int kv_format, int dtype, const AppendParams& p, const mla_rope_table_t& table,
+                             cudaStream_t stream);
+
+cudaError_t launch_page_means(const uint8_t* pool, int64_t pool_tokens, const int32_t* slots, int64_t n, uint8_t* means,
+                              int32_t* d_error, cudaStream_t stream);
+
 // RMS norm with the residual's addition to FP8 blocks; strides in elements.
 struct NormParams {
   const void* x;

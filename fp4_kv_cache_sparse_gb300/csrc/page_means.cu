@@ -1,0 +1,177 @@
+// page_means.cu -- the mean of a full page's 64 latents in 8 bits
+// (include/mla.h, mla_page_means): what a page is about, for the selection of
+// pages to read 513 bytes of it instead of 18432.
+//
+// A decoded value is a multiple of 2^-10 (e2m1 in halves, e4m3 in 2^-9) below
+// 2^12, so the sum S_d of 64 of them is an integer below 2^28 in that unit,
+// and every step here is exact: four tokens' sums fit fp32 (4 * 2688 * 2^10 <
+// 2^24), the rest are 32-bit integers, in any order.  With the least e' that
+// gives max |S| 2^-e' <= 127 the codes are S_d 2^-e', rounded half to even, and
+// the page's scale is 2^(e' - 16).
+//
+// One block per page, 16 lanes to a record's 512 dims (32 each), four records a
+// thread.  The next page's records are on their way while this one is summed up.
+// Which pages: those whose last slot (offset 63) is in the list, as tokens are
+// appended in order.  Blocks take the list's entries at an odd stride, so that
+// the pages of one request, 64 entries apart, spread over all of them.
+#include <cstdint>
+
+#include "mla_device.cuh"
+#include "mla_internal.h"
+
+namespace mla {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTokens = kPage / (kThreads / 16);  // records of a thread
+
+struct Piece {
+  uint4 data;
+  uint32_t sc;
+};
+
+// The 32 dims' values, two e4m3 scales; a NaN scale counts as 448.
+__device__ __forceinline__ void add32(const Piece& p, float (&acc)[32]) {
+  uint32_t s2 = e4m3x2_to_f16x2(p.sc & 0x7F7Fu);
+  asm("min.f16x2 %0, %0, %1;" : "+r"(s2) : "r"(0x5F005F00u));
+  s2 |= (p.sc & 0x80u) << 8 | (p.sc & 0x8000u) << 16;
+  const uint32_t w[4] = {p.data.x, p.data.y, p.data.z, p.data.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t s = k < 2 ? __byte_perm(s2, s2, 0x1010) : __byte_perm(s2, s2, 0x3232);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t h = e2m1x2_to_f16x2((w[k] >> (8 * j)) & 0xFFu);
+      uint32_t v;
+      asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(v) : "r"(h), "r"(s));
+      float lo, hi;
+      asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+          : "=f"(lo), "=f"(hi)
+          : "r"(v));
+      acc[8 * k + 2 * j] += lo;
+      acc[8 * k + 2 * j + 1] += hi;
+    }
+  }
+}
+
+// 128 dims' worth of columns is skewed by 4 words, so that lanes that write 32
+// words each do not meet in the same banks.
+__device__ __forceinline__ int column(int d) { return d + (d >> 5) * 4; }
+constexpr int kRow = kD + (kD / 32) * 4;
+
+__global__ void __launch_bounds__(kThreads, 3)
+    page_means_kernel(const uint8_t* pool, int64_t pool_tokens, const int32_t* slots, int64_t n, uint8_t* means,
+                      int32_t* d_error) {
+  __shared__ int sums[kThreads / 32][kRow];
+  __shared__ int32_t pages[kThreads];
+  __shared__ uint32_t counts[kThreads / 32];
+  __shared__ uint32_t tops[kThreads / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  for (int64_t base = blockIdx.x; base < n; base += static_cast<int64_t>(gridDim.x) * kThreads) {
+    // Up to kThreads entries of the list; those that complete a page, in order.
+    const int64_t i = base + static_cast<int64_t>(tid) * gridDim.x;
+    int32_t slot = -1;
+    if (i < n) slot = slots[i];
+    const bool good = slot >= 0 && slot < pool_tokens;
+    if (!good && slot != -1 && d_error) atomicOr(d_error, MLA_DEVERR_BAD_INDEX);
+    const bool full = good && slot % kPage == kPage - 1;
+    const uint32_t vote = __ballot_sync(0xFFFFFFFFu, full);
+    if (lane == 0) counts[warp] = __popc(vote);
+    __syncthreads();
+    int before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += counts[w];
+      total += counts[w];
+    }
+    if (full) pages[before + __popc(vote & ((1u << lane) - 1))] = slot / kPage;
+    __syncthreads();
+
+    Piece next[kTokens];
+    const auto fetch = [&](int k) {
+      const uint8_t* rec = pool + (static_cast<int64_t>(pages[k]) * kPage + (tid >> 4) * kTokens) * kRecFp4;
+#pragma unroll
+      for (int j = 0; j < kTokens; ++j) {
+        next[j].data = *reinterpret_cast<const uint4*>(rec + j * kRecFp4 + (tid & 15) * 16);
+        next[j].sc = *reinterpret_cast<const uint16_t*>(rec + j * kRecFp4 + 256 + (tid & 15) * 2);
+      }
+    };
+    if (total > 0) fetch(0);
+    for (int k = 0; k < total; ++k) {
+      float acc[32];
+#pragma unroll
+      for (int c = 0; c < 32; ++c) acc[c] = 0.f;
+#pragma unroll
+      for (int j = 0; j < kTokens; ++j) add32(next[j], acc);
+      if (k + 1 < total) fetch(k + 1);
+      // In units of 2^-10; lanes l and l + 16 have the same dims.
+#pragma unroll
+      for (int c = 0; c < 32; c += 4) {
+        int v[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          v[m] = static_cast<int>(acc[c + m] * 1024.f);
+          v[m] += __shfl_xor_sync(0xFFFFFFFFu, v[m], 16);
+        }
+        if ((lane >> 4) == ((c >> 2) & 1))
+          *reinterpret_cast<int4*>(&sums[warp][column((lane & 15) * 32 + c)]) = make_int4(v[0], v[1], v[2], v[3]);
+      }
+      __syncthreads();
+      // Thread t: dims 2 t and 2 t + 1.
+      int a = 0, b = 0;
+#pragma unroll
+      for (int w = 0; w < kThreads / 32; ++w) {
+        const int2 v = *reinterpret_cast<const int2*>(&sums[w][column(2 * tid)]);
+        a += v.x;
+        b += v.y;
+      }
+      uint32_t top = max(abs(a), abs(b));
+      top = __reduce_max_sync(0xFFFFFFFFu, top);
+      if (lane == 0) tops[warp] = top;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kThreads / 32; ++w) top = max(top, tops[w]);
+      // 2^e' with top * 2^-e' in (63.5, 127].
+      int e = 0;
+      if (top > 0) {
+        e = 25 - __clz(top);  // the leading bit to 2^6
+        if (e > 0 && top > (127u << e)) ++e;
+      }
+      const auto code = [&](int v) -> uint32_t {
+        if (e <= 0) return static_cast<uint32_t>(v * (1 << -e)) & 0xFFu;
+        // Half to even: what is added makes exact halves carry only into odd codes.
+        return static_cast<uint32_t>((v + (1 << (e - 1)) - 1 + ((v >> e) & 1)) >> e) & 0xFFu;
+      };
+      uint8_t* rec = means + static_cast<int64_t>(pages[k]) * MLA_MEAN_BYTES;
+      *reinterpret_cast<uint16_t*>(rec + 2 * tid) = static_cast<uint16_t>(code(a) | (code(b) << 8));
+      if (tid < 4)
+        *reinterpret_cast<uint32_t*>(rec + kD + 4 * tid) = tid == 0 ? static_cast<uint32_t>(127 + (top > 0 ? e - 16 : 0)) : 0u;
+    }
+    __syncthreads();  // the page list may change again
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_page_means(const uint8_t* pool, int64_t pool_tokens, const int32_t* slots, int64_t n, uint8_t* means,
+                              int32_t* d_error, cudaStream_t stream) {
+  int dev = 0, sms = 152;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int64_t most = static_cast<int64_t>(sms) * 4 - 1;  // odd
+  const int64_t blocks = n < most ? n : most;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.stream = stream;
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(kThreads);
+  return cudaLaunchKernelEx(&cfg, page_means_kernel, pool, pool_tokens, slots, n, means, d_error);
+}
+
+}  // namespace mla

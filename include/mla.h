@@ -383,6 +383,50 @@ mla_status_t mla_rope(int32_t dtype, const void* x, int64_t x_row_stride, int64_
                       mla_stream_t stream);
 
 /*
+ * New tokens into the paged pool with their rotary positions applied on the
+ * way: mla_rope on dims offset .. offset + rope_dim - 1 of each latent and
+ * mla_kv_write of the result, in one pass and with one rounding, that to the
+ * record (the turned values are fp32 in between).
+ *   kv_format  MLA_KV_FP8_528 or MLA_KV_FP4_288; records as mla_kv_write makes them.
+ *   dtype      MLA_BF16, MLA_FP16 or MLA_FP32.
+ *   latents    dtype [n][512], rows row_stride elements apart, each 16-byte
+ *              aligned (so the rows of a wider projection serve); finite values,
+ *              finite after the turn in fp32 too.
+ *   table      the rotary table, or NULL: nothing turns (positions is then
+ *              not read and may be NULL).
+ *   positions  int32 [n] (device); those of skipped rows are not used.
+ *   slots, pool, num_pages, d_error   as in mla_kv_write: -1 skips a row, other
+ *              slots outside the pool are skipped and flagged, only the
+ *              addressed records are written, two rows with the same slot race.
+ * Rows of 16 bits without a table give the bytes that mla_kv_write gives.
+ */
+mla_status_t mla_kv_append(int32_t kv_format, int32_t dtype, const void* latents, int64_t row_stride, int64_t n,
+                           const mla_rope_table_t* table, int32_t offset, const int32_t* positions,
+                           const int32_t* slots, void* pool, int64_t num_pages, int32_t* d_error, mla_stream_t stream);
+
+/*
+ * The means of full pages in 8 bits, by which mla_paged_sparse_decode_fp4 selects
+ * pages.  Tokens are appended in order, so a page is full when its last slot is
+ * written: every slot of the list that is the last one of its page (slot % 64 ==
+ * 63) has that page's mean computed from its 64 FP4 records; other entries do
+ * nothing.  So the slots of a step (mla_page_plan's) keep the means up to date,
+ * and a list of last slots makes those of a cache that was filled before.
+ * A mean is a record of MLA_MEAN_BYTES: 512 int8 codes, the byte 127 + e, 15
+ * zeros.  With the exact mean m and the least e that gives max |m_d| 2^-e <= 127
+ * (e = 0 for a mean of zeros), code d is m_d 2^-e rounded to nearest even: no
+ * other rounding.  A NaN scale in a record counts as 448.
+ *   pool     uint8 [num_pages][64][288] FP4 records, 16-byte aligned.
+ *   slots    int32 [n] (device); -1 = skip, others outside the pool are skipped
+ *            and flagged (MLA_DEVERR_BAD_INDEX).
+ *   means    uint8 [num_pages][MLA_MEAN_BYTES], 16-byte aligned; only those of
+ *            the pages named are written.
+ *   d_error  device int32 or NULL.
+ */
+#define MLA_MEAN_BYTES 528
+mla_status_t mla_page_means(const void* pool, int64_t num_pages, const int32_t* slots, int64_t n, void* means,
+                            int32_t* d_error, mla_stream_t stream);
+
+/*
  * Root-mean-square norm with the residual's addition, cast to FP8 blocks:
  *     s = x + residual        (fp32; residual may be NULL)
  *     residual_out = s        (rounded to dtype; may be residual itself, NULL to drop it)
