@@ -22,6 +22,7 @@ __all__ = [
     "DEVERR_BAD_INDEX", "DEVERR_TIMEOUT", "DEVERR_BAD_METADATA", "DEVERR_NO_ROOM", "DEVERR_BAD_LENGTH", "SCHED_INTS",
     "page_plan", "RopeScaling", "RopeTable", "rope", "kv_append", "page_means", "rms_norm_fp8",
     "PagedProblem", "paged_decode_plan", "paged_decode_fp4", "PagedFP4Decoder",
+    "PagedSparseProblem", "paged_sparse_plan", "paged_sparse_decode_fp4", "PagedSparseFP4Decoder",
 ]
 
 KV_NONE, KV_FP8_528, KV_FP4_288, KV_BF16 = 0, 1, 2, 3
@@ -92,6 +93,24 @@ class PagedProblem(ctypes.Structure):
                    sm_scale)
 
 
+class PagedSparseProblem(ctypes.Structure):
+    """mla_paged_sparse_problem_t (include/mla.h)."""
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("seq_len_q", ctypes.c_int32), ("h_q", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+        ("top_pages", ctypes.c_int32), ("sink_pages", ctypes.c_int32), ("local_pages", ctypes.c_int32),
+        ("num_pages", ctypes.c_int64), ("kv_format", ctypes.c_int32), ("sm_scale", ctypes.c_float),
+    ]
+
+    @classmethod
+    def make(cls, batch, seq_len_q, h_q, max_pages, num_pages, top_pages, sink_pages=1, local_pages=1, sm_scale=None,
+             head_dim=HEAD_DIM, page_size=PAGE_SIZE, kv_format=KV_FP4_288) -> "PagedSparseProblem":
+        if sm_scale is None:
+            sm_scale = 1.0 / math.sqrt(head_dim)
+        return cls(batch, seq_len_q, h_q, head_dim, page_size, max_pages, top_pages, sink_pages, local_pages, num_pages,
+                   kv_format, sm_scale)
+
+
 _lib = None
 
 
@@ -122,12 +141,14 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.mla_rms_norm_fp8.argtypes = [I32, P, I64, P, I64, P, F, P, I64, P, I64, P, I64, I64, I32, P, P]
     lib.mla_paged_decode_plan.argtypes = [P, I32, ctypes.POINTER(I32), ctypes.POINTER(SZ)]
     lib.mla_paged_decode_fp4.argtypes = [P, P, P, P, P, I32, P, SZ, P, P, P, P]
+    lib.mla_paged_sparse_plan.argtypes = [P, I32, ctypes.POINTER(I32), ctypes.POINTER(SZ)]
+    lib.mla_paged_sparse_decode_fp4.argtypes = [P, P, P, P, P, P, I32, P, SZ, P, P, P, P, P]
     lib.mla_status_string.argtypes = [ctypes.c_int]
     lib.mla_status_string.restype = ctypes.c_char_p
     for f in (lib.mla_get_metadata, lib.mla_sparse_decode, lib.mla_sparse_decode_rope_fp8, lib.mla_combine,
               lib.mla_dequantize, lib.mla_kv_write, lib.mla_page_plan, lib.mla_rope_table,
               lib.mla_rope_table_from_freqs, lib.mla_rope, lib.mla_kv_append, lib.mla_page_means, lib.mla_rms_norm_fp8, lib.mla_paged_decode_plan,
-              lib.mla_paged_decode_fp4):
+              lib.mla_paged_decode_fp4, lib.mla_paged_sparse_plan, lib.mla_paged_sparse_decode_fp4):
         f.restype = ctypes.c_int
     if path == _build.LIB:
         _lib = lib
@@ -578,3 +599,62 @@ class PagedFP4Decoder:
         paged_decode_fp4(self.problem, q, kv, block_table, seq_lens, self.num_parts, self.workspace, out, lse,
                          self.error, stream)
         return out, lse
+
+
+def paged_sparse_plan(problem: PagedSparseProblem, num_sms: int = 0):
+    """(num_parts, workspace_bytes) of a decode over selected pages (host only; num_sms = 0 asks the current device)."""
+    lib = load()
+    parts, ws = ctypes.c_int32(0), ctypes.c_size_t(0)
+    _check(lib.mla_paged_sparse_plan(ctypes.addressof(problem), num_sms, ctypes.byref(parts), ctypes.byref(ws)),
+           "mla_paged_sparse_plan")
+    return parts.value, ws.value
+
+
+def paged_sparse_decode_fp4(problem: PagedSparseProblem, q, kv, means, block_table, seq_lens, num_parts, workspace, out,
+                            lse, selected=None, error=None, stream=None) -> None:
+    """Attention of each sequence's last seq_len_q tokens over the pages that
+    the pages' means (uint8 [num_pages, 528], page_means) select for each of
+    them (mla_paged_sparse_decode_fp4).  selected: optional int32 [b, s,
+    top_pages], the pages taken, ascending, -1 after the last; the others as
+    in paged_decode_fp4, the workspace as paged_sparse_plan says."""
+    lib = load()
+    dev = _device_of(q, "paged_sparse_decode_fp4")
+    p = problem
+    rows = (p.batch, p.seq_len_q, p.h_q)
+    u8, i32 = torch.uint8, torch.int32
+    if kv.numel() != p.num_pages * PAGE_SIZE * FP4_RECORD_BYTES:
+        raise ValueError("kv: expected num_pages * 64 records of 288 bytes")
+    _call(lib.mla_paged_sparse_decode_fp4, "mla_paged_sparse_decode_fp4", dev, stream, ctypes.addressof(p),
+          _arg(q, dev, torch.bfloat16, "q", rows + (HEAD_DIM,)), _arg(kv, dev, u8, "kv"),
+          _arg(means, dev, u8, "means", (p.num_pages, MEAN_BYTES)),
+          _arg(block_table, dev, i32, "block_table", (p.batch, p.max_pages)),
+          _arg(seq_lens, dev, i32, "seq_lens", (p.batch,)), num_parts, _arg(workspace, dev, u8, "workspace"),
+          workspace.numel(), _arg(out, dev, torch.bfloat16, "out", q.shape), _arg(lse, dev, torch.float32, "lse", rows),
+          _arg(selected, dev, i32, "selected", (p.batch, p.seq_len_q, p.top_pages)), _arg(error, dev, i32, "error"))
+
+
+class PagedSparseFP4Decoder:
+    """Plan and workspace of a decode over selected pages, made once for a
+    problem shape.  The workspace serves one call at a time: concurrent
+    streams, and graphs that are replayed concurrently, take a decoder each."""
+
+    def __init__(self, problem: PagedSparseProblem, device=None, num_sms: int = 0):
+        self.problem = problem
+        self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        with torch.cuda.device(self.device):
+            self.num_parts, self.ws_bytes = paged_sparse_plan(problem, num_sms)
+        self.workspace = torch.empty((self.ws_bytes,), dtype=torch.uint8, device=self.device)
+        self.error = torch.zeros((1,), dtype=torch.int32, device=self.device)
+
+    def __call__(self, q, kv, means, block_table, seq_lens, out=None, lse=None, selected=None, stream=None):
+        """(out, lse, selected); memory for those not given comes from the call's stream."""
+        p = self.problem
+        if out is None or lse is None or selected is None:
+            with torch.cuda.stream(stream):
+                out = torch.empty_like(q) if out is None else out
+                lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device) if lse is None else lse
+                if selected is None:
+                    selected = torch.empty(q.shape[:2] + (p.top_pages,), dtype=torch.int32, device=q.device)
+        paged_sparse_decode_fp4(p, q, kv, means, block_table, seq_lens, self.num_parts, self.workspace, out, lse, selected,
+                                self.error, stream)
+        return out, lse, selected

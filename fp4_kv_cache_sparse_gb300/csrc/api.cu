@@ -129,6 +129,65 @@ mla_status_t validate_paged(const mla_paged_problem_t* p) {
   return MLA_OK;
 }
 
+PagedParams paged_params(const mla_paged_problem_t* problem, const PagedPlan& pl, const void* q, const void* kv,
+                         const int32_t* block_table, const int32_t* seq_lens, void* workspace, void* out, float* lse,
+                         int32_t* d_error) {
+  PagedParams p{};
+  p.q = static_cast<const uint16_t*>(q);
+  p.kv = static_cast<const uint8_t*>(kv);
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
+  p.ws_o = static_cast<float*>(workspace);
+  p.ws_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + pl.ws_o_bytes);
+  p.ws_info = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + pl.ws_o_bytes + pl.ws_lse_bytes);
+  p.d_error = d_error;
+  p.batch = problem->batch;
+  p.s = problem->seq_len_q;
+  p.h = problem->h_q;
+  p.rows = problem->seq_len_q * problem->h_q;
+  p.max_pages = problem->max_pages;
+  p.window = problem->window;
+  p.sinks = problem->sinks;
+  p.num_pages = problem->num_pages;
+  p.scale_log2 = problem->sm_scale * kLog2e;
+  return p;
+}
+
+// The decode over selected pages: every query token a sequence of one token over a table of its own.
+mla_status_t validate_paged_sparse(const mla_paged_sparse_problem_t* p, mla_paged_problem_t* one) {
+  if (p == nullptr) return MLA_ERR_INVALID_ARG;
+  if (p->batch < 1 || p->seq_len_q < 1 || p->max_pages < 1 || p->top_pages < 1 || p->sink_pages < 0 ||
+      p->local_pages < 1 || static_cast<int64_t>(p->sink_pages) + p->local_pages > p->top_pages)
+    return MLA_ERR_INVALID_ARG;
+  mla_paged_problem_t whole{p->batch,   p->seq_len_q, p->h_q,       p->head_dim,  p->page_size, p->max_pages, 0,
+                            0,          p->num_pages, p->kv_format, p->sm_scale};
+  mla_status_t st = validate_paged(&whole);
+  if (st != MLA_OK) return st;
+  const int64_t most = int64_t(1) << 31, queries = static_cast<int64_t>(p->batch) * p->seq_len_q;
+  if (queries >= most || queries * ((static_cast<int64_t>(p->max_pages) + 15) / 16) >= most) return MLA_ERR_UNSUPPORTED;
+  *one = whole;
+  one->batch = static_cast<int32_t>(queries);
+  one->seq_len_q = 1;
+  one->max_pages = p->top_pages;
+  return validate_paged(one);
+}
+
+struct SparseWorkspace {
+  size_t scores, table, lens, bytes;  // offsets behind the decode's own workspace
+};
+SparseWorkspace sparse_workspace(const mla_paged_sparse_problem_t* p, const PagedPlan& pl) {
+  const auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
+  const size_t queries = static_cast<size_t>(p->batch) * p->seq_len_q;
+  SparseWorkspace w;
+  w.scores = up(pl.ws_bytes);
+  w.table = w.scores + up(queries * p->max_pages * sizeof(float));
+  w.lens = w.table + up(queries * p->top_pages * sizeof(int32_t));
+  w.bytes = w.lens + up(queries * sizeof(int32_t));
+  return w;
+}
+
 bool rope_table_ok(const mla_rope_table_t& t) {
   return t.rope_dim >= 2 && t.rope_dim <= MLA_ROPE_MAX_DIM && (t.rope_dim & 1) == 0 &&
          (t.layout == MLA_ROPE_INTERLEAVED || t.layout == MLA_ROPE_HALF) && std::isfinite(t.factor);
@@ -602,27 +661,69 @@ mla_status_t mla_paged_decode_fp4(const mla_paged_problem_t* problem, const void
   const PagedPlan pl = paged_plan(problem, num_parts);
   if (workspace == nullptr || workspace_bytes < pl.ws_bytes) return MLA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return MLA_ERR_INVALID_ARG;
-  PagedParams p{};
-  p.q = static_cast<const uint16_t*>(q);
-  p.kv = static_cast<const uint8_t*>(kv);
-  p.block_table = block_table;
-  p.seq_lens = seq_lens;
-  p.out = static_cast<uint16_t*>(out);
-  p.lse = lse;
-  p.ws_o = static_cast<float*>(workspace);
-  p.ws_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + pl.ws_o_bytes);
-  p.ws_info = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + pl.ws_o_bytes + pl.ws_lse_bytes);
-  p.d_error = d_error;
-  p.batch = problem->batch;
-  p.s = problem->seq_len_q;
-  p.h = problem->h_q;
-  p.rows = problem->seq_len_q * problem->h_q;
-  p.max_pages = problem->max_pages;
-  p.window = problem->window;
-  p.sinks = problem->sinks;
-  p.num_pages = problem->num_pages;
-  p.scale_log2 = problem->sm_scale * kLog2e;
+  const PagedParams p = paged_params(problem, pl, q, kv, block_table, seq_lens, workspace, out, lse, d_error);
   if (launch_paged_decode(p, pl, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return cuda_failed();
+  return MLA_OK;
+}
+
+mla_status_t mla_paged_sparse_plan(const mla_paged_sparse_problem_t* problem, int32_t num_sms, int32_t* num_parts_out,
+                                   size_t* workspace_bytes_out) {
+  mla_paged_problem_t one;
+  mla_status_t st = validate_paged_sparse(problem, &one);
+  if (st != MLA_OK) return st;
+  if (num_parts_out == nullptr || workspace_bytes_out == nullptr || num_sms < 0 || num_sms > (1 << 16))
+    return MLA_ERR_INVALID_ARG;
+  if (num_sms == 0) {
+    st = device_sm_count(&num_sms);
+    if (st != MLA_OK) return st;
+  }
+  *num_parts_out = num_sms;
+  *workspace_bytes_out = sparse_workspace(problem, paged_plan(&one, num_sms)).bytes;
+  return MLA_OK;
+}
+
+mla_status_t mla_paged_sparse_decode_fp4(const mla_paged_sparse_problem_t* problem, const void* q, const void* kv,
+                                         const void* means, const int32_t* block_table, const int32_t* seq_lens,
+                                         int32_t num_parts, void* workspace, size_t workspace_bytes, void* out,
+                                         float* lse, int32_t* selected, int32_t* d_error, mla_stream_t stream) {
+  mla_paged_problem_t one;
+  const mla_status_t st = validate_paged_sparse(problem, &one);
+  if (st != MLA_OK) return st;
+  if (q == nullptr || kv == nullptr || means == nullptr || block_table == nullptr || seq_lens == nullptr ||
+      out == nullptr || lse == nullptr)
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(kv) || !aligned16(means) || !aligned16(out) || !aligned_to(block_table, 4) ||
+      !aligned_to(seq_lens, 4) || !aligned_to(lse, 4) || !aligned_to(selected, 4))
+    return MLA_ERR_INVALID_ARG;
+  if (num_parts < 1 || num_parts > (1 << 16)) return MLA_ERR_INVALID_ARG;
+  const PagedPlan pl = paged_plan(&one, num_parts);
+  const SparseWorkspace ws = sparse_workspace(problem, pl);
+  if (workspace == nullptr || workspace_bytes < ws.bytes) return MLA_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return MLA_ERR_INVALID_ARG;
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  SelectParams sp{};
+  sp.q = static_cast<const uint16_t*>(q);
+  sp.means = static_cast<const uint8_t*>(means);
+  sp.block_table = block_table;
+  sp.seq_lens = seq_lens;
+  sp.scores = reinterpret_cast<float*>(base + ws.scores);
+  sp.sel_table = reinterpret_cast<int32_t*>(base + ws.table);
+  sp.sel_lens = reinterpret_cast<int32_t*>(base + ws.lens);
+  sp.selected = selected;
+  sp.d_error = d_error;
+  sp.batch = problem->batch;
+  sp.s = problem->seq_len_q;
+  sp.h = problem->h_q;
+  sp.max_pages = problem->max_pages;
+  sp.top = problem->top_pages;
+  sp.sinks = problem->sink_pages;
+  sp.local = problem->local_pages;
+  sp.num_pages = problem->num_pages;
+  sp.sign = problem->sm_scale < 0.f ? -1.f : 1.f;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (launch_page_select(sp, s) != cudaSuccess) return cuda_failed();
+  const PagedParams p = paged_params(&one, pl, q, kv, sp.sel_table, sp.sel_lens, base, out, lse, d_error);
+  if (launch_paged_decode(p, pl, s) != cudaSuccess) return cuda_failed();
   return MLA_OK;
 }
 

@@ -170,6 +170,24 @@ struct PagedPlan {
 PagedPlan paged_plan(const mla_paged_problem_t* p, int num_parts);
 cudaError_t launch_paged_decode(const PagedParams& p, const PagedPlan& plan, cudaStream_t stream);
 
+// Which pages each query token attends to: scores of the pages' means, and the
+// best of them as block tables and lengths of one-token sequences.
+struct SelectParams {
+  const uint16_t* q;           // bf16 [batch * s * h][512]
+  const uint8_t* means;        // [num_pages][MLA_MEAN_BYTES]
+  const int32_t* block_table;  // [batch][max_pages]
+  const int32_t* seq_lens;     // [batch]
+  float* scores;               // [batch * s][max_pages]
+  int32_t* sel_table;          // [batch * s][top]: page ids
+  int32_t* sel_lens;           // [batch * s]
+  int32_t* selected;           // [batch * s][top]: pages of the sequence, nullable
+  int32_t* d_error;            // nullable
+  int batch, s, h, max_pages, top, sinks, local;
+  int64_t num_pages;
+  float sign;                  // that of the softmax scale
+};
+cudaError_t launch_page_select(const SelectParams& p, cudaStream_t stream);
+
 // cuTensorMapEncodeTiled from the driver, looked up once (thread-safe
 // static initialization); nullptr if the driver does not offer it.
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,

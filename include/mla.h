@@ -506,6 +506,58 @@ mla_status_t mla_paged_decode_fp4(const mla_paged_problem_t* problem, const void
                                   void* workspace, size_t workspace_bytes, void* out, float* lse, int32_t* d_error,
                                   mla_stream_t stream);
 
+/*
+ * Attention of each query token over a few pages of its sequence, which a cheap
+ * score of the pages' means selects: long contexts at the cost of top_pages.
+ */
+typedef struct {
+  int32_t batch;        /* b >= 1 */
+  int32_t seq_len_q;    /* s >= 1: the last s tokens of each sequence are the query tokens */
+  int32_t h_q;          /* query heads, 1 .. 128 */
+  int32_t head_dim;     /* must be 512 */
+  int32_t page_size;    /* must be 64 */
+  int32_t max_pages;    /* entries of a block table row */
+  int32_t top_pages;    /* pages a query token attends to at most, >= 1 */
+  int32_t sink_pages;   /* the first pages, always among them, >= 0 */
+  int32_t local_pages;  /* the query token's own page and those before it, always among them, >= 1 */
+  int64_t num_pages;    /* pages in the pool (bounds check of the block table) */
+  int32_t kv_format;    /* must be MLA_KV_FP4_288 */
+  float sm_scale;       /* as in mla_paged_problem_t */
+} mla_paged_sparse_problem_t; /* sink_pages + local_pages <= top_pages */
+
+/* Host-only planning, as mla_paged_decode_plan.  The workspace holds a float for each (query token, table entry). */
+mla_status_t mla_paged_sparse_plan(const mla_paged_sparse_problem_t* problem, int32_t num_sms, int32_t* num_parts_out,
+                                   size_t* workspace_bytes_out);
+
+/*
+ * One attention step.  Query token i of sequence b stands at position
+ * p = seq_lens[b] - s + i, in page c = p / 64.  It attends to the tokens j <= p
+ * of the selected pages: all of 0 .. c if they are at most top_pages, otherwise
+ *   0 .. sink_pages - 1,  c - local_pages + 1 .. c,  and of the pages between
+ *   them (all full) those with the highest scores, top_pages in all; equal
+ *   scores go to the lower page.
+ * A page's score is the largest of its heads' <q_h, mean of the page> (smallest
+ * for a negative sm_scale), from 8-bit codes of both: with e_h the least exponent
+ * (at least -120) that gives max |q_hd| 2^-e_h <= 127, a_hd = q_hd 2^-e_h rounded
+ * to nearest even and a mean's codes c_d and exponent e (mla_page_means),
+ *     score = max_h  2^max(e_h - max_g e_g, -100) * sum_d a_hd c_d  * 2^e,
+ * g over the rows that are not all 0.  That is exact in fp32, so the selection
+ * does not depend on the order of any sum.
+ *   q, kv, block_table, seq_lens, out, lse   as in mla_paged_decode_fp4, as are
+ *                rows that see nothing and what is flagged.  A page id outside the
+ *                pool scores minus infinity; its tokens are skipped.
+ *   means        uint8 [num_pages][MLA_MEAN_BYTES], 16-byte aligned; read for
+ *                the full pages of the block tables that are scored.
+ *   selected     int32 [batch][s][top_pages] or NULL, written: the pages of the
+ *                sequence each query token attends to, ascending, -1 after the last.
+ *   num_parts, workspace, workspace_bytes   as mla_paged_sparse_plan says,
+ *                16-byte aligned; calls that share a workspace must not overlap.
+ */
+mla_status_t mla_paged_sparse_decode_fp4(const mla_paged_sparse_problem_t* problem, const void* q, const void* kv,
+                                         const void* means, const int32_t* block_table, const int32_t* seq_lens,
+                                         int32_t num_parts, void* workspace, size_t workspace_bytes, void* out,
+                                         float* lse, int32_t* selected, int32_t* d_error, mla_stream_t stream);
+
 /* Static description of a status code. */
 const char* mla_status_string(mla_status_t status);
 
