@@ -23,6 +23,7 @@ __all__ = [
     "page_plan", "RopeScaling", "RopeTable", "rope", "kv_append", "page_means", "rms_norm_fp8",
     "PagedProblem", "paged_decode_plan", "paged_decode_fp4", "PagedFP4Decoder",
     "PagedSparseProblem", "paged_sparse_plan", "paged_sparse_decode_fp4", "PagedSparseFP4Decoder",
+    "PagedSharedProblem", "paged_shared_plan", "paged_shared_decode_fp4", "PagedSharedFP4Decoder",
 ]
 
 KV_NONE, KV_FP8_528, KV_FP4_288, KV_BF16 = 0, 1, 2, 3
@@ -111,6 +112,24 @@ class PagedSparseProblem(ctypes.Structure):
                    kv_format, sm_scale)
 
 
+class PagedSharedProblem(ctypes.Structure):
+    """mla_paged_shared_problem_t (include/mla.h)."""
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("seq_len_q", ctypes.c_int32), ("h_q", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32), ("groups", ctypes.c_int32),
+        ("max_prefix_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("num_pages", ctypes.c_int64),
+        ("kv_format", ctypes.c_int32), ("sm_scale", ctypes.c_float),
+    ]
+
+    @classmethod
+    def make(cls, batch, seq_len_q, h_q, max_pages, max_prefix_pages, num_pages, groups=1, sm_scale=None,
+             head_dim=HEAD_DIM, page_size=PAGE_SIZE, kv_format=KV_FP4_288) -> "PagedSharedProblem":
+        if sm_scale is None:
+            sm_scale = 1.0 / math.sqrt(head_dim)
+        return cls(batch, seq_len_q, h_q, head_dim, page_size, groups, max_prefix_pages, max_pages, num_pages, kv_format,
+                   sm_scale)
+
+
 _lib = None
 
 
@@ -143,12 +162,15 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.mla_paged_decode_fp4.argtypes = [P, P, P, P, P, I32, P, SZ, P, P, P, P]
     lib.mla_paged_sparse_plan.argtypes = [P, I32, ctypes.POINTER(I32), ctypes.POINTER(SZ)]
     lib.mla_paged_sparse_decode_fp4.argtypes = [P, P, P, P, P, P, I32, P, SZ, P, P, P, P, P]
+    lib.mla_paged_shared_plan.argtypes = [P, I32, ctypes.POINTER(I32), ctypes.POINTER(SZ)]
+    lib.mla_paged_shared_decode_fp4.argtypes = [P, P, P, P, P, P, P, P, I32, P, SZ, P, P, P, P]
     lib.mla_status_string.argtypes = [ctypes.c_int]
     lib.mla_status_string.restype = ctypes.c_char_p
     for f in (lib.mla_get_metadata, lib.mla_sparse_decode, lib.mla_sparse_decode_rope_fp8, lib.mla_combine,
               lib.mla_dequantize, lib.mla_kv_write, lib.mla_page_plan, lib.mla_rope_table,
               lib.mla_rope_table_from_freqs, lib.mla_rope, lib.mla_kv_append, lib.mla_page_means, lib.mla_rms_norm_fp8, lib.mla_paged_decode_plan,
-              lib.mla_paged_decode_fp4, lib.mla_paged_sparse_plan, lib.mla_paged_sparse_decode_fp4):
+              lib.mla_paged_decode_fp4, lib.mla_paged_sparse_plan, lib.mla_paged_sparse_decode_fp4,
+              lib.mla_paged_shared_plan, lib.mla_paged_shared_decode_fp4):
         f.restype = ctypes.c_int
     if path == _build.LIB:
         _lib = lib
@@ -658,3 +680,62 @@ class PagedSparseFP4Decoder:
         paged_sparse_decode_fp4(p, q, kv, means, block_table, seq_lens, self.num_parts, self.workspace, out, lse, selected,
                                 self.error, stream)
         return out, lse, selected
+
+
+def paged_shared_plan(problem: PagedSharedProblem, num_sms: int = 0):
+    """(num_parts, workspace_bytes) of a decode with shared prefixes (host only; num_sms = 0 asks the current device)."""
+    lib = load()
+    parts, ws = ctypes.c_int32(0), ctypes.c_size_t(0)
+    _check(lib.mla_paged_shared_plan(ctypes.addressof(problem), num_sms, ctypes.byref(parts), ctypes.byref(ws)),
+           "mla_paged_shared_plan")
+    return parts.value, ws.value
+
+
+def paged_shared_decode_fp4(problem: PagedSharedProblem, q, kv, group_start, prefix_table, prefix_lens, block_table,
+                            seq_lens, num_parts, workspace, out, lse, error=None, stream=None) -> None:
+    """Attention of each sequence's last seq_len_q tokens over its group's
+    prefix and its own pages (mla_paged_shared_decode_fp4).  All int32:
+    group_start [groups + 1], prefix_table [groups, max_prefix_pages],
+    prefix_lens [groups], block_table [b, max_pages] and seq_lens [b] of the
+    sequences' own tokens; the others as in paged_decode_fp4, the workspace as
+    paged_shared_plan says."""
+    lib = load()
+    dev = _device_of(q, "paged_shared_decode_fp4")
+    p = problem
+    rows = (p.batch, p.seq_len_q, p.h_q)
+    i32 = torch.int32
+    if kv.numel() != p.num_pages * PAGE_SIZE * FP4_RECORD_BYTES:
+        raise ValueError("kv: expected num_pages * 64 records of 288 bytes")
+    _call(lib.mla_paged_shared_decode_fp4, "mla_paged_shared_decode_fp4", dev, stream, ctypes.addressof(p),
+          _arg(q, dev, torch.bfloat16, "q", rows + (HEAD_DIM,)), _arg(kv, dev, torch.uint8, "kv"),
+          _arg(group_start, dev, i32, "group_start", (p.groups + 1,)),
+          _arg(prefix_table, dev, i32, "prefix_table", (p.groups, p.max_prefix_pages)),
+          _arg(prefix_lens, dev, i32, "prefix_lens", (p.groups,)),
+          _arg(block_table, dev, i32, "block_table", (p.batch, p.max_pages)),
+          _arg(seq_lens, dev, i32, "seq_lens", (p.batch,)), num_parts, _arg(workspace, dev, torch.uint8, "workspace"),
+          workspace.numel(), _arg(out, dev, torch.bfloat16, "out", q.shape), _arg(lse, dev, torch.float32, "lse", rows),
+          _arg(error, dev, i32, "error"))
+
+
+class PagedSharedFP4Decoder:
+    """Plan and workspace of a decode with shared prefixes, made once for a
+    problem shape.  The workspace serves one call at a time: concurrent
+    streams, and graphs that are replayed concurrently, take a decoder each."""
+
+    def __init__(self, problem: PagedSharedProblem, device=None, num_sms: int = 0):
+        self.problem = problem
+        self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        with torch.cuda.device(self.device):
+            self.num_parts, self.ws_bytes = paged_shared_plan(problem, num_sms)
+        self.workspace = torch.empty((self.ws_bytes,), dtype=torch.uint8, device=self.device)
+        self.error = torch.zeros((1,), dtype=torch.int32, device=self.device)
+
+    def __call__(self, q, kv, group_start, prefix_table, prefix_lens, block_table, seq_lens, out=None, lse=None,
+                 stream=None):
+        if out is None or lse is None:
+            with torch.cuda.stream(stream):  # memory of the stream that writes it
+                out = torch.empty_like(q) if out is None else out
+                lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device) if lse is None else lse
+        paged_shared_decode_fp4(self.problem, q, kv, group_start, prefix_table, prefix_lens, block_table, seq_lens,
+                                self.num_parts, self.workspace, out, lse, self.error, stream)
+        return out, lse

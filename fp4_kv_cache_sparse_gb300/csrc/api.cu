@@ -188,6 +188,26 @@ SparseWorkspace sparse_workspace(const mla_paged_sparse_problem_t* p, const Page
   return w;
 }
 
+// The sequences' own tokens as a paged problem, and the prefixes' share of the counts.
+mla_status_t validate_paged_shared(const mla_paged_shared_problem_t* p, mla_paged_problem_t* own) {
+  if (p == nullptr) return MLA_ERR_INVALID_ARG;
+  if (p->groups < 1 || p->max_prefix_pages < 1) return MLA_ERR_INVALID_ARG;
+  *own = mla_paged_problem_t{p->batch, p->seq_len_q, p->h_q,       p->head_dim,  p->page_size, p->max_pages, 0,
+                             0,        p->num_pages, p->kv_format, p->sm_scale};
+  const mla_status_t st = validate_paged(own);
+  if (st != MLA_OK) return st;
+  if (p->groups > MLA_MAX_PREFIX_GROUPS) return MLA_ERR_UNSUPPORTED;
+  const int64_t most = int64_t(1) << 31, rows = static_cast<int64_t>(p->seq_len_q) * p->h_q;
+  if (static_cast<int64_t>(p->max_prefix_pages) * MLA_PAGE_SIZE >= most - 256 ||
+      static_cast<int64_t>(p->groups) * p->max_prefix_pages >= most)
+    return MLA_ERR_UNSUPPORTED;
+  // Tiles of all units and their own cost, rounded up to whole parts.
+  const int64_t own_units = p->batch * ((rows + 15) / 16), prefix_units = p->batch * rows / 16 + p->groups;
+  const double cost = static_cast<double>(own_units) * ((p->max_pages + 1) / 2 + 4) +
+                      static_cast<double>(prefix_units) * ((p->max_prefix_pages + 1) / 2 + 4);
+  return cost >= static_cast<double>(most - (1 << 16)) ? MLA_ERR_UNSUPPORTED : MLA_OK;
+}
+
 bool rope_table_ok(const mla_rope_table_t& t) {
   return t.rope_dim >= 2 && t.rope_dim <= MLA_ROPE_MAX_DIM && (t.rope_dim & 1) == 0 &&
          (t.layout == MLA_ROPE_INTERLEAVED || t.layout == MLA_ROPE_HALF) && std::isfinite(t.factor);
@@ -724,6 +744,53 @@ mla_status_t mla_paged_sparse_decode_fp4(const mla_paged_sparse_problem_t* probl
   if (launch_page_select(sp, s) != cudaSuccess) return cuda_failed();
   const PagedParams p = paged_params(&one, pl, q, kv, sp.sel_table, sp.sel_lens, base, out, lse, d_error);
   if (launch_paged_decode(p, pl, s) != cudaSuccess) return cuda_failed();
+  return MLA_OK;
+}
+
+mla_status_t mla_paged_shared_plan(const mla_paged_shared_problem_t* problem, int32_t num_sms, int32_t* num_parts_out,
+                                   size_t* workspace_bytes_out) {
+  mla_paged_problem_t own;
+  mla_status_t st = validate_paged_shared(problem, &own);
+  if (st != MLA_OK) return st;
+  if (num_parts_out == nullptr || workspace_bytes_out == nullptr || num_sms < 0 || num_sms > (1 << 16))
+    return MLA_ERR_INVALID_ARG;
+  if (num_sms == 0) {
+    st = device_sm_count(&num_sms);
+    if (st != MLA_OK) return st;
+  }
+  const PagedPlan pl = shared_plan(problem, num_sms);
+  *num_parts_out = pl.num_parts;
+  *workspace_bytes_out = pl.ws_bytes;
+  return MLA_OK;
+}
+
+mla_status_t mla_paged_shared_decode_fp4(const mla_paged_shared_problem_t* problem, const void* q, const void* kv,
+                                         const int32_t* group_start, const int32_t* prefix_table,
+                                         const int32_t* prefix_lens, const int32_t* block_table,
+                                         const int32_t* seq_lens, int32_t num_parts, void* workspace,
+                                         size_t workspace_bytes, void* out, float* lse, int32_t* d_error,
+                                         mla_stream_t stream) {
+  mla_paged_problem_t own;
+  const mla_status_t st = validate_paged_shared(problem, &own);
+  if (st != MLA_OK) return st;
+  for (const void* a : {q, kv, static_cast<const void*>(out)})
+    if (a == nullptr || !aligned16(a)) return MLA_ERR_INVALID_ARG;
+  for (const void* a : {static_cast<const void*>(group_start), static_cast<const void*>(prefix_table),
+                        static_cast<const void*>(prefix_lens), static_cast<const void*>(block_table),
+                        static_cast<const void*>(seq_lens), static_cast<const void*>(lse)})
+    if (a == nullptr || !aligned_to(a, 4)) return MLA_ERR_INVALID_ARG;
+  if (num_parts < 1 || num_parts > (1 << 16)) return MLA_ERR_INVALID_ARG;
+  const PagedPlan pl = shared_plan(problem, num_parts);
+  if (workspace == nullptr || workspace_bytes < pl.ws_bytes) return MLA_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return MLA_ERR_INVALID_ARG;
+  SharedParams p{paged_params(&own, pl, q, kv, block_table, seq_lens, workspace, out, lse, d_error)};
+  p.group_start = group_start;
+  p.prefix_table = prefix_table;
+  p.prefix_lens = prefix_lens;
+  p.num_groups = problem->groups;
+  p.max_prefix_pages = problem->max_prefix_pages;
+  p.units = pl.units;
+  if (launch_shared_decode(p, pl, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return cuda_failed();
   return MLA_OK;
 }
 

@@ -165,10 +165,27 @@ struct PagedPlan {
   int nr;          // query rows a CTA works on: 16, 32 or 64
   int groups;      // row groups of a sequence
   int num_parts;
+  int units;       // shared prefixes: numbers of units
   size_t ws_o_bytes, ws_lse_bytes, ws_bytes;
 };
 PagedPlan paged_plan(const mla_paged_problem_t* p, int num_parts);
 cudaError_t launch_paged_decode(const PagedParams& p, const PagedPlan& plan, cudaStream_t stream);
+
+// The same for sequences in groups that share a prefix: partials of all units,
+// then their merge, which writes the outputs.
+struct SharedParams : PagedParams {
+  // Units 0 .. batch * groups - 1 are those of the sequences'
+  // own tokens; those of group g's rows over its prefix begin at batch * groups +
+  // floor(group_start[g] * rows / nr) + g.  ws_info has an entry for each unit
+  // and, behind them, the number of groups that count (0: they were not in order).
+  const int32_t* group_start;  // [num_groups + 1]
+  const int32_t* prefix_table; // [num_groups][max_prefix_pages]
+  const int32_t* prefix_lens;  // [num_groups]
+  int num_groups, max_prefix_pages, units;
+};
+PagedPlan shared_plan(const mla_paged_shared_problem_t* p, int num_parts);
+cudaError_t launch_shared_decode(const SharedParams& p, const PagedPlan& plan, cudaStream_t stream);
+cudaError_t launch_shared_merge(const SharedParams& p, const PagedPlan& plan, cudaStream_t stream);
 
 // Which pages each query token attends to: scores of the pages' means, and the
 // best of them as block tables and lengths of one-token sequences.

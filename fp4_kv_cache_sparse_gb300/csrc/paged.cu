@@ -67,6 +67,7 @@
 // of 2^10): 11 bits down to 2^-19 of the largest weight, where bf16 has 8, and
 // weights down to 2^-29 of it still count.  Sums, maxima and O are fp32.
 #include <cstdint>
+#include <type_traits>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -196,8 +197,44 @@ __device__ __forceinline__ int window_start(const PagedParams& p, int at) {
   return p.window > 0 && from > 0 ? static_cast<int>(from) : 0;
 }
 
+template <bool kShared>
+using Params = std::conditional_t<kShared, SharedParams, PagedParams>;
+
+// The first prefix unit of group g, counted from the first of all (mla_internal.h).
+__device__ __forceinline__ int prefix_unit(const SharedParams& p, int nr, int g) {
+  return load_i32(p.group_start + g) * p.rows / nr + g;
+}
+
+// A block of rows of a group of sequences over their prefix: b is -1 - g, row0
+// counts from the batch's first row, every row sees every token.  Numbers that
+// fall between two groups, and groups without a prefix, have no tiles.
 template <int NR>
-__device__ __forceinline__ Unit unit_of(const PagedParams& p, int groups, int u, bool& bad) {
+__device__ __forceinline__ Unit prefix_unit_of(const SharedParams& p, int v, int num_groups, bool& bad) {
+  Unit t{};
+  bad = false;
+  if (num_groups == 0) return t;
+  int g = 0;  // the last group whose units begin at or before v
+  for (int n = num_groups; n > 1;) {
+    const int half = n / 2;
+    if (prefix_unit(p, NR, g + half) <= v) g += half;
+    n -= half;
+  }
+  const int from = load_i32(p.group_start + g) * p.rows, to = load_i32(p.group_start + g + 1) * p.rows;
+  const int len = load_i32(p.prefix_lens + g), k = v - prefix_unit(p, NR, g);
+  bad = len < 0 || len > p.max_prefix_pages * kPage;
+  t.b = -1 - g;
+  t.row0 = from + k * NR;
+  t.nrows = min(NR, to - t.row0);
+  t.first = t.p_lo = t.p_hi = len - 1;
+  t.tiles = bad || k < 0 || t.nrows <= 0 ? 0 : (len + kTile - 1) / kTile;
+  return t;
+}
+
+template <int NR, bool kShared>
+__device__ __forceinline__ Unit unit_of(const Params<kShared>& p, int groups, int u, bool& bad, int num_groups) {
+  if constexpr (kShared) {
+    if (u >= p.batch * groups) return prefix_unit_of<NR>(p, u - p.batch * groups, num_groups, bad);
+  }
   Unit t;
   t.b = u / groups;
   t.row0 = (u - t.b * groups) * NR;
@@ -426,9 +463,13 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 
 // ------------------------------------------------------------------ the kernel
 
-template <int NR>
+// kShared: sequences in groups that share a prefix (mla_paged_shared_decode_fp4).
+// After the units of the sequences' own tokens come those of the prefixes, NR
+// rows of a group at a time whichever sequences they belong to; every unit
+// leaves partials, which launch_shared_merge joins.
+template <int NR, bool kShared>
 __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
-    paged_decode_kernel(const PagedParams p, const int groups, const __grid_constant__ CUtensorMap q_map,
+    paged_decode_kernel(const Params<kShared> p, const int groups, const __grid_constant__ CUtensorMap q_map,
                         const __grid_constant__ CUtensorMap data_map, const __grid_constant__ CUtensorMap scale_map) {
   using L = PSmem<NR>;
   constexpr int NC = NR / L::kSides;    // rows of a softmax thread
@@ -484,24 +525,46 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
   // (That kernel may write the lengths and tables, hence load_i32.)
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
+  int num_groups = 0;
+  if constexpr (kShared) {
+    // Groups that are not in order count as none.
+    bool wrong = false;
+    for (int g = tid; g <= p.num_groups; g += kPagedThreads) {
+      const int at = load_i32(p.group_start + g);
+      wrong = wrong || at < 0 || at > p.batch || (g > 0 && at < load_i32(p.group_start + g - 1));
+    }
+    const bool none = __syncthreads_or(wrong);
+    num_groups = none ? 0 : p.num_groups;
+    if (part == 0 && tid == 0) {
+      p.ws_info[p.units * 4] = num_groups;
+      if (none && p.d_error) atomicOr(p.d_error, MLA_DEVERR_BAD_METADATA);
+    }
+  }
+
   // A unit's Q arrives by TMA as bf16, K-major with 128-byte swizzle ...
   const auto request_q = [&](int u) {
-    const int b = u / groups, y = b * p.rows + (u - b * groups) * NR;
+    int b = u / groups, y = b * p.rows + (u - b * groups) * NR;
+    if constexpr (kShared) {
+      bool bad;
+      if (u >= p.batch * groups) y = prefix_unit_of<NR>(p, u - p.batch * groups, num_groups, bad).row0;
+    }
     expect_tx(&bars[L::bQRaw], L::kQBytes);
 #pragma unroll 1
     for (int c = 0; c < 8; ++c) tma_load_2d(sQ + c * (NR * 128), &q_map, c * 64, y, &bars[L::bQRaw]);
   };
 
   // The cut: items of all units, this part's run, and the unit it begins in.
-  const int units = p.batch * groups;
+  int units = p.batch * groups;
+  if constexpr (kShared) units = p.units;
   const int per = (units + kPagedThreads - 1) / kPagedThreads;
   const int u_a = min(units, tid * per), u_b = min(units, u_a + per);
+  const auto cost_of = [](const Unit& t) { return kShared && t.tiles == 0 ? 0 : t.tiles + kUnitCost; };
   int mine = 0, most = 0;
   Unit unit{};  // this thread's last, which is its only one unless units are very many
   for (int u = u_a; u < u_b; ++u) {
     bool bad;
-    unit = unit_of<NR>(p, groups, u, bad);
-    const int cost = unit.tiles + kUnitCost;
+    unit = unit_of<NR, kShared>(p, groups, u, bad, num_groups);
+    const int cost = cost_of(unit);
     mine += cost;
     most = max(most, cost);
     if (bad && part == 0 && p.d_error) atomicOr(p.d_error, MLA_DEVERR_BAD_LENGTH);
@@ -536,10 +599,10 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
     if (whole ? u_a <= part && part < u_b : g0 < g1 && excl <= g0 && g0 < excl + mine) {
       int at = excl, u = whole ? part : u_a;
       bool bad;
-      if (per > 1) unit = unit_of<NR>(p, groups, u, bad);
-      while (!whole && at + kUnitCost + unit.tiles <= g0) {
-        at += kUnitCost + unit.tiles;
-        unit = unit_of<NR>(p, groups, ++u, bad);
+      if (per > 1) unit = unit_of<NR, kShared>(p, groups, u, bad, num_groups);
+      while (!whole && at + cost_of(unit) <= g0) {
+        at += cost_of(unit);
+        unit = unit_of<NR, kShared>(p, groups, ++u, bad, num_groups);
       }
       const int k = whole ? 0 : max(g0 - at - kUnitCost, 0);
       int count = unit.tiles;
@@ -550,8 +613,8 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
       if (!whole) {
         int tiles = unit.tiles, next = u;
         count = max(min(at + kUnitCost + tiles, g1) - (at + kUnitCost + k), 0);
-        for (at += kUnitCost + tiles; at + kUnitCost < g1; at += kUnitCost + tiles) {
-          tiles = unit_of<NR>(p, groups, ++next, bad).tiles;
+        for (at += kUnitCost + tiles; at + kUnitCost < g1; at += kShared && tiles == 0 ? 0 : kUnitCost + tiles) {
+          tiles = unit_of<NR, kShared>(p, groups, ++next, bad, num_groups).tiles;
           count += min(at + kUnitCost + tiles, g1) - (at + kUnitCost);
         }
       }
@@ -564,7 +627,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
   const uint32_t items = static_cast<uint32_t>(cut[2]);
 
   if (items == 0) {
-    if (tid == 0 && !p.info_by_unit) p.ws_info[part * 4] = -1;
+    if (tid == 0 && !(kShared || p.info_by_unit)) p.ws_info[part * 4] = -1;
   } else {
 
     if (warp == kLoadWarp) {
@@ -589,7 +652,11 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
           const int pos = tile * kTile + lane * kPage;
           const bool seen = pos < end && (pos + kPage > unit.start || pos < p.sinks);
           if (seen) {
-            const int page = load_i32(p.block_table + static_cast<int64_t>(unit.b) * p.max_pages + tile * 2 + lane);
+            const int32_t* row = p.block_table + static_cast<int64_t>(unit.b) * p.max_pages;
+            if constexpr (kShared) {
+              if (unit.b < 0) row = p.prefix_table + static_cast<int64_t>(-1 - unit.b) * p.max_prefix_pages;
+            }
+            const int page = load_i32(row + tile * 2 + lane);
             if (page >= 0 && page < p.num_pages) {
               tokens = min(kPage, end - pos);
               first_row = page * kPage;
@@ -610,11 +677,21 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
         // A piece begins with its unit unless the run's first item lies inside the unit.
         if (!(mid && u == u_first)) word |= kFromStart;
         if (k + 1 == unit.tiles) word |= kToEnd;
+        int next_u = u + 1;
+        Unit next_unit;
+        if constexpr (kShared) {
+          // The next unit that has tiles (there is one, as items are left).
+          if (k + 1 == unit.tiles && n + 1 < items) {
+            next_unit = unit_of<NR, true>(p, groups, next_u, bad_len, num_groups);
+            while (next_unit.tiles == 0 && next_u + 1 < units)
+              next_unit = unit_of<NR, true>(p, groups, ++next_u, bad_len, num_groups);
+          }
+        }
 #pragma unroll 1
         for (int j = 0; j < 2; ++j) {
           wait_for(&bars[L::bRawFree + slot], parity, abort_flag, p.d_error);
           if (j == 0 && lane == 0) {
-            info[n % kInfoRing] = make_int4(word, tile, u, 0);
+            info[n % kInfoRing] = make_int4(word, tile, u, kShared ? next_u : 0);
             mbar_arrive(&bars[L::bInfo + n % kInfoRing]);
           }
           // After a wait that gave up nothing more is asked for.
@@ -637,19 +714,25 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
           // join the pieces of parts `part` .. last when this part's end cuts it.
           const bool merges = k + 1 < unit.tiles;
           const int last = part + (cut[3] - 1 + unit.tiles - k - 1) / cut[3];
-          if (p.info_by_unit)
+          if (kShared || p.info_by_unit)
             *reinterpret_cast<int4*>(p.ws_info + u * 4) = make_int4(merges ? u : -1, part, last, 0);
           else if (n + 1 == items)
             *reinterpret_cast<int4*>(p.ws_info + part * 4) = make_int4(merges ? u : -1, part, last, 0);
-        } else if (n + 1 == items && lane == 0 && !p.info_by_unit) {
+        } else if (n + 1 == items && lane == 0 && !(kShared || p.info_by_unit)) {
           p.ws_info[part * 4] = -1;
         }
         if (++k == unit.tiles && n + 1 < items) {
           k = 0;
-          unit = unit_of<NR>(p, groups, ++u, bad_len);
+          if constexpr (kShared) {
+            unit = next_unit;
+            u = next_u;
+          } else {
+            unit = unit_of<NR, false>(p, groups, ++u, bad_len, 0);
+          }
           // Its Q on the way to L2, a few tiles before it is read.
           const uint8_t* next = reinterpret_cast<const uint8_t*>(
-              p.q + (static_cast<int64_t>(unit.b) * p.rows + unit.row0) * kD);
+              p.q + (kShared && unit.b < 0 ? static_cast<int64_t>(unit.row0)
+                                           : static_cast<int64_t>(unit.b) * p.rows + unit.row0) * kD);
           for (int line = lane; line < unit.nrows * 8; line += 32)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(next + line * 128));
         }
@@ -855,7 +938,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
       const auto convert_q = [&](int u, bool first) {
         constexpr int kRowsAtOnce = NR == 16 ? 2 : 1;  // (registers)
         bool bad_len;
-        const Unit t = first ? *first_unit : unit_of<NR>(p, groups, u, bad_len);
+        const Unit t = first ? *first_unit : unit_of<NR, kShared>(p, groups, u, bad_len, num_groups);
         wait_for(&bars[L::bQRaw], q_parity, abort_flag, p.d_error);
         q_parity ^= 1;
         uint8_t* base = sQ + (lane >> 2) * (NR * 128);
@@ -895,7 +978,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[L::bQFull]);
         if (tid < NR) {
-          const int hi = t.first + min(t.row0 + tid, p.rows - 1) / p.h;
+          const int hi = kShared && t.b < 0 ? t.p_hi : t.first + min(t.row0 + tid, p.rows - 1) / p.h;
           c_hi[tid] = hi;
           c_lo[tid] = window_start(p, hi);
         }
@@ -938,7 +1021,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
         // The piece's last scores are there, so its Q has been read: the next unit's may come.
         // (None after a wait that gave up: the last one asked for has to have landed at the end.)
         if ((it.x & kCloses) && n + 1 < items && tid == 0 && !*abort_flag) {
-          request_q(min(max(info[n % kInfoRing].z, 0) + 1, units - 1));
+          request_q(min(kShared ? max(info[n % kInfoRing].w, 0) : max(info[n % kInfoRing].z, 0) + 1, units - 1));
           cut[4] ^= 1;
         }
         if (!(it.x & kWhole)) {
@@ -1083,10 +1166,15 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
         LaneReduce<NC, 16>::run(l, lane, OpAdd());
         if (lane % (32 / NC) == 0) red[quad * NR + c0 + column_of<NC>(lane)] = l[0];
         named_bar_sync(1, kSoftmaxThreads);
-        const bool whole_unit = (it.x & (kFromStart | kToEnd)) == (kFromStart | kToEnd);
+        const bool whole_unit = !kShared && (it.x & (kFromStart | kToEnd)) == (kFromStart | kToEnd);
         // Partials: slot 2 part + 1 for a piece that begins its unit, 2 part for one that goes on with it.
-        const int prow = (part * 2 + ((it.x & kFromStart) ? 1 : 0)) * NR;
+        std::conditional_t<kShared, int64_t, int> prow = (part * 2 + ((it.x & kFromStart) ? 1 : 0)) * NR;
         const int u = min(max(info[n % kInfoRing].z, 0), units - 1);  // (after a wait that gave up it may be anything)
+        if constexpr (kShared) {
+          // A whole unit has a slot of its own behind those.
+          if ((it.x & (kFromStart | kToEnd)) == (kFromStart | kToEnd))
+            prow = (2 * static_cast<int64_t>(gridDim.x) + u) * NR;
+        }
         const int ub = u / groups, urow0 = (u - ub * groups) * NR;
         const int orow = ub * p.rows + urow0, nrows = min(NR, p.rows - urow0);
         if (tid < NR) {
@@ -1101,7 +1189,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
         }
         named_bar_sync(1, kSoftmaxThreads);
         // The next unit's Q goes in while the last product runs (this piece's scores are all done).
-        if (n + 1 < items) convert_q(min(u + 1, units - 1), false);
+        if (n + 1 < items) convert_q(min(kShared ? max(info[n % kInfoRing].w, 0) : u + 1, units - 1), false);
         wait_for(&bars[L::bPFree + 1], n & 1, abort_flag, p.d_error);
         tc_fence_after();
         // Lane = dim, columns = rows.
@@ -1263,11 +1351,11 @@ __global__ void __launch_bounds__(512) paged_merge_many_kernel(const PagedParams
   if (tid == 0) p.lse[row] = z > 0.f ? m + logf(z) : -INFINITY;
 }
 
-template <int NR>
-cudaError_t launch(PagedParams p, const PagedPlan& plan, cudaStream_t stream) {
-  p.info_by_unit = static_cast<int64_t>(p.batch) * plan.groups <= plan.num_parts;
+template <int NR, bool kShared>
+cudaError_t launch(Params<kShared> p, const PagedPlan& plan, cudaStream_t stream) {
+  p.info_by_unit = kShared || static_cast<int64_t>(p.batch) * plan.groups <= plan.num_parts;
   static std::atomic<uint64_t> configured{0};
-  cudaError_t e = max_dynamic_smem_once(configured, reinterpret_cast<const void*>(paged_decode_kernel<NR>),
+  cudaError_t e = max_dynamic_smem_once(configured, reinterpret_cast<const void*>(paged_decode_kernel<NR, kShared>),
                                         PSmem<NR>::kAlloc);
   if (e != cudaSuccess) return e;
   // Q viewed as rows of 512 bf16; a box is NR rows x 64 dims, 128-byte swizzled.
@@ -1308,8 +1396,9 @@ cudaError_t launch(PagedParams p, const PagedPlan& plan, cudaStream_t stream) {
   cfg.gridDim = dim3(static_cast<unsigned>(plan.num_parts));
   cfg.blockDim = dim3(PSmem<NR>::kThreads);
   cfg.dynamicSmemBytes = PSmem<NR>::kAlloc;
-  e = cudaLaunchKernelEx(&cfg, paged_decode_kernel<NR>, p, plan.groups, q_map, data_map, scale_map);
+  e = cudaLaunchKernelEx(&cfg, paged_decode_kernel<NR, kShared>, p, plan.groups, q_map, data_map, scale_map);
   if (e != cudaSuccess) return e;
+  if constexpr (kShared) return launch_shared_merge(p, plan, stream);
   // Units that are few against the parts are cut into many pieces (one
   // sequence of 64k tokens, 16 heads: 32 us so, 66 by single warps; 64 x 64
   // heads over 1k to 8k, in three pieces: 89 against 72).
@@ -1355,9 +1444,40 @@ PagedPlan paged_plan(const mla_paged_problem_t* p, int num_parts) {
 
 cudaError_t launch_paged_decode(const PagedParams& p, const PagedPlan& plan, cudaStream_t stream) {
   switch (plan.nr) {
-    case 16: return launch<16>(p, plan, stream);
-    case 32: return launch<32>(p, plan, stream);
-    default: return launch<64>(p, plan, stream);
+    case 16: return launch<16, false>(p, plan, stream);
+    case 32: return launch<32, false>(p, plan, stream);
+    default: return launch<64, false>(p, plan, stream);
+  }
+}
+
+PagedPlan shared_plan(const mla_paged_shared_problem_t* p, int num_parts) {
+  PagedPlan pl{};
+  const int64_t rows = static_cast<int64_t>(p->seq_len_q) * p->h_q, all = rows * p->batch;
+  // Rows of a unit, by the same reasoning as above: as few as hold a group's
+  // rows, or as leave no part more than three or four tiles.
+  const int64_t group_rows = (all + p->groups - 1) / p->groups;
+  const int64_t tiles = (p->max_prefix_pages + 1) / 2 + kUnitCost, own = (p->max_pages + 1) / 2 + kUnitCost;
+  const auto fits = [&](int nr) {
+    return group_rows <= nr || 2 * (((all + nr - 1) / nr) * tiles + p->batch * ((rows + nr - 1) / nr) * own) <=
+                                   int64_t(7) * num_parts;
+  };
+  pl.nr = fits(16) ? 16 : (fits(32) ? 32 : 64);
+  pl.groups = static_cast<int>((rows + pl.nr - 1) / pl.nr);
+  pl.num_parts = num_parts;
+  const int64_t units = p->batch * static_cast<int64_t>(pl.groups) + all / pl.nr + p->groups;
+  pl.units = static_cast<int>(units);
+  const size_t slots = 2 * static_cast<size_t>(num_parts) + static_cast<size_t>(units);
+  pl.ws_o_bytes = slots * pl.nr * MLA_HEAD_DIM * sizeof(float);
+  pl.ws_lse_bytes = slots * pl.nr * sizeof(float);
+  pl.ws_bytes = pl.ws_o_bytes + pl.ws_lse_bytes + (static_cast<size_t>(units) + 1) * 4 * sizeof(int32_t);
+  return pl;
+}
+
+cudaError_t launch_shared_decode(const SharedParams& p, const PagedPlan& plan, cudaStream_t stream) {
+  switch (plan.nr) {
+    case 16: return launch<16, true>(p, plan, stream);
+    case 32: return launch<32, true>(p, plan, stream);
+    default: return launch<64, true>(p, plan, stream);
   }
 }
 

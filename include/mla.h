@@ -558,6 +558,60 @@ mla_status_t mla_paged_sparse_decode_fp4(const mla_paged_sparse_problem_t* probl
                                          int32_t num_parts, void* workspace, size_t workspace_bytes, void* out,
                                          float* lse, int32_t* selected, int32_t* d_error, mla_stream_t stream);
 
+/*
+ * Attention for a batch whose sequences share long prefixes (a system prompt, a
+ * document, the prompt of many samples): each group of consecutive sequences has
+ * one prefix, whose records are read and decoded once for all rows of the group,
+ * and every sequence goes on with pages of its own.
+ */
+typedef struct {
+  int32_t batch;            /* b >= 1 */
+  int32_t seq_len_q;        /* s >= 1: the last s tokens of each sequence are the query tokens */
+  int32_t h_q;              /* query heads, 1 .. 128 */
+  int32_t head_dim;         /* must be 512 */
+  int32_t page_size;        /* must be 64 */
+  int32_t groups;           /* prefixes, 1 .. MLA_MAX_PREFIX_GROUPS */
+  int32_t max_prefix_pages; /* entries of a prefix table row */
+  int32_t max_pages;        /* entries of a block table row (own pages); tables no wider than the sequences need are faster */
+  int64_t num_pages;        /* pages in the pool (bounds check of the tables) */
+  int32_t kv_format;        /* must be MLA_KV_FP4_288 */
+  float sm_scale;           /* as in mla_paged_problem_t */
+} mla_paged_shared_problem_t;
+#define MLA_MAX_PREFIX_GROUPS 8192
+
+/* Host-only planning, as mla_paged_decode_plan.  The workspace holds fp32 outputs of every query row twice. */
+mla_status_t mla_paged_shared_plan(const mla_paged_shared_problem_t* problem, int32_t num_sms, int32_t* num_parts_out,
+                                   size_t* workspace_bytes_out);
+
+/*
+ * One attention step.  Sequences group_start[g] .. group_start[g + 1] - 1 share
+ * prefix g; sequences in no group have none.  Query token i of sequence b stands
+ * at position p = seq_lens[b] - s + i of its own tokens; it sees the own tokens
+ * j <= p and, if p >= 0, the whole prefix, all under one softmax:
+ *     lse = ln sum_j exp(sm_scale <q, k_j>),  out = sum_j exp(sm_scale <q, k_j> - lse) k_j.
+ * A query token with p < 0 (padding) gets +0 and -inf.
+ *   q, kv, out, lse   as in mla_paged_decode_fp4.
+ *   group_start  int32 [groups + 1], ascending from >= 0 to <= batch; groups may
+ *                be empty.  Otherwise no sequence has a prefix (MLA_DEVERR_BAD_METADATA).
+ *   prefix_table int32 [groups][max_prefix_pages]: page ids; entries past
+ *                ceil(prefix_lens[g] / 64) are not read.
+ *   prefix_lens  int32 [groups], any length (the last page may be part full);
+ *                negative or past 64 * max_prefix_pages: treated as 0 and
+ *                flagged (MLA_DEVERR_BAD_LENGTH).
+ *   block_table  int32 [batch][max_pages]: the sequences' own pages.
+ *   seq_lens     int32 [batch]: their own tokens, the query tokens included, the
+ *                prefix not; bad lengths as in mla_paged_decode_fp4.
+ * Page ids outside the pool: their tokens are skipped and flagged
+ * (MLA_DEVERR_BAD_INDEX).  num_parts, workspace, workspace_bytes and d_error as in
+ * mla_paged_decode_fp4, from mla_paged_shared_plan.
+ */
+mla_status_t mla_paged_shared_decode_fp4(const mla_paged_shared_problem_t* problem, const void* q, const void* kv,
+                                         const int32_t* group_start, const int32_t* prefix_table,
+                                         const int32_t* prefix_lens, const int32_t* block_table,
+                                         const int32_t* seq_lens, int32_t num_parts, void* workspace,
+                                         size_t workspace_bytes, void* out, float* lse, int32_t* d_error,
+                                         mla_stream_t stream);
+
 /* Static description of a status code. */
 const char* mla_status_string(mla_status_t status);
 
