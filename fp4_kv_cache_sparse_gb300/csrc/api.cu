@@ -738,6 +738,7 @@ mla_status_t mla_paged_sparse_decode_fp4(const mla_paged_sparse_problem_t* probl
   sp.top = problem->top_pages;
   sp.sinks = problem->sink_pages;
   sp.local = problem->local_pages;
+  sp.num_parts = num_parts;
   sp.num_pages = problem->num_pages;
   sp.sign = problem->sm_scale < 0.f ? -1.f : 1.f;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

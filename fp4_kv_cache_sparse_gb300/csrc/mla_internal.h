@@ -199,7 +199,7 @@ struct SelectParams {
   int32_t* sel_lens;           // [batch * s]
   int32_t* selected;           // [batch * s][top]: pages of the sequence, nullable
   int32_t* d_error;            // nullable
-  int batch, s, h, max_pages, top, sinks, local;
+  int batch, s, h, max_pages, top, sinks, local, num_parts;
   int64_t num_pages;
   float sign;                  // that of the softmax scale
 };

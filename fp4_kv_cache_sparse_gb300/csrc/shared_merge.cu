@@ -10,16 +10,11 @@
 
 #include "mla_device.cuh"
 #include "mla_internal.h"
+#include "mla_tensor.cuh"
 
 namespace mla {
 
 namespace {
-
-__device__ __forceinline__ int load_i32(const int32_t* p) {
-  int v;
-  asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  return v;
-}
 
 // Where the pieces of a unit lie: in its own slot when it is whole, otherwise
 // in the first part's slot 2 part + 1 and the slots 2 part of those that follow.
