@@ -182,6 +182,11 @@ def _check(status: int, what: str):
         raise MLAError(status, what)
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or (lambda: torch.cuda.current_device())
+
+
 def _ptr(t):
     if t is None:
         return None
@@ -195,8 +200,7 @@ def _ptr(t):
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    return ctypes.c_void_p(stream.cuda_stream if stream is not None else _raw_stream(_current_device()))
 
 
 def get_metadata(problem: Problem, num_sms: int = 0, device=None, stream=None):
@@ -318,11 +322,6 @@ def decode(q, kv, indices, extra_kv=None, extra_indices=None, sm_scale=None):
 # one CUDA device; the call runs there, on `stream` or that device's current
 # stream, whichever device is current.
 # ---------------------------------------------------------------------------
-
-
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-_current_device = getattr(torch._C, "_cuda_getDevice", None) or (lambda: torch.cuda.current_device())
 
 
 def _device_of(t, what):

@@ -31,7 +31,8 @@ struct Piece {
   uint32_t sc;
 };
 
-// The 32 dims' values, two e4m3 scales; a NaN scale counts as 448.
+// acc += the 32 dims' values under two e4m3 scales: f16 codes times f16 scales
+// into fp32 by single instructions, exact each.  A NaN scale counts as 448.
 __device__ __forceinline__ void add32(const Piece& p, float (&acc)[32]) {
   uint32_t s2 = e4m3x2_to_f16x2(p.sc & 0x7F7Fu);
   asm("min.f16x2 %0, %0, %1;" : "+r"(s2) : "r"(0x5F005F00u));
@@ -39,19 +40,26 @@ __device__ __forceinline__ void add32(const Piece& p, float (&acc)[32]) {
   const uint32_t w[4] = {p.data.x, p.data.y, p.data.z, p.data.w};
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const uint32_t s = k < 2 ? __byte_perm(s2, s2, 0x1010) : __byte_perm(s2, s2, 0x3232);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t h = e2m1x2_to_f16x2((w[k] >> (8 * j)) & 0xFFu);
-      uint32_t v;
-      asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(v) : "r"(h), "r"(s));
-      float lo, hi;
-      asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
-          : "=f"(lo), "=f"(hi)
-          : "r"(v));
-      acc[8 * k + 2 * j] += lo;
-      acc[8 * k + 2 * j + 1] += hi;
-    }
+    const uint32_t s = k < 2 ? s2 : s2 >> 16;
+    float* o = acc + 8 * k;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t.reg .b32 h0, h1, h2, h3;\n\t.reg .b16 s, t, l0, u0, l1, u1, l2, u2, l3, u3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %8;\n\t"
+        "mov.b32 {s, t}, %9;\n\t"
+        "cvt.rn.f16x2.e2m1x2 h0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 h1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 h2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 h3, b3;\n\t"
+        "mov.b32 {l0, u0}, h0;\n\tmov.b32 {l1, u1}, h1;\n\tmov.b32 {l2, u2}, h2;\n\tmov.b32 {l3, u3}, h3;\n\t"
+        "fma.rn.f32.f16 %0, l0, s, %0;\n\t"
+        "fma.rn.f32.f16 %1, u0, s, %1;\n\t"
+        "fma.rn.f32.f16 %2, l1, s, %2;\n\t"
+        "fma.rn.f32.f16 %3, u1, s, %3;\n\t"
+        "fma.rn.f32.f16 %4, l2, s, %4;\n\t"
+        "fma.rn.f32.f16 %5, u2, s, %5;\n\t"
+        "fma.rn.f32.f16 %6, l3, s, %6;\n\t"
+        "fma.rn.f32.f16 %7, u3, s, %7;\n\t}"
+        : "+f"(o[0]), "+f"(o[1]), "+f"(o[2]), "+f"(o[3]), "+f"(o[4]), "+f"(o[5]), "+f"(o[6]), "+f"(o[7])
+        : "r"(w[k]), "r"(s));
   }
 }
 
@@ -60,10 +68,10 @@ __device__ __forceinline__ void add32(const Piece& p, float (&acc)[32]) {
 __device__ __forceinline__ int column(int d) { return d + (d >> 5) * 4; }
 constexpr int kRow = kD + (kD / 32) * 4;
 
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, 4)
     page_means_kernel(const uint8_t* pool, int64_t pool_tokens, const int32_t* slots, int64_t n, uint8_t* means,
                       int32_t* d_error) {
-  __shared__ int sums[kThreads / 32][kRow];
+  __shared__ float sums[kThreads / 16][kRow];  // of four tokens each
   __shared__ int32_t pages[kThreads];
   __shared__ uint32_t counts[kThreads / 32];
   __shared__ uint32_t tops[kThreads / 32];
@@ -107,26 +115,18 @@ __global__ void __launch_bounds__(kThreads, 3)
 #pragma unroll
       for (int j = 0; j < kTokens; ++j) add32(next[j], acc);
       if (k + 1 < total) fetch(k + 1);
-      // In units of 2^-10; lanes l and l + 16 have the same dims.
+      float* mine = &sums[tid >> 4][column((tid & 15) * 32)];
 #pragma unroll
-      for (int c = 0; c < 32; c += 4) {
-        int v[4];
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          v[m] = static_cast<int>(acc[c + m] * 1024.f);
-          v[m] += __shfl_xor_sync(0xFFFFFFFFu, v[m], 16);
-        }
-        if ((lane >> 4) == ((c >> 2) & 1))
-          *reinterpret_cast<int4*>(&sums[warp][column((lane & 15) * 32 + c)]) = make_int4(v[0], v[1], v[2], v[3]);
-      }
+      for (int c = 0; c < 32; c += 4)
+        *reinterpret_cast<float4*>(mine + c) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
       __syncthreads();
-      // Thread t: dims 2 t and 2 t + 1.
+      // Thread t: dims 2 t and 2 t + 1, in units of 2^-10.
       int a = 0, b = 0;
 #pragma unroll
-      for (int w = 0; w < kThreads / 32; ++w) {
-        const int2 v = *reinterpret_cast<const int2*>(&sums[w][column(2 * tid)]);
-        a += v.x;
-        b += v.y;
+      for (int g = 0; g < kThreads / 16; ++g) {
+        const float2 v = *reinterpret_cast<const float2*>(&sums[g][column(2 * tid)]);
+        a += static_cast<int>(v.x * 1024.f);
+        b += static_cast<int>(v.y * 1024.f);
       }
       uint32_t top = max(abs(a), abs(b));
       top = __reduce_max_sync(0xFFFFFFFFu, top);
@@ -160,7 +160,7 @@ cudaError_t launch_page_means(const uint8_t* pool, int64_t pool_tokens, const in
                               int32_t* d_error, cudaStream_t stream) {
   int dev = 0, sms = 152;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const int64_t most = static_cast<int64_t>(sms) * 4 - 1;  // odd
+  const int64_t most = static_cast<int64_t>(sms) * 4 - 1;  // odd; all of them resident
   const int64_t blocks = n < most ? n : most;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
