@@ -21,8 +21,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libmla.so")
 SOURCES = ["api.cu", "metadata.cu", "decode.cu", "decode_pair.cu", "combine.cu", "dequant.cu", "noalloc.cu", "kv_write.cu",
            "page_plan.cu", "rope.cu", "norm.cu", "paged.cu", "append.cu", "page_means.cu",
-           "select.cu", "shared_merge.cu"]
-HEADERS = ["mla_device.cuh", "mla_internal.h", "mla_rows.cuh", "mla_tensor.cuh"]
+           "select.cu", "shared_merge.cu", "paged_pair.cu"]
+HEADERS = ["mla_device.cuh", "mla_internal.h", "mla_rows.cuh", "mla_tensor.cuh", "shared_units.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
          "--expt-relaxed-constexpr"]

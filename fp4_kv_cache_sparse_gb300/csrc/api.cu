@@ -760,7 +760,7 @@ mla_status_t mla_paged_shared_plan(const mla_paged_shared_problem_t* problem, in
     if (st != MLA_OK) return st;
   }
   const PagedPlan pl = shared_plan(problem, num_sms);
-  *num_parts_out = pl.num_parts;
+  *num_parts_out = num_sms;
   *workspace_bytes_out = pl.ws_bytes;
   return MLA_OK;
 }

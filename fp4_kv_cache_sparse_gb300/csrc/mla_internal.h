@@ -166,6 +166,7 @@ struct PagedPlan {
   int groups;      // row groups of a sequence
   int num_parts;
   int units;       // shared prefixes: numbers of units
+  bool pair;       // shared prefixes by pairs of SMs: a unit is 128 rows, a part is a pair
   size_t ws_o_bytes, ws_lse_bytes, ws_bytes;
 };
 PagedPlan paged_plan(const mla_paged_problem_t* p, int num_parts);
@@ -186,6 +187,7 @@ struct SharedParams : PagedParams {
 PagedPlan shared_plan(const mla_paged_shared_problem_t* p, int num_parts);
 cudaError_t launch_shared_decode(const SharedParams& p, const PagedPlan& plan, cudaStream_t stream);
 cudaError_t launch_shared_merge(const SharedParams& p, const PagedPlan& plan, cudaStream_t stream);
+cudaError_t launch_shared_pair(const SharedParams& p, const PagedPlan& plan, cudaStream_t stream);
 
 // Which pages each query token attends to: scores of the pages' means, and the
 // best of them as block tables and lengths of one-token sequences.

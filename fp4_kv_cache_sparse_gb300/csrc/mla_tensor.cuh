@@ -124,4 +124,82 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
+// 32 consecutive dims of a record: 16 data bytes and their two scale bytes
+// (sc, low byte first) -> 16 f16x2, exact.  As a value a NaN scale counts as
+// 448: a row that does not see the token multiplies it by 0, one that does
+// has a NaN weight from the key.
+template <bool kValue>
+__device__ __forceinline__ void decode32(const uint4& data, uint32_t sc, uint32_t (&o)[16]) {
+  uint32_t s2 = e4m3x2_to_f16x2(sc);
+  if constexpr (kValue) asm("min.f16x2 %0, %0, %1;" : "+r"(s2) : "r"(0x5F005F00u));
+  const uint32_t s0 = __byte_perm(s2, s2, 0x1010), s1 = __byte_perm(s2, s2, 0x3232);
+  const uint32_t w[4] = {data.x, data.y, data.z, data.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t a, b, c, d;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+        : "r"(w[k]));
+    const uint32_t s = k < 2 ? s0 : s1;
+    o[4 * k + 0] = mul_f16x2(a, s);
+    o[4 * k + 1] = mul_f16x2(b, s);
+    o[4 * k + 2] = mul_f16x2(c, s);
+    o[4 * k + 3] = mul_f16x2(d, s);
+  }
+}
+
+// Reduction of v[N] over the 32 lanes; afterwards lane l holds in v[0 ..
+// max(N/32, 1)) the columns column_of<N>(l).
+template <int SIZE, int O>
+struct LaneReduce {
+  template <int N, typename Op>
+  __device__ __forceinline__ static void run(float (&v)[N], int lane, Op op) {
+    if constexpr (O == 0) {
+      return;
+    } else if constexpr (SIZE == 1) {
+      v[0] = op(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], O));
+      LaneReduce<1, O / 2>::run(v, lane, op);
+    } else {
+      constexpr int H = SIZE / 2;
+      const bool up = (lane & O) != 0;
+#pragma unroll
+      for (int k = 0; k < H; ++k) {
+        const float send = up ? v[k] : v[k + H];
+        const float keep = up ? v[k + H] : v[k];
+        v[k] = op(keep, __shfl_xor_sync(0xFFFFFFFFu, send, O));
+      }
+      LaneReduce<H, O / 2>::run(v, lane, op);
+    }
+  }
+};
+template <int N>
+__device__ __forceinline__ int column_of(int lane) {
+  static_assert(N <= 32, "one column per lane");
+  return lane / (32 / N);
+}
+struct OpMax {
+  __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+struct OpAdd {
+  __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+
+__device__ __forceinline__ bool any_of(int id, int threads, bool mine) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred pi, po;\n\t"
+      "setp.ne.s32 pi, %1, 0;\n\t"
+      "bar.red.or.pred po, %2, %3, pi;\n\t"
+      "selp.s32 %0, 1, 0, po;\n\t}"
+      : "=r"(r)
+      : "r"(mine ? 1 : 0), "r"(id), "r"(threads)
+      : "memory");
+  return r != 0;
+}
+
 }  // namespace mla

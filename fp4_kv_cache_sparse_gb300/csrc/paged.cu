@@ -74,6 +74,7 @@
 #include "mla_device.cuh"
 #include "mla_internal.h"
 #include "mla_tensor.cuh"
+#include "shared_units.cuh"
 
 namespace mla {
 
@@ -193,33 +194,17 @@ __device__ __forceinline__ int window_start(const PagedParams& p, int at) {
 template <bool kShared>
 using Params = std::conditional_t<kShared, SharedParams, PagedParams>;
 
-// The first prefix unit of group g, counted from the first of all (mla_internal.h).
-__device__ __forceinline__ int prefix_unit(const SharedParams& p, int nr, int g) {
-  return load_i32(p.group_start + g) * p.rows / nr + g;
-}
-
-// A block of rows of a group of sequences over their prefix: b is -1 - g, row0
-// counts from the batch's first row, every row sees every token.  Numbers that
-// fall between two groups, and groups without a prefix, have no tiles.
+// A prefix unit: b is -1 - group, row0 counts from the batch's first row, every row sees every token.
 template <int NR>
 __device__ __forceinline__ Unit prefix_unit_of(const SharedParams& p, int v, int num_groups, bool& bad) {
+  const PrefixUnit at = prefix_unit_at<NR>(p, v, num_groups);
   Unit t{};
-  bad = false;
-  if (num_groups == 0) return t;
-  int g = 0;  // the last group whose units begin at or before v
-  for (int n = num_groups; n > 1;) {
-    const int half = n / 2;
-    if (prefix_unit(p, NR, g + half) <= v) g += half;
-    n -= half;
-  }
-  const int from = load_i32(p.group_start + g) * p.rows, to = load_i32(p.group_start + g + 1) * p.rows;
-  const int len = load_i32(p.prefix_lens + g), k = v - prefix_unit(p, NR, g);
-  bad = len < 0 || len > p.max_prefix_pages * kPage;
-  t.b = -1 - g;
-  t.row0 = from + k * NR;
-  t.nrows = min(NR, to - t.row0);
-  t.first = t.p_lo = t.p_hi = len - 1;
-  t.tiles = bad || k < 0 || t.nrows <= 0 ? 0 : (len + kTile - 1) / kTile;
+  bad = at.bad;
+  t.b = -1 - at.group;
+  t.row0 = at.row0;
+  t.nrows = at.nrows;
+  t.first = t.p_lo = t.p_hi = at.len - 1;
+  t.tiles = (at.len + kTile - 1) / kTile;
   return t;
 }
 
@@ -267,84 +252,6 @@ __device__ __forceinline__ bool token_there(int info, int row) {
 
 __device__ __forceinline__ void wait_for(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* d_error) {
   mbar_wait_warp(bar, parity, abort_flag, d_error, kPagedWaitNs);
-}
-
-// 32 consecutive dims of a record: 16 data bytes and their two scale bytes
-// (sc, low byte first) -> 16 f16x2, exact.  As a value a NaN scale counts as
-// 448: a row that does not see the token multiplies it by 0, one that does
-// has a NaN weight from the key.
-template <bool kValue>
-__device__ __forceinline__ void decode32(const uint4& data, uint32_t sc, uint32_t (&o)[16]) {
-  uint32_t s2 = e4m3x2_to_f16x2(sc);
-  if constexpr (kValue) asm("min.f16x2 %0, %0, %1;" : "+r"(s2) : "r"(0x5F005F00u));
-  const uint32_t s0 = __byte_perm(s2, s2, 0x1010), s1 = __byte_perm(s2, s2, 0x3232);
-  const uint32_t w[4] = {data.x, data.y, data.z, data.w};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    uint32_t a, b, c, d;
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-        : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
-        : "r"(w[k]));
-    const uint32_t s = k < 2 ? s0 : s1;
-    o[4 * k + 0] = mul_f16x2(a, s);
-    o[4 * k + 1] = mul_f16x2(b, s);
-    o[4 * k + 2] = mul_f16x2(c, s);
-    o[4 * k + 3] = mul_f16x2(d, s);
-  }
-}
-
-// Reduction of v[N] over the 32 lanes; afterwards lane l holds in v[0 ..
-// max(N/32, 1)) the columns column_of<N>(l).
-template <int SIZE, int O>
-struct LaneReduce {
-  template <int N, typename Op>
-  __device__ __forceinline__ static void run(float (&v)[N], int lane, Op op) {
-    if constexpr (O == 0) {
-      return;
-    } else if constexpr (SIZE == 1) {
-      v[0] = op(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], O));
-      LaneReduce<1, O / 2>::run(v, lane, op);
-    } else {
-      constexpr int H = SIZE / 2;
-      const bool up = (lane & O) != 0;
-#pragma unroll
-      for (int k = 0; k < H; ++k) {
-        const float send = up ? v[k] : v[k + H];
-        const float keep = up ? v[k + H] : v[k];
-        v[k] = op(keep, __shfl_xor_sync(0xFFFFFFFFu, send, O));
-      }
-      LaneReduce<H, O / 2>::run(v, lane, op);
-    }
-  }
-};
-template <int N>
-__device__ __forceinline__ int column_of(int lane) {
-  static_assert(N <= 32, "one column per lane");
-  return lane / (32 / N);
-}
-struct OpMax {
-  __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
-};
-struct OpAdd {
-  __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
-};
-
-__device__ __forceinline__ bool any_of(int id, int threads, bool mine) {
-  int r;
-  asm volatile(
-      "{\n\t.reg .pred pi, po;\n\t"
-      "setp.ne.s32 pi, %1, 0;\n\t"
-      "bar.red.or.pred po, %2, %3, pi;\n\t"
-      "selp.s32 %0, 1, 0, po;\n\t}"
-      : "=r"(r)
-      : "r"(mine ? 1 : 0), "r"(id), "r"(threads)
-      : "memory");
-  return r != 0;
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -413,18 +320,7 @@ __global__ void __launch_bounds__(PSmem<NR>::kThreads, 1)
 
   int num_groups = 0;
   if constexpr (kShared) {
-    // Groups that are not in order count as none.
-    bool wrong = false;
-    for (int g = tid; g <= p.num_groups; g += kPagedThreads) {
-      const int at = load_i32(p.group_start + g);
-      wrong = wrong || at < 0 || at > p.batch || (g > 0 && at < load_i32(p.group_start + g - 1));
-    }
-    const bool none = __syncthreads_or(wrong);
-    num_groups = none ? 0 : p.num_groups;
-    if (part == 0 && tid == 0) {
-      p.ws_info[p.units * 4] = num_groups;
-      if (none && p.d_error) atomicOr(p.d_error, MLA_DEVERR_BAD_METADATA);
-    }
+    num_groups = groups_in_order(p, tid, kPagedThreads, part == 0);
   }
 
   // A unit's Q arrives by TMA as bf16, K-major with 128-byte swizzle ...
@@ -1293,7 +1189,8 @@ cudaError_t launch(Params<kShared> p, const PagedPlan& plan, cudaStream_t stream
   cfg.gridDim = dim3(static_cast<unsigned>(p.info_by_unit ? units : plan.num_parts), many ? NR : NR / 4);
   cfg.blockDim = dim3(many ? 512 : 128);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, many ? paged_merge_many_kernel : paged_merge_kernel, p, plan.groups, NR);
+  return cudaLaunchKernelEx(&cfg, many ? paged_merge_many_kernel : paged_merge_kernel,
+                            static_cast<const PagedParams&>(p), plan.groups, NR);
 }
 
 }  // namespace
@@ -1348,11 +1245,25 @@ PagedPlan shared_plan(const mla_paged_shared_problem_t* p, int num_parts) {
                                    int64_t(7) * num_parts;
   };
   pl.nr = fits(16) ? 16 : (fits(32) ? 32 : 64);
-  pl.groups = static_cast<int>((rows + pl.nr - 1) / pl.nr);
   pl.num_parts = num_parts;
+  // By pairs of SMs where there are many rows to a prefix and long ones: an item of 256 tokens x 128 rows takes a pair
+  // some 8000 cycles, a tile of 128 x 64 an SM 6000, and a pair's start, exchanges and end 10 us more (64 x 128 heads
+  // over a prefix of 16k tokens 266 and 354 us; 31 x 2 x 24 heads over three of up to 9k 52 and 43; 8 x 16 heads over 4k
+  // 24 and 13).
+  const auto work = [&](int64_t nr, int64_t tokens) {
+    const auto items = [&](int64_t pages) { return (pages * kPage + tokens - 1) / tokens + kUnitCost; };
+    return static_cast<double>((all + nr - 1) / nr + p->groups / 2) * items(p->max_prefix_pages) +
+           static_cast<double>(p->batch) * ((rows + nr - 1) / nr) * items(p->max_pages);
+  };
+  if (num_parts >= 2 && work(128, 256) * 8000 / (num_parts / 2) + 20000 < work(64, 128) * 6000 / num_parts) {
+    pl.pair = true;
+    pl.nr = 128;
+    pl.num_parts = num_parts / 2;
+  }
+  pl.groups = static_cast<int>((rows + pl.nr - 1) / pl.nr);
   const int64_t units = p->batch * static_cast<int64_t>(pl.groups) + all / pl.nr + p->groups;
   pl.units = static_cast<int>(units);
-  const size_t slots = 2 * static_cast<size_t>(num_parts) + static_cast<size_t>(units);
+  const size_t slots = 2 * static_cast<size_t>(pl.num_parts) + static_cast<size_t>(units);
   pl.ws_o_bytes = slots * pl.nr * MLA_HEAD_DIM * sizeof(float);
   pl.ws_lse_bytes = slots * pl.nr * sizeof(float);
   pl.ws_bytes = pl.ws_o_bytes + pl.ws_lse_bytes + (static_cast<size_t>(units) + 1) * 4 * sizeof(int32_t);
@@ -1360,6 +1271,7 @@ PagedPlan shared_plan(const mla_paged_shared_problem_t* p, int num_parts) {
 }
 
 cudaError_t launch_shared_decode(const SharedParams& p, const PagedPlan& plan, cudaStream_t stream) {
+  if (plan.pair) return launch_shared_pair(p, plan, stream);
   switch (plan.nr) {
     case 16: return launch<16, true>(p, plan, stream);
     case 32: return launch<32, true>(p, plan, stream);

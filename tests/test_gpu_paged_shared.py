@@ -17,15 +17,24 @@ DEV = torch.device("cuda", 0)
 I32 = torch.int32
 
 
+@pytest.fixture(params=[1, 9000], ids=["narrow", "wide"], autouse=True)
+def width(request):
+    """Prefix tables as wide as needed, or so wide that the plan expects long prefixes: pairs of SMs then take 128 rows."""
+    Shared.width = request.param
+    yield
+    Shared.width = 1
+
+
 class Shared(Case):
     """Own tokens as Case lays them out; prefixes in pages of their own, whatever is past their ends NaN scales."""
+    width = 1
 
     def __init__(self, lens, s, h, start, plens, max_prefix_pages=None, seed=0, **kw):
         super().__init__(lens, s, h, seed=seed, **kw)
         g = torch.Generator(device=DEV).manual_seed(seed + 1)
         self.starts, self.plens = list(start), list(plens)
         held = [-(-n // 64) for n in plens]
-        self.max_prefix_pages = max_prefix_pages or max(max(held), 1)
+        self.max_prefix_pages = max_prefix_pages or max(max(held), Shared.width)
         first = self.num_pages
         extra = torch.full((sum(held) + 1, 64, 288), 0xFF, dtype=torch.uint8, device=DEV)
         self.num_pages += extra.shape[0]
@@ -243,3 +252,43 @@ def test_captured_graph_follows_what_is_on_the_device():
         torch.cuda.synchronize()
         c.check_shared(out, lse)
         assert int(dec.error) == 0
+
+
+@pytest.mark.parametrize("b,s,h", [(9, 1, 128), (3, 4, 100), (40, 1, 33), (129, 1, 1), (1, 2, 128)])
+def test_many_rows_over_every_length(b, s, h):
+    """Rows that fill blocks of 128 and do not, prefixes around the tiles' and items' ends."""
+    for plen in (1, 64, 127, 128, 192, 255, 256, 257, 300, 511, 513, 1025):
+        c = Shared([(29 * r + s) % 300 + (r % 7 > 0) for r in range(b)], s, h, [0, b], [plen], seed=plen + h)
+        out, lse, err = c.run_shared()
+        assert err == 0
+        c.check_shared(out, lse)
+
+
+def test_masses_that_move_between_the_halves_of_an_item():
+    """Large scores alternate between the first and the second 128 tokens of an item, so either half of a pair's tokens
+    raises the maximum that both share; the same bits from run to run."""
+    c = Shared([3, 70, 129, 300] * 8, 1, 64, [0, 32], [256 * 12 - 9], seed=31)
+    n = c.plens[0]
+    pages = c.ptable[0, : -(-n // 64)].long()
+    flat = c.kv[pages].reshape(-1, 288)
+    step = torch.arange(n, device=DEV) // 256
+    big = ((torch.arange(n, device=DEV) // 128) % 2) == (step % 2)
+    flat[:n, :8] = 0x77
+    flat[:n, 256] = torch.where(big, 0x38 + step, torch.full_like(step, 0x20)).to(torch.uint8)
+    c.kv[pages] = flat.view(-1, 64, 288)
+    c.q[..., :16] = 12 * 0.6931471805599453 * 8 / 96 * 512 ** 0.5
+    first = c.run_shared()
+    assert first[2] == 0
+    c.check_shared(*first[:2])
+    for _ in range(20):
+        out, lse, err = c.run_shared()
+        assert err == 0 and torch.equal(out, first[0]) and torch.equal(lse, first[1])
+
+
+def test_nan_records_reach_only_the_rows_that_see_them():
+    c = Shared([65, 200, 9, 64], 2, 64, [0, 2, 4], [500, 700], seed=41)
+    want = c.run_shared()
+    c.kv[int(c.ptable[1, 3]), 5, 256:] = 0x7F           # in the second group's prefix
+    out, lse, err = c.run_shared()
+    assert err == 0
+    assert torch.equal(out[:2], want[0][:2]) and torch.equal(lse[:2], want[1][:2])
