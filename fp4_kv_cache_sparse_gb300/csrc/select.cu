@@ -69,7 +69,7 @@ template <int kThreads>
 __device__ __forceinline__ void choose(const SelectParams& p, int query, const Query& at, uint32_t* keys, int room,
                                        int* counts) {
   int* found = counts + 256;
-  int2* warps = reinterpret_cast<int2*>(found + 2);
+  int2* warps = reinterpret_cast<int2*>(found + 4);
   const int tid = threadIdx.x;
   const int32_t* row = p.block_table + static_cast<int64_t>(query / p.s) * p.max_pages;
   int32_t* selected = p.selected ? p.selected + static_cast<int64_t>(query) * p.top : nullptr;
@@ -88,31 +88,45 @@ __device__ __forceinline__ void choose(const SelectParams& p, int query, const Q
     }
     return;
   }
-  for (int j = tid; j < p.sinks; j += kThreads) take(j, j);
-  for (int j = tid; j < p.local; j += kThreads) take(p.top - p.local + j, at.pages - p.local + j);
   const int k = p.top - p.sinks - p.local, n = at.hi - at.lo;  // n > k
-  if (k == 0) return;
   const float* scores = p.scores + static_cast<int64_t>(query) * p.max_pages + at.lo;
   const auto key_at = [&](int j) { return j < room ? keys[j] : key_of(__ldcg(scores + j)); };
+  uint32_t least = ~0u, most = 0;
 #pragma unroll 4
-  for (int j = tid; j < min(n, room); j += kThreads) keys[j] = key_of(__ldcg(scores + j));
-  uint32_t known = 0;
-  int left = k;  // of the keys that agree with `known` so far, how many are taken
+  for (int j = tid; j < n; j += kThreads) {
+    const uint32_t key = key_of(__ldcg(scores + j));
+    if (j < room) keys[j] = key;
+    least = min(least, key);
+    most = max(most, key);
+  }
+  least = __reduce_min_sync(0xFFFFFFFFu, least);
+  most = __reduce_max_sync(0xFFFFFFFFu, most);
+  if (tid % 32 == 0) warps[tid / 32] = make_int2(least, most);
+  for (int j = tid; j < 256; j += kThreads) counts[j] = 0;
+  __syncthreads();
+  for (int w = 0; w < kThreads / 32; ++w) {
+    least = min(least, static_cast<uint32_t>(warps[w].x));
+    most = max(most, static_cast<uint32_t>(warps[w].y));
+  }
+  __syncthreads();
+  // Bits from `bit` up agree with `known` for every key that still counts.
+  int bit = k > 0 ? 32 - __clz(least ^ most) : 0, left = k;
+  uint32_t known = bit == 32 ? 0 : most >> bit << bit;
+  // The keys from `known` on are taken, all of them when `left` says so.
 #pragma unroll 1
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int j = tid; j < 256; j += kThreads) counts[j] = 0;
-    __syncthreads();
+  for (bool all = false; bit > 0 && !all;) {
+    const int digit = min(bit, 8), shift = bit - digit;
 #pragma unroll 2
     for (int j = tid; j < n; j += kThreads) {
       const uint32_t key = key_at(j);
-      if (shift == 24 || (key >> (shift + 8)) == (known >> (shift + 8))) atomicAdd(&counts[(key >> shift) & 255], 1);
+      if (((key ^ known) >> shift) < (1u << digit)) atomicAdd(&counts[(key >> shift) & ((1u << digit) - 1)], 1);
     }
     __syncthreads();
     if (tid < 32) {
       // Lane l: values 255 - 8 l and the seven below.
-      int sum = 0;
-#pragma unroll 8
-      for (int v = 0; v < 8; ++v) sum += counts[255 - 8 * tid - v];
+      int of[8], sum = 0;
+#pragma unroll
+      for (int v = 0; v < 8; ++v) sum += of[v] = counts[255 - 8 * tid - v];
       int incl = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -121,33 +135,60 @@ __device__ __forceinline__ void choose(const SelectParams& p, int query, const Q
       }
       int above = incl - sum;
       if (above < left && left <= incl) {
-        int v = 255 - 8 * tid;
-        while (above + counts[v] < left) above += counts[v--];
-        found[0] = v;
+        int v = 0;
+#pragma unroll
+        for (int w = 0; w < 7; ++w)
+          if (v == w && above + of[w] < left) above += of[w], ++v;
+        found[0] = 255 - 8 * tid - v;
         found[1] = left - above;
+        found[2] = counts[255 - 8 * tid - v];
       }
     }
     __syncthreads();
     known |= static_cast<uint32_t>(found[0]) << shift;
     left = found[1];
+    all = left == found[2];
+    bit = shift;
+    for (int j = tid; j < 256; j += kThreads) counts[j] = 0;
+    __syncthreads();
   }
-  // Thread t: `per` pages in a row.
+  // Thread t: `per` pages in a row.  A key counts by its bits above those that were not looked at.
   const int per = (n + kThreads - 1) / kThreads;
   const int j0 = min(n, tid * per), j1 = min(n, j0 + per);
+  known >>= bit;
   int2 mine = make_int2(0, 0);
 #pragma unroll 2
   for (int j = j0; j < j1; ++j) {
-    const uint32_t key = key_at(j);
+    const uint32_t key = key_at(j) >> bit;
     mine.x += key > known;
     mine.y += key == known;
   }
   int2 before = block_prefix(mine, warps);
+  // The pages go into a list first, so that their ids are looked up side by side.
+  const bool listed = n + k <= room;
+  uint32_t* list = keys + n;
 #pragma unroll 1
   for (int j = j0; j < j1; ++j) {
-    const uint32_t key = key_at(j);
-    if (key > known || (key == known && before.y < left)) take(p.sinks + before.x + min(before.y, left), at.lo + j);
+    const uint32_t key = key_at(j) >> bit;
+    if (key > known || (key == known && before.y < left)) {
+      const int place = before.x + min(before.y, left);
+      if (listed)
+        list[place] = at.lo + j;
+      else
+        take(p.sinks + place, at.lo + j);
+    }
     before.x += key > known;
     before.y += key == known;
+  }
+  __syncthreads();
+  for (int j = tid; j < p.top; j += kThreads) {
+    const int i = j - p.sinks;
+    if (i < 0)
+      take(j, j);
+    else if (i >= k)
+      take(j, at.pages - p.top + j);
+    else if (listed)
+      take(j, list[i]);
   }
 }
 
@@ -167,9 +208,11 @@ __device__ __forceinline__ void choose(const SelectParams& p, int query, const Q
 // One CTA, 13 warps: decode (8), epilogue (4, which ask for the records of later
 // tiles first), product issuer.  Decode and epilogue warps also make a query
 // token's codes, while its first pages are on their way.
-constexpr int kScoreDecodeWarps = 8, kScoreEpilogueWarps = 4;
+constexpr int kTeams = 2;
+constexpr int kScoreDecodeWarps = 4 * kTeams, kScoreEpilogueWarps = 4;
 constexpr int kCodeWarps = kScoreDecodeWarps + kScoreEpilogueWarps;
-constexpr int kScoreMmaWarp = kCodeWarps;
+constexpr int kScoreLoadWarp0 = kCodeWarps, kScoreLoadWarps = 3,
+              kScoreMmaWarp = kScoreLoadWarp0 + kScoreLoadWarps;
 constexpr int kScoreWarps = kScoreMmaWarp + 1, kScoreThreads = kScoreWarps * 32;
 constexpr uint64_t kScoreWaitNs = 2000000000ull;
 
@@ -179,10 +222,14 @@ struct ScoreSmem {
   // apart as in memory: an odd number of 16-byte units, so rows of a warp meet in
   // no bank.
   static constexpr int kRecords = 32, kStageBytes = kRecords * MLA_MEAN_BYTES;
-  static constexpr int kStages = NR == 128 ? 4 : 8;  // one tile or two
+  static constexpr int kStages = 8;                        // two tiles
+  static constexpr bool kHeadsOnM = NR == 128;
   static constexpr int kKeys = kStages * kStageBytes / 4;  // scores that the choice keeps where the stages were
-  static constexpr int kQOff = 0;
-  static constexpr int kRawOff = NR * kD * 2;
+  // The heads' codes; or, with those in tensor memory, two dim quarters of the pages'
+  // and, before them, the heads' as bytes, 528 apart.
+  static constexpr int kQOff = 0, kQuarter = kTile * 128 * 2;
+  static constexpr int kRawOff = kHeadsOnM ? NR * MLA_MEAN_BYTES : NR * kD * 2;
+  static_assert(kRawOff % 16 == 0 && (!kHeadsOnM || kRawOff >= 2 * kQuarter), "the codes' place");
   static constexpr int kWeightOff = kRawOff + kStages * kStageBytes;  // float[NR]
   static constexpr int kExpOff = kWeightOff + NR * 4;                 // int[NR]
   static constexpr int kScaleOff = kExpOff + NR * 4;                  // float[2][128]
@@ -193,18 +240,19 @@ struct ScoreSmem {
                        bDrain = bQFull + 1, kNumBars = bDrain + 1;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
   static constexpr int kCountOff = kMiscOff + 16;         // int[256], then the choice's small things
-  static constexpr int kAlloc = kCountOff + 1024 + 256 + 1024;
+  static constexpr int kRedOff = kCountOff + 1024 + 256;  // float[2][4][128]: a tile's maxima by lane quadrants
+  static constexpr int kAlloc = kRedOff + (kHeadsOnM ? 2 * 4 * kTile * 4 : 0) + 1024;
   static_assert(kBarOff % 8 == 0 && kAlloc <= 232448, "shared memory of one CTA");
   __device__ static int arrivals(int i) {
     if (i < bRawFree) return 33;                // the lanes whose copies have landed, and the mask's
-    if (i < bKFull) return 2;                   // both teams
+    if (i < bKFull) return kTeams;
     if (i >= bKFull && i < bKFree) return 4;
     if (i >= bSFree && i < bQFull) return 4;
-    if (i == bQFull) return kCodeWarps;
+    if (i == bQFull) return kHeadsOnM ? kScoreDecodeWarps : kCodeWarps;
     return 1;
   }
-  // Tensor memory columns: the codes' quarters, two score buffers.
-  static constexpr int cA = 0, cS = 256;
+  // Tensor memory columns: the codes on M (of the pages by quarters, or the heads'), two score buffers.
+  static constexpr int cA = 0, cS = 256, kSCols = kHeadsOnM ? kTile : NR;
 };
 
 __device__ __forceinline__ int tiles_of(const SelectParams& p, const Query& q) {
@@ -216,6 +264,18 @@ __device__ __forceinline__ void bytes_to_f16(uint32_t w, uint32_t& lo, uint32_t&
   const uint32_t x = w ^ 0x80808080u;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(__byte_perm(x, 0x64646464u, 0x4140)), "r"(0x64806480u));
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(__byte_perm(x, 0x64646464u, 0x4342)), "r"(0x64806480u));
+}
+
+// 32 codes in shared memory.
+__device__ __forceinline__ void codes_to_f16(uint32_t src, uint32_t (&o)[16]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint4 v = lds128(src + h * 16);
+    bytes_to_f16(v.x, o[8 * h + 0], o[8 * h + 1]);
+    bytes_to_f16(v.y, o[8 * h + 2], o[8 * h + 3]);
+    bytes_to_f16(v.z, o[8 * h + 4], o[8 * h + 5]);
+    bytes_to_f16(v.w, o[8 * h + 6], o[8 * h + 7]);
+  }
 }
 
 // 16 bytes into shared memory, and this thread's arrival once its copies so far have landed.
@@ -272,6 +332,22 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_select_kernel(const Sel
   uint32_t n0 = 0, scored = 0;  // tiles and query tokens of this CTA so far
   const int queries = p.batch * p.s;
   for (int u = first, round = 0; u < queries; u += step, ++round) {
+    // The heads by rows, one per warp at a time, lane = 16 dims; the first are under way while the lengths are.
+    constexpr int kRows = (NR + kCodeWarps - 1) / kCodeWarps, kAtOnce = kRows < 6 ? kRows : 6;
+    uint4 raw[kAtOnce][2];
+    const auto load_heads = [&](int i0) {
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int r = warp + (i0 + i) * kCodeWarps;
+        raw[i][0] = raw[i][1] = make_uint4(0, 0, 0, 0);
+        if (r < p.h) {
+          const uint4* src = reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(u) * p.h + r) * kD + 16 * lane);
+          raw[i][0] = src[0];
+          raw[i][1] = src[1];
+        }
+      }
+    };
+    if (warp < kCodeWarps) load_heads(0);
     bool bad;
     const Query query = query_of(p, u / p.s, u % p.s, bad);
     // Tiles rank, rank + cluster, ...
@@ -279,23 +355,20 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_select_kernel(const Sel
     const auto first_page = [&](uint32_t n) {
       return query.lo + (rank + static_cast<int>(n - n0) * cluster) * kTile;
     };
-    // Epilogue warp `quad` asks for its quadrant's records of a tile: lane = record
-    // for the ids, then a record at a time, lane = 16 bytes.  (By a bulk copy per
-    // record, issued by one warp: XXX.)
+    // A load warp asks for a stage's records: lane = record for the ids, then a record
+    // at a time, lane = 16 bytes.  (By a bulk copy per record, issued by one warp: XXX.)
     const int quad = warp & 3;
     const int32_t* table = p.block_table + static_cast<int64_t>(u / p.s) * p.max_pages;
-    int id_next = -1;
-    const auto look_up = [&](uint32_t n) {
-      const int page = first_page(n) + quad * 32 + lane;
-      id_next = n < n0 + tiles && page < query.hi ? load_i32(table + page) : -1;
+    const auto page_of = [&](uint32_t stage_no) { return first_page(stage_no >> 2) + (stage_no & 3) * 32 + lane; };
+    const auto look_up = [&](uint32_t stage_no) {
+      const int page = page_of(stage_no);
+      return stage_no < 4 * (n0 + tiles) && page < query.hi ? load_i32(table + page) : -1;
     };
-    const auto ask = [&](uint32_t n) {
-      const uint32_t stage_no = 4 * n + quad, stage = stage_no % L::kStages;
-      const int id = id_next;
+    const auto ask = [&](uint32_t stage_no, int id) {
+      const uint32_t stage = stage_no % L::kStages;
       const bool ok = id >= 0 && id < p.num_pages;
-      if (!ok && first_page(n) + quad * 32 + lane < query.hi && p.d_error) atomicOr(p.d_error, MLA_DEVERR_BAD_INDEX);
+      if (!ok && page_of(stage_no) < query.hi && p.d_error) atomicOr(p.d_error, MLA_DEVERR_BAD_INDEX);
       const uint32_t there = __ballot_sync(0xFFFFFFFFu, ok);
-      look_up(n + 1);
       wait(L::bRawFree + stage, ((stage_no / L::kStages) & 1) ^ 1);
       if (lane == 0) {
         masks[stage] = there;
@@ -312,31 +385,15 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_select_kernel(const Sel
       __syncwarp();
       copies_arrive(&bars[L::bRawFull + stage]);
     };
-    constexpr int kAhead = L::kStages / 4;  // tiles
-    if (tiles > 0 && warp >= kScoreDecodeWarps && warp < kCodeWarps) {
-      look_up(n0);
-      for (uint32_t n = n0; n < n0 + min(tiles, kAhead); ++n) ask(n);
-    }
     if (tiles > 0 && warp < kCodeWarps) {
-      // The heads' codes: a row per warp at a time, lane = 16 dims; rows past the heads become zeros.  (Every
-      // product with the last token's has been read, as the CTA's barrier behind its scores says.)
-      constexpr int kAtOnce = NR >= 64 ? 3 : (NR + kCodeWarps - 1) / kCodeWarps;
+      // The heads' codes; rows past the heads become zeros.  (Every product with the last token's has been read, as
+      // the CTA's barrier behind its scores says.)
 #pragma unroll 1
-      for (int r0 = warp; r0 < NR; r0 += kCodeWarps * kAtOnce) {
-        uint4 raw[kAtOnce][2];
+      for (int i0 = 0; i0 < kRows; i0 += kAtOnce) {
+        if (i0 > 0) load_heads(i0);
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
-          const int r = r0 + i * kCodeWarps;
-          raw[i][0] = raw[i][1] = make_uint4(0, 0, 0, 0);
-          if (r < p.h) {
-            const uint4* src = reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(u) * p.h + r) * kD + 16 * lane);
-            raw[i][0] = src[0];
-            raw[i][1] = src[1];
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {
-          const int r = r0 + i * kCodeWarps;
+          const int r = warp + (i0 + i) * kCodeWarps;
           if (r >= NR) break;
           const uint4 a = raw[i][0], b = raw[i][1];
           uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
@@ -348,19 +405,37 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_select_kernel(const Sel
           // set) E - 5.
           const int e = max(static_cast<int>((top + 1) >> 7) - 127 - 6, -120);
           const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 - e) << 23), p.sign);
+          if constexpr (L::kHeadsOnM) {
+            // 1.5 2^23 + code has the code's byte in its low bits.
+            uint32_t four[4];
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            w[k] = pack_f16x2(rintf(__uint_as_float(w[k] << 16) * up), rintf(__uint_as_float(w[k] & 0xFFFF0000u) * up));
-          uint8_t* base = sQ + (lane >> 2) * (NR * 128);
-          const uint32_t off = r * 128 + (lane & 3) * 32;
-          *reinterpret_cast<uint4*>(base + swz<128>(off)) = make_uint4(w[0], w[1], w[2], w[3]);
-          *reinterpret_cast<uint4*>(base + swz<128>(off + 16)) = make_uint4(w[4], w[5], w[6], w[7]);
+            for (int k = 0; k < 4; ++k) {
+              uint32_t c[4];
+#pragma unroll
+              for (int i2 = 0; i2 < 2; ++i2) {
+                c[2 * i2] = __float_as_uint(fmaf(__uint_as_float(w[2 * k + i2] << 16), up, 12582912.f));
+                c[2 * i2 + 1] = __float_as_uint(fmaf(__uint_as_float(w[2 * k + i2] & 0xFFFF0000u), up, 12582912.f));
+              }
+              four[k] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+            }
+            *reinterpret_cast<uint4*>(sQ + r * MLA_MEAN_BYTES + lane * 16) = make_uint4(four[0], four[1], four[2], four[3]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              w[k] = pack_f16x2(rintf(__uint_as_float(w[k] << 16) * up), rintf(__uint_as_float(w[k] & 0xFFFF0000u) * up));
+            uint8_t* base = sQ + (lane >> 2) * (NR * 128);
+            const uint32_t off = r * 128 + (lane & 3) * 32;
+            *reinterpret_cast<uint4*>(base + swz<128>(off)) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(base + swz<128>(off + 16)) = make_uint4(w[4], w[5], w[6], w[7]);
+          }
           if (lane == 0) exps[r] = top == 0 ? -1000 : e;
         }
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[L::bQFull]);
+      if constexpr (!L::kHeadsOnM) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[L::bQFull]);
+      }
       named_bar_sync(1, kCodeWarps * 32);
       if (warp >= kScoreDecodeWarps) {
         const int i = tid - kScoreDecodeWarps * 32;
@@ -380,6 +455,20 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_select_kernel(const Sel
       // ---------------------------------------------------------------- codes to f16: lane = page
       const int team = warp >> 2;
       const uint32_t tA = tmem + (static_cast<uint32_t>(quad * 32) << 16) + L::cA;
+      if (L::kHeadsOnM && tiles > 0) {
+        // lane = head, this team's part of the dims
+        const uint32_t src = smem_u32(sQ) + (quad * 32 + lane) * MLA_MEAN_BYTES + team * (kD / kTeams);
+#pragma unroll 1
+        for (int part = 0; part < kD / 32 / kTeams; ++part) {
+          uint32_t o[16];
+          codes_to_f16(src + part * 32, o);
+          tmem_st16(tA + team * (kD / 2 / kTeams) + part * 16, o);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        named_bar_sync(3, kScoreDecodeWarps * 32);  // the pages' codes go where the heads' bytes were
+        if (lane == 0) mbar_arrive(&bars[L::bQFull]);
+      }
       for (uint32_t n = n0; n < n0 + tiles; ++n) {
         const uint32_t stage_no = 4 * n + quad, stage = stage_no % L::kStages;
         wait(L::bRawFull + stage, (stage_no / L::kStages) & 1);
@@ -395,27 +484,39 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_select_kernel(const Sel
           if (lane == 0) mbar_arrive(&bars[L::bScale + (n & 1)]);
         }
 #pragma unroll 1
-        for (int qq = team; qq < 4; qq += 2) {
-          wait(L::bKFree + qq, (n & 1) ^ 1);
-          tc_fence_after();
+        for (int qq = team; qq < 4; qq += kTeams) {
           const uint32_t src = smem_u32(rec) + qq * 128;
+          if constexpr (L::kHeadsOnM) {
+            const int slot = qq & 1;
+            wait(L::bKFree + slot, (qq >> 1) ^ 1);
+            uint8_t* at = sQ + slot * L::kQuarter;
 #pragma unroll 1
-          for (int part = 0; part < 4; ++part) {
-            uint32_t o[16];
+            for (int part = 0; part < 4; ++part) {
+              uint32_t o[16];
+              codes_to_f16(src + part * 32, o);
+              uint8_t* base = at + (part >> 1) * (kTile * 128);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint4 v = lds128(src + part * 32 + h * 16);
-              bytes_to_f16(v.x, o[8 * h + 0], o[8 * h + 1]);
-              bytes_to_f16(v.y, o[8 * h + 2], o[8 * h + 3]);
-              bytes_to_f16(v.z, o[8 * h + 4], o[8 * h + 5]);
-              bytes_to_f16(v.w, o[8 * h + 6], o[8 * h + 7]);
+              for (int k = 0; k < 4; ++k)
+                *reinterpret_cast<uint4*>(base + swz<128>((quad * 32 + lane) * 128 + (part & 1) * 64 + k * 16)) =
+                    make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
             }
-            tmem_st16(tA + qq * 64 + part * 16, o);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[L::bKFull + slot]);
+          } else {
+            wait(L::bKFree + qq, (n & 1) ^ 1);
+            tc_fence_after();
+#pragma unroll 1
+            for (int part = 0; part < 4; ++part) {
+              uint32_t o[16];
+              codes_to_f16(src + part * 32, o);
+              tmem_st16(tA + qq * 64 + part * 16, o);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[L::bKFull + qq]);
           }
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[L::bKFull + qq]);
         }
         if (lane == 0) mbar_arrive(&bars[L::bRawFree + stage]);
       }
@@ -424,13 +525,34 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_select_kernel(const Sel
       const uint32_t tS = tmem + (static_cast<uint32_t>(quad * 32) << 16) + L::cS;
       float* dst = p.scores + static_cast<int64_t>(u) * p.max_pages;
       for (uint32_t n = n0; n < n0 + tiles; ++n) {
-        if (n + kAhead < n0 + tiles) ask(n + kAhead);
         wait(L::bScale + (n & 1), (n >> 1) & 1);
         wait(L::bSFull + (n & 1), (n >> 1) & 1);
         tc_fence_after();
         float best = -INFINITY;
+        if constexpr (L::kHeadsOnM) {
+          // lane = head: the largest of the warp's for each page, then of the four warps'
+          const float w = weight[quad * 32 + lane];
+          float* red = reinterpret_cast<float*>(smem + L::kRedOff) + (n & 1) * (4 * kTile);
+#pragma unroll 1
+          for (int c = 0; c < kTile; c += 32) {
+            float v[32];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t r[16];
+              tmem_ld16(tS + (n & 1) * kTile + c + 16 * h, r);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[16 * h + i] = __uint_as_float(r[i]) * w;
+            }
+            LaneReduce<32, 16>::run(v, lane, OpMax{});
+            red[quad * kTile + c + lane] = v[0];
+          }
+          named_bar_sync(2, kScoreEpilogueWarps * 32);
+          const int at = quad * 32 + lane;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) best = fmaxf(best, red[k * kTile + at]);
+        }
 #pragma unroll 2
-        for (int c = 0; c < NR; c += 16) {
+        for (int c = 0; c < (L::kHeadsOnM ? 0 : NR); c += 16) {
           uint32_t r[16];
           tmem_ld16(tS + (n & 1) * NR + c, r);
 #pragma unroll
@@ -447,24 +569,35 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_select_kernel(const Sel
         const int page = first_page(n) + quad * 32 + lane;
         if (page < query.hi) dst[page] = scale < 0.f ? -INFINITY : best * scale;
       }
+    } else if (warp < kScoreMmaWarp) {
+      // ---------------------------------------------------------------- records
+      uint32_t stage_no = 4 * n0 + warp - kScoreLoadWarp0;
+      int id = look_up(stage_no), next = look_up(stage_no + kScoreLoadWarps);
+      for (; stage_no < 4 * (n0 + tiles); stage_no += kScoreLoadWarps) {
+        const int after = look_up(stage_no + 2 * kScoreLoadWarps);
+        ask(stage_no, id);
+        id = next;
+        next = after;
+      }
     } else if (tiles > 0) {
       // ---------------------------------------------------------------- D = C A^T
-      constexpr uint32_t idesc = idesc_f16(128, NR, false, false);
+      constexpr uint32_t idesc = idesc_f16(128, L::kSCols, false, false);
       const uint64_t desc = make_smem_desc(smem_u32(sQ), 16, 1024, kSwizzle128);
       const uint32_t lo = static_cast<uint32_t>(desc), hi = static_cast<uint32_t>(desc >> 32);
       wait(L::bQFull, scored & 1);
       for (uint32_t n = n0; n < n0 + tiles; ++n) {
-        const uint32_t d = tmem + L::cS + (n & 1) * NR;
+        const uint32_t d = tmem + L::cS + (n & 1) * L::kSCols;
         wait(L::bSFree + (n & 1), ((n >> 1) & 1) ^ 1);
 #pragma unroll 1
         for (int qq = 0; qq < 4; ++qq) {
-          wait(L::bKFull + qq, n & 1);
+          const int slot = L::kHeadsOnM ? qq & 1 : qq;
+          wait(L::bKFull + slot, L::kHeadsOnM ? qq >> 1 : n & 1);
           tc_fence_after();
-          const uint32_t a = tmem + L::cA + qq * 64, b = lo + ((2 * qq * NR * 128) >> 4);
+          const uint32_t a = tmem + L::cA + qq * 64, b = lo + ((2 * slot * NR * 128) >> 4);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             mma_f16_ts(d, a + j * 8, b + (((j >> 2) * NR * 128 + (j & 3) * 32) >> 4), hi, idesc, (qq | j) != 0);
-          commit_one(&bars[L::bKFree + qq]);
+          commit_one(&bars[L::bKFree + slot]);
         }
         commit_one(&bars[L::bSFull + (n & 1)]);
       }
