@@ -18,7 +18,6 @@ namespace mla {
 
 namespace {
 
-
 // Where a query token stands and what may be left out of its pages.
 struct Query {
   int at;      // position, below 0 when there is no such token
@@ -202,18 +201,31 @@ __device__ __forceinline__ void choose(const SelectParams& p, int query, const Q
 // of two.
 //
 // Work: a cluster of up to eight CTAs takes a query token at a time, its tiles
-// of 128 pages in turn; behind the cluster's barrier one of them chooses.  (As a
-// kernel of its own the choice costs its launch: XXX.)
+// of 128 pages in turn; behind the cluster's barrier one of them chooses.  With
+// the choice in a kernel of its own the two took 41 + 9 us for 64 query tokens
+// of 128 heads over 2048 pages and 11 + 6 us for one of 16 heads over 125; this
+// kernel takes 36 and 8.6.
 //
-// One CTA, 13 warps: decode (8), epilogue (4, which ask for the records of later
-// tiles first), product issuer.  Decode and epilogue warps also make a query
-// token's codes, while its first pages are on their way.
+// What bounds it at 128 heads is the way through shared memory: a tile of 128
+// pages costs 68 KB in, 64 KB to the decode warps and 128 KB of heads' codes to
+// the products, 2000 cycles at 128 bytes each, as long as the products
+// themselves (2048), and a quarter's decode takes its warps 1750 between them;
+// a tile takes 5000.  (The heads' codes in tensor memory and the pages' in
+// shared memory, so that two tiles were in flight instead of one, moved more
+// bytes: 35.4 us against 34.5 in the same arrangement.)  At 16 heads it is the
+// chain of loads, lengths, page ids, records, scores: 8.6 us, 1.4 of them the choice.
+//
+// One CTA, 16 warps: decode (8), epilogue (4, of which the first issues the
+// products, a tile ahead), loads (4).  Loads by one warp took 20.5 us for 32
+// query tokens of 64 heads over 1024 pages, by two 16.0, by four 15.4, with a
+// bulk copy per record or 16-byte copies by all lanes; asked for by the
+// epilogue's warps 18.2.  Decode and epilogue warps also make a query token's
+// codes, while its first pages are on their way.
 constexpr int kTeams = 2;
 constexpr int kScoreDecodeWarps = 4 * kTeams, kScoreEpilogueWarps = 4;
 constexpr int kCodeWarps = kScoreDecodeWarps + kScoreEpilogueWarps;
-constexpr int kScoreLoadWarp0 = kCodeWarps, kScoreLoadWarps = 3,
-              kScoreMmaWarp = kScoreLoadWarp0 + kScoreLoadWarps;
-constexpr int kScoreWarps = kScoreMmaWarp + 1, kScoreThreads = kScoreWarps * 32;
+constexpr int kScoreLoadWarp0 = kCodeWarps, kScoreWarps = kScoreLoadWarp0 + 4, kScoreThreads = kScoreWarps * 32;
+constexpr int kScoreMmaWarp = kScoreDecodeWarps;  // the first of the epilogue
 constexpr uint64_t kScoreWaitNs = 2000000000ull;
 
 template <int NR>
@@ -222,14 +234,13 @@ struct ScoreSmem {
   // apart as in memory: an odd number of 16-byte units, so rows of a warp meet in
   // no bank.
   static constexpr int kRecords = 32, kStageBytes = kRecords * MLA_MEAN_BYTES;
-  static constexpr int kStages = 8;                        // two tiles
-  static constexpr bool kHeadsOnM = NR == 128;
+  static constexpr int kStages = NR == 128 ? 4 : 8;  // one tile or two
+  // A stage is one quadrant's: its uses are one load warp's and the same decode
+  // warps', in order.  (Who runs ahead of another's use would take the phase two before for its own.)
+  static_assert(kScoreLoadWarp0 % 4 == 0 && kStages % 4 == 0, "stages by quadrants");
   static constexpr int kKeys = kStages * kStageBytes / 4;  // scores that the choice keeps where the stages were
-  // The heads' codes; or, with those in tensor memory, two dim quarters of the pages'
-  // and, before them, the heads' as bytes, 528 apart.
-  static constexpr int kQOff = 0, kQuarter = kTile * 128 * 2;
-  static constexpr int kRawOff = kHeadsOnM ? NR * MLA_MEAN_BYTES : NR * kD * 2;
-  static_assert(kRawOff % 16 == 0 && (!kHeadsOnM || kRawOff >= 2 * kQuarter), "the codes' place");
+  static constexpr int kQOff = 0;
+  static constexpr int kRawOff = NR * kD * 2;
   static constexpr int kWeightOff = kRawOff + kStages * kStageBytes;  // float[NR]
   static constexpr int kExpOff = kWeightOff + NR * 4;                 // int[NR]
   static constexpr int kScaleOff = kExpOff + NR * 4;                  // float[2][128]
@@ -240,19 +251,18 @@ struct ScoreSmem {
                        bDrain = bQFull + 1, kNumBars = bDrain + 1;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
   static constexpr int kCountOff = kMiscOff + 16;         // int[256], then the choice's small things
-  static constexpr int kRedOff = kCountOff + 1024 + 256;  // float[2][4][128]: a tile's maxima by lane quadrants
-  static constexpr int kAlloc = kRedOff + (kHeadsOnM ? 2 * 4 * kTile * 4 : 0) + 1024;
+  static constexpr int kAlloc = kCountOff + 1024 + 256 + 1024;
   static_assert(kBarOff % 8 == 0 && kAlloc <= 232448, "shared memory of one CTA");
   __device__ static int arrivals(int i) {
     if (i < bRawFree) return 33;                // the lanes whose copies have landed, and the mask's
     if (i < bKFull) return kTeams;
     if (i >= bKFull && i < bKFree) return 4;
     if (i >= bSFree && i < bQFull) return 4;
-    if (i == bQFull) return kHeadsOnM ? kScoreDecodeWarps : kCodeWarps;
+    if (i == bQFull) return kCodeWarps;
     return 1;
   }
-  // Tensor memory columns: the codes on M (of the pages by quarters, or the heads'), two score buffers.
-  static constexpr int cA = 0, cS = 256, kSCols = kHeadsOnM ? kTile : NR;
+  // Tensor memory columns: the codes' quarters, two score buffers.
+  static constexpr int cA = 0, cS = 256;
 };
 
 __device__ __forceinline__ int tiles_of(const SelectParams& p, const Query& q) {
@@ -355,19 +365,18 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_select_kernel(const Sel
     const auto first_page = [&](uint32_t n) {
       return query.lo + (rank + static_cast<int>(n - n0) * cluster) * kTile;
     };
-    // A load warp asks for a stage's records: lane = record for the ids, then a record
-    // at a time, lane = 16 bytes.  (By a bulk copy per record, issued by one warp: XXX.)
+    // Load warp `quad` asks for its quadrant's records of a tile: lane = record for
+    // the ids, then a record at a time, lane = 16 bytes.
     const int quad = warp & 3;
     const int32_t* table = p.block_table + static_cast<int64_t>(u / p.s) * p.max_pages;
-    const auto page_of = [&](uint32_t stage_no) { return first_page(stage_no >> 2) + (stage_no & 3) * 32 + lane; };
-    const auto look_up = [&](uint32_t stage_no) {
-      const int page = page_of(stage_no);
-      return stage_no < 4 * (n0 + tiles) && page < query.hi ? load_i32(table + page) : -1;
+    const auto look_up = [&](uint32_t n) {
+      const int page = first_page(n) + quad * 32 + lane;
+      return n < n0 + tiles && page < query.hi ? load_i32(table + page) : -1;
     };
-    const auto ask = [&](uint32_t stage_no, int id) {
-      const uint32_t stage = stage_no % L::kStages;
+    const auto ask = [&](uint32_t n, int id) {
+      const uint32_t stage_no = 4 * n + quad, stage = stage_no % L::kStages;
       const bool ok = id >= 0 && id < p.num_pages;
-      if (!ok && page_of(stage_no) < query.hi && p.d_error) atomicOr(p.d_error, MLA_DEVERR_BAD_INDEX);
+      if (!ok && first_page(n) + quad * 32 + lane < query.hi && p.d_error) atomicOr(p.d_error, MLA_DEVERR_BAD_INDEX);
       const uint32_t there = __ballot_sync(0xFFFFFFFFu, ok);
       wait(L::bRawFree + stage, ((stage_no / L::kStages) & 1) ^ 1);
       if (lane == 0) {
@@ -405,37 +414,19 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_select_kernel(const Sel
           // set) E - 5.
           const int e = max(static_cast<int>((top + 1) >> 7) - 127 - 6, -120);
           const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 - e) << 23), p.sign);
-          if constexpr (L::kHeadsOnM) {
-            // 1.5 2^23 + code has the code's byte in its low bits.
-            uint32_t four[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t c[4];
-#pragma unroll
-              for (int i2 = 0; i2 < 2; ++i2) {
-                c[2 * i2] = __float_as_uint(fmaf(__uint_as_float(w[2 * k + i2] << 16), up, 12582912.f));
-                c[2 * i2 + 1] = __float_as_uint(fmaf(__uint_as_float(w[2 * k + i2] & 0xFFFF0000u), up, 12582912.f));
-              }
-              four[k] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
-            }
-            *reinterpret_cast<uint4*>(sQ + r * MLA_MEAN_BYTES + lane * 16) = make_uint4(four[0], four[1], four[2], four[3]);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              w[k] = pack_f16x2(rintf(__uint_as_float(w[k] << 16) * up), rintf(__uint_as_float(w[k] & 0xFFFF0000u) * up));
-            uint8_t* base = sQ + (lane >> 2) * (NR * 128);
-            const uint32_t off = r * 128 + (lane & 3) * 32;
-            *reinterpret_cast<uint4*>(base + swz<128>(off)) = make_uint4(w[0], w[1], w[2], w[3]);
-            *reinterpret_cast<uint4*>(base + swz<128>(off + 16)) = make_uint4(w[4], w[5], w[6], w[7]);
-          }
+          for (int k = 0; k < 8; ++k)
+            w[k] = pack_f16x2(rintf(__uint_as_float(w[k] << 16) * up), rintf(__uint_as_float(w[k] & 0xFFFF0000u) * up));
+          uint8_t* base = sQ + (lane >> 2) * (NR * 128);
+          const uint32_t off = r * 128 + (lane & 3) * 32;
+          *reinterpret_cast<uint4*>(base + swz<128>(off)) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(base + swz<128>(off + 16)) = make_uint4(w[4], w[5], w[6], w[7]);
           if (lane == 0) exps[r] = top == 0 ? -1000 : e;
         }
       }
-      if constexpr (!L::kHeadsOnM) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[L::bQFull]);
-      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[L::bQFull]);
       named_bar_sync(1, kCodeWarps * 32);
       if (warp >= kScoreDecodeWarps) {
         const int i = tid - kScoreDecodeWarps * 32;
@@ -455,24 +446,26 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_select_kernel(const Sel
       // ---------------------------------------------------------------- codes to f16: lane = page
       const int team = warp >> 2;
       const uint32_t tA = tmem + (static_cast<uint32_t>(quad * 32) << 16) + L::cA;
-      if (L::kHeadsOnM && tiles > 0) {
-        // lane = head, this team's part of the dims
-        const uint32_t src = smem_u32(sQ) + (quad * 32 + lane) * MLA_MEAN_BYTES + team * (kD / kTeams);
-#pragma unroll 1
-        for (int part = 0; part < kD / 32 / kTeams; ++part) {
-          uint32_t o[16];
-          codes_to_f16(src + part * 32, o);
-          tmem_st16(tA + team * (kD / 2 / kTeams) + part * 16, o);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        named_bar_sync(3, kScoreDecodeWarps * 32);  // the pages' codes go where the heads' bytes were
-        if (lane == 0) mbar_arrive(&bars[L::bQFull]);
-      }
       for (uint32_t n = n0; n < n0 + tiles; ++n) {
         const uint32_t stage_no = 4 * n + quad, stage = stage_no % L::kStages;
         wait(L::bRawFull + stage, (stage_no / L::kStages) & 1);
         const uint8_t* rec = sRaw + stage * L::kStageBytes + lane * MLA_MEAN_BYTES;
+#pragma unroll 1
+        for (int qq = team; qq < 4; qq += kTeams) {
+          const uint32_t src = smem_u32(rec) + qq * 128;
+          wait(L::bKFree + qq, (n & 1) ^ 1);
+          tc_fence_after();
+#pragma unroll 1
+          for (int part = 0; part < 4; ++part) {
+            uint32_t o[16];
+            codes_to_f16(src + part * 32, o);
+            tmem_st16(tA + qq * 64 + part * 16, o);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[L::bKFull + qq]);
+        }
         if (team == 0) {
           wait(L::bSFree + (n & 1), ((n >> 1) & 1) ^ 1);
           const bool there = (masks[stage] >> lane) & 1;
@@ -483,76 +476,43 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_select_kernel(const Sel
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[L::bScale + (n & 1)]);
         }
-#pragma unroll 1
-        for (int qq = team; qq < 4; qq += kTeams) {
-          const uint32_t src = smem_u32(rec) + qq * 128;
-          if constexpr (L::kHeadsOnM) {
-            const int slot = qq & 1;
-            wait(L::bKFree + slot, (qq >> 1) ^ 1);
-            uint8_t* at = sQ + slot * L::kQuarter;
-#pragma unroll 1
-            for (int part = 0; part < 4; ++part) {
-              uint32_t o[16];
-              codes_to_f16(src + part * 32, o);
-              uint8_t* base = at + (part >> 1) * (kTile * 128);
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                *reinterpret_cast<uint4*>(base + swz<128>((quad * 32 + lane) * 128 + (part & 1) * 64 + k * 16)) =
-                    make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[L::bKFull + slot]);
-          } else {
-            wait(L::bKFree + qq, (n & 1) ^ 1);
-            tc_fence_after();
-#pragma unroll 1
-            for (int part = 0; part < 4; ++part) {
-              uint32_t o[16];
-              codes_to_f16(src + part * 32, o);
-              tmem_st16(tA + qq * 64 + part * 16, o);
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[L::bKFull + qq]);
-          }
-        }
         if (lane == 0) mbar_arrive(&bars[L::bRawFree + stage]);
       }
     } else if (warp < kCodeWarps) {
       // ---------------------------------------------------------------- the largest of a page's row
       const uint32_t tS = tmem + (static_cast<uint32_t>(quad * 32) << 16) + L::cS;
       float* dst = p.scores + static_cast<int64_t>(u) * p.max_pages;
+      // D = C A^T of a tile, before the last one's maxima.
+      constexpr uint32_t idesc = idesc_f16(128, NR, false, false);
+      const uint64_t desc = make_smem_desc(smem_u32(sQ), 16, 1024, kSwizzle128);
+      const uint32_t lo = static_cast<uint32_t>(desc), hi = static_cast<uint32_t>(desc >> 32);
+      const auto multiply = [&](uint32_t n) {
+        const uint32_t d = tmem + L::cS + (n & 1) * NR;
+        wait(L::bSFree + (n & 1), ((n >> 1) & 1) ^ 1);
+#pragma unroll 1
+        for (int qq = 0; qq < 4; ++qq) {
+          wait(L::bKFull + qq, n & 1);
+          tc_fence_after();
+          const uint32_t a = tmem + L::cA + qq * 64, b = lo + ((2 * qq * NR * 128) >> 4);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            mma_f16_ts(d, a + j * 8, b + (((j >> 2) * NR * 128 + (j & 3) * 32) >> 4), hi, idesc, (qq | j) != 0);
+          commit_one(&bars[L::bKFree + qq]);
+        }
+        commit_one(&bars[L::bSFull + (n & 1)]);
+      };
+      if (warp == kScoreMmaWarp && tiles > 0) {
+        wait(L::bQFull, scored & 1);
+        multiply(n0);
+      }
       for (uint32_t n = n0; n < n0 + tiles; ++n) {
+        if (warp == kScoreMmaWarp && n + 1 < n0 + tiles) multiply(n + 1);
         wait(L::bScale + (n & 1), (n >> 1) & 1);
         wait(L::bSFull + (n & 1), (n >> 1) & 1);
         tc_fence_after();
         float best = -INFINITY;
-        if constexpr (L::kHeadsOnM) {
-          // lane = head: the largest of the warp's for each page, then of the four warps'
-          const float w = weight[quad * 32 + lane];
-          float* red = reinterpret_cast<float*>(smem + L::kRedOff) + (n & 1) * (4 * kTile);
-#pragma unroll 1
-          for (int c = 0; c < kTile; c += 32) {
-            float v[32];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t r[16];
-              tmem_ld16(tS + (n & 1) * kTile + c + 16 * h, r);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) v[16 * h + i] = __uint_as_float(r[i]) * w;
-            }
-            LaneReduce<32, 16>::run(v, lane, OpMax{});
-            red[quad * kTile + c + lane] = v[0];
-          }
-          named_bar_sync(2, kScoreEpilogueWarps * 32);
-          const int at = quad * 32 + lane;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) best = fmaxf(best, red[k * kTile + at]);
-        }
 #pragma unroll 2
-        for (int c = 0; c < (L::kHeadsOnM ? 0 : NR); c += 16) {
+        for (int c = 0; c < NR; c += 16) {
           uint32_t r[16];
           tmem_ld16(tS + (n & 1) * NR + c, r);
 #pragma unroll
@@ -569,37 +529,13 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_select_kernel(const Sel
         const int page = first_page(n) + quad * 32 + lane;
         if (page < query.hi) dst[page] = scale < 0.f ? -INFINITY : best * scale;
       }
-    } else if (warp < kScoreMmaWarp) {
+    } else {
       // ---------------------------------------------------------------- records
-      uint32_t stage_no = 4 * n0 + warp - kScoreLoadWarp0;
-      int id = look_up(stage_no), next = look_up(stage_no + kScoreLoadWarps);
-      for (; stage_no < 4 * (n0 + tiles); stage_no += kScoreLoadWarps) {
-        const int after = look_up(stage_no + 2 * kScoreLoadWarps);
-        ask(stage_no, id);
-        id = next;
-        next = after;
-      }
-    } else if (tiles > 0) {
-      // ---------------------------------------------------------------- D = C A^T
-      constexpr uint32_t idesc = idesc_f16(128, L::kSCols, false, false);
-      const uint64_t desc = make_smem_desc(smem_u32(sQ), 16, 1024, kSwizzle128);
-      const uint32_t lo = static_cast<uint32_t>(desc), hi = static_cast<uint32_t>(desc >> 32);
-      wait(L::bQFull, scored & 1);
+      int id = look_up(n0);
       for (uint32_t n = n0; n < n0 + tiles; ++n) {
-        const uint32_t d = tmem + L::cS + (n & 1) * L::kSCols;
-        wait(L::bSFree + (n & 1), ((n >> 1) & 1) ^ 1);
-#pragma unroll 1
-        for (int qq = 0; qq < 4; ++qq) {
-          const int slot = L::kHeadsOnM ? qq & 1 : qq;
-          wait(L::bKFull + slot, L::kHeadsOnM ? qq >> 1 : n & 1);
-          tc_fence_after();
-          const uint32_t a = tmem + L::cA + qq * 64, b = lo + ((2 * slot * NR * 128) >> 4);
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            mma_f16_ts(d, a + j * 8, b + (((j >> 2) * NR * 128 + (j & 3) * 32) >> 4), hi, idesc, (qq | j) != 0);
-          commit_one(&bars[L::bKFree + slot]);
-        }
-        commit_one(&bars[L::bSFull + (n & 1)]);
+        const int next = look_up(n + 1);
+        ask(n, id);
+        id = next;
       }
     }
     n0 += tiles;
