@@ -14,6 +14,13 @@
 // offset and either layout are the same code, and the 32 pairs of a 64-dim
 // tail take one sine and cosine a lane (in registers they would take eight, on
 // four lanes).
+//
+// Bound by bytes where there are many rows: 100000 fp16 rows with 128 turned
+// dims to FP8, 156 MB, take 30.6 us, 5.1 TB/s or 76 % of a copy (34.9 without
+// the next row on its way, 31.2 with the steps read from the table each time and
+// eight blocks of every SM in the grid instead of the four that are resident).
+// 8191 bf16 rows to FP4 take 4.9 us (11 MB, latency), 64 rows 2, less than the
+// host's call.
 #include <cstdint>
 
 #include "mla_device.cuh"
@@ -78,8 +85,9 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
         if (j < pairs) {
           const uint64_t phase = static_cast<uint64_t>(pos) * step[j];
           const float half_turns = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f;  // 2^-31
-          // (The fast functions are within 2^-21.4 here, an eighth of a half step of E4M3's seven million; by
-          // sincospif 100000 rows of 128 turned dims take XXX us.)
+          // The fast functions are within 2^-21.1 of the whole turn's sine and cosine; a record's smallest step is
+          // 2^-18 of its block's largest value.  (By sincospif 100000 rows of 128 turned dims took 36.0 us where
+          // they took 34.9 so.)
           float s, c;
           __sincosf(half_turns * 3.14159265f, &s, &c);
           c *= table.factor;

@@ -14,6 +14,13 @@
 // Which pages: those whose last slot (offset 63) is in the list, as tokens are
 // appended in order.  Blocks take the list's entries at an odd stride, so that
 // the pages of one request, 64 entries apart, spread over all of them.
+//
+// 4096 pages, 78 MB, take 22.0 us: 3.5 TB/s, 53 % of a copy.  What bounds it is
+// the decode, 32 conversions and 32 multiply-adds a thread and record and half
+// of them again for the sums' way through shared memory (with f16 products
+// turned to fp32 and added by instructions of their own 32.2 us, with the
+// mixed-precision ones 25.9, with four blocks to an SM and the next page on its
+// way 22.0); 128 pages, as a long prompt's chunk of 8192 tokens completes, take 3.6.
 #include <cstdint>
 
 #include "mla_device.cuh"

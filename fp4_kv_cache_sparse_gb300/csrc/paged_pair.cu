@@ -17,6 +17,14 @@
 // (both CTAs hold the same running maximum of all 128 rows, as O^T adds up the
 // tokens of both), the new maxima when it has, row sums at a unit's end.
 //
+// What bounds it is instruction issue: an item takes some 8000 cycles, in which a
+// scheduler issues 5500 instructions of decode and softmax and the products take
+// 4100.  64 sequences x 128 heads over one prefix of 16k tokens take 267 us, 284
+// GFLOP at 1.06 PFLOP/s or 53 % of measured (paged.cu's form: 354).
+// Decodes of a sequence's own pages stay there: 64 query tokens x 128 heads over 64
+// selected pages each took 129 us so and 113 there, where the parts' starts and
+// ends count for more.
+//
 // One CTA, 28 warps: softmax (16, thread = token x 32 rows), K decode (4), V
 // decode (4), loader; in the first CTA the score issuer and two value issuers.
 #include <cstdint>

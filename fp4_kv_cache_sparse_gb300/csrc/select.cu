@@ -213,7 +213,7 @@ __device__ __forceinline__ void choose(const SelectParams& p, int query, const Q
 // a tile takes 5000.  (The heads' codes in tensor memory and the pages' in
 // shared memory, so that two tiles were in flight instead of one, moved more
 // bytes: 35.4 us against 34.5 in the same arrangement.)  At 16 heads it is the
-// chain of loads, lengths, page ids, records, scores: 8.6 us, 1.4 of them the choice.
+// chain of loads, lengths, page ids, records, scores, the choice: 8.6 us.
 //
 // One CTA, 16 warps: decode (8), epilogue (4, of which the first issues the
 // products, a tile ahead), loads (4).  Loads by one warp took 20.5 us for 32

@@ -5,6 +5,10 @@
 // Pieces with normalised outputs o_i and log-sum-exps L_i give
 // L = ln sum exp L_i and out = sum exp(L_i - L) o_i, in fp32, rounded once.
 // The pieces' order is that of the sum, so the result is the same every time.
+//
+// Bound by bytes: 8192 rows (64 x 128 heads) with some three pieces of 2 KB each
+// are 58 MB with their outputs and take 11 us behind the kernel that writes them,
+// 5 TB/s, out of L2 for the most part.
 #include <cstdint>
 #include <cuda_bf16.h>
 
