@@ -180,7 +180,7 @@ def test_heads_of_very_different_magnitudes():
     assert got[2][0, 0].tolist() == expected_pages(c.q[0, 0], c_means, c.table[0].cpu().long(), 30, 8, 0, 1)
 
 
-def test_more_pages_than_shared_memory_keeps():
+def test_long_sequences_with_repeated_pages():
     """9000 pages (half a million tokens) out of a small pool, so that scores repeat."""
     c = Sparse([64 * 300], 1, 16, seed=8)
     pages = 9001
@@ -192,6 +192,45 @@ def test_more_pages_than_shared_memory_keeps():
         got = c.run_sparse(top, sinks, local)
         assert got[3] == 0
         c.check_sparse(got, top, sinks, local)
+
+
+def repeated(lens, pool_pages, s, h, seed):
+    """Sequences whose pages come out of a small pool, again and again."""
+    c = Sparse([64 * pool_pages], s, h, seed=seed)
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    c.max_pages = max(lens) // 64 + 2
+    c.lens = list(lens)
+    held = c.table[0, :pool_pages]
+    c.table = held[torch.randint(0, pool_pages, (len(lens), c.max_pages), generator=g, device=DEV)]
+    c.seq = torch.tensor(c.lens, dtype=torch.int32, device=DEV)
+    c.q = torch.randn(len(lens), s, h, 512, generator=g, device=DEV).to(torch.bfloat16)
+    return c
+
+
+@pytest.mark.parametrize("h,pages,top,sinks,local", [
+    (65, 17500, 150, 1, 2),       # more scores than the choice keeps in shared memory
+    (65, 12000, 6000, 0, 1),      # room for the scores, not for the list of pages behind them
+    (16, 34100, 100, 3, 3),
+    (16, 20000, 14000, 0, 2),
+    (16, 300, 7, 3, 4),           # nothing left to choose
+])
+def test_scores_and_lists_of_every_size(h, pages, top, sinks, local):
+    c = repeated([pages * 64 - 9], 260, 1, h, seed=pages)
+    got = c.run_sparse(top, sinks, local)
+    assert got[3] == 0
+    c.check_sparse(got, top, sinks, local)
+
+
+@pytest.mark.parametrize("h", [8, 24, 64, 128])
+@pytest.mark.parametrize("num_sms", [0, 1, 7])
+def test_many_tiles_and_query_tokens_of_one_block(h, num_sms):
+    """Tiles of 128 pages by the dozen, several query tokens a block, short ones in between."""
+    c = repeated([64 * 1700 + 3, 5, 64 * 129, 64 * 640 + 63, 0, 64 * 386 + 1], 200, 2, h, seed=h)
+    got = c.run_sparse(12, 1, 2, num_sms=num_sms)
+    assert got[3] == 0
+    c.check_sparse(got, 12, 1, 2)
+    again = c.run_sparse(12, 1, 2, num_sms=num_sms)
+    assert all(torch.equal(x, y) for x, y in zip(got[:3], again[:3]))
 
 
 def test_bad_page_ids_are_skipped_and_flagged():
