@@ -292,3 +292,24 @@ def test_nan_records_reach_only_the_rows_that_see_them():
     out, lse, err = c.run_shared()
     assert err == 0
     assert torch.equal(out[:2], want[0][:2]) and torch.equal(lse[:2], want[1][:2])
+
+
+@pytest.mark.parametrize("sm_scale", [-0.05, 0.3, 1e-30, 0.0])
+@pytest.mark.parametrize("s,h", [(2, 24), (1, 128)])
+def test_scales_of_either_sign(sm_scale, s, h):
+    c = Shared([300, 64, 1, 129], s, h, [0, 3, 4], [900, 257], seed=51)
+    out, lse, err = c.run_shared(sm_scale=sm_scale)
+    assert err == 0
+    c.check_shared(out, lse, sm_scale=sm_scale)
+
+
+def test_pool_beyond_4_gib():
+    c = Shared([300, 64, 1, 129], 1, 100, [0, 3, 4], [900, 257], seed=52)
+    want = c.run_shared()
+    off, pages = 250000, c.num_pages
+    big = torch.zeros(off + pages, 64, 288, dtype=torch.uint8, device=DEV)
+    big[off:] = c.kv
+    c.kv, c.num_pages = big, off + pages
+    c.table, c.ptable = ((t + off).where((t >= 0) & (t < pages), t) for t in (c.table, c.ptable))
+    out, lse, err = c.run_shared()
+    assert err == 0 and torch.equal(out, want[0]) and torch.equal(lse, want[1])

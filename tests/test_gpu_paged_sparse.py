@@ -304,3 +304,21 @@ def test_rows_past_the_batch_and_no_selected_output():
     c.check_sparse((out, lse, sel), 5, 1, 1)
     assert torch.all(out[2:] == 7) and torch.all(lse[2:] == 7) and torch.all(sel[2:] == -9)
     assert torch.all(work[ws:] == 0xA5)
+
+
+def test_pool_beyond_4_gib():
+    """The same pages at the far end of a large pool: means, choice and attention as before."""
+    c = Sparse([64 * 300 + 5, 900], 1, 24, seed=21)
+    want = c.run_sparse(9, 1, 2)
+    off, pages, means = 250000, c.num_pages, c.means
+    big = torch.zeros(off + pages, 64, 288, dtype=torch.uint8, device=DEV)
+    big[off:] = c.kv
+    c.kv, c.num_pages = big, off + pages
+    c.table = (c.table + off).where((c.table >= 0) & (c.table < pages), c.table)
+    c.means = torch.full((c.num_pages, 528), 0xA5, dtype=torch.uint8, device=DEV)
+    c.refresh()
+    assert torch.equal(c.means[off:], means) and not torch.any(c.means[:off, :512])
+    got = c.run_sparse(9, 1, 2)
+    assert got[3] == 0
+    for x, y in zip(got[:3], want[:3]):
+        assert torch.equal(x, y)
