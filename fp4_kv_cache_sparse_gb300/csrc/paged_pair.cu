@@ -21,9 +21,11 @@
 // scheduler issues 5500 instructions of decode and softmax and the products take
 // 4100.  64 sequences x 128 heads over one prefix of 16k tokens take 267 us, 284
 // GFLOP at 1.06 PFLOP/s or 53 % of measured (paged.cu's form: 354).
-// Decodes of a sequence's own pages stay there: 64 query tokens x 128 heads over 64
-// selected pages each took 129 us so and 113 there, where the parts' starts and
-// ends count for more.
+// A vote that passes costs an item some 3000 cycles, as the last product and both
+// CTAs have to be waited for.  So the pages that are selected for a query
+// token stay with paged.cu: 64 x 128 heads over 64 pages each take 82 us here
+// and 93 there when scores are flat, but 130 and 113 when many heads have a page
+// of their own that towers above the others, which is what is selected.
 //
 // One CTA, 28 warps: softmax (16, thread = token x 32 rows), K decode (4), V
 // decode (4), loader; in the first CTA the score issuer and two value issuers.
@@ -957,7 +959,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const float m = fmaxf(m0, lds_f(x + (c ^ 1) * (NR * 4)));
           const float minus_old = lds_f(sm + L::kMinusMOff + tid * 4), s = lds_f(scale() + tid * 4);
           float alpha = 1.f;
-          if (fmaf(m + minus_old, s, kPBias) > kSlack + kPBias) {  // (its exponent, as above)
+          // Every row's that has grown, as O^T is rescaled as a whole: the votes to come are fewer (64 query tokens x
+          // 128 heads over 4096 tokens, scores of deviation 7: 120 us if only rows past the slack move, 105 so).
+          if (m + minus_old > 0.f) {
             alpha = ex2_approx(-(m + minus_old) * s);
             moved = minus_old != -kNoMax;
             sts_f(sm + L::kMinusMOff + tid * 4, -m);

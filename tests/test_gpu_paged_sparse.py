@@ -322,3 +322,15 @@ def test_pool_beyond_4_gib():
     assert got[3] == 0
     for x, y in zip(got[:3], want[:3]):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("h,num_sms", [(128, 4), (100, 5), (65, 2), (128, 1), (128, 0)])
+def test_many_query_tokens_on_few_blocks(h, num_sms):
+    """Enough pages a block that pairs of SMs take the selected ones, lengths of every kind among them."""
+    c = Sparse(LENGTHS + [64 * 40, 1800, 1] + ([1500] * 40 if num_sms == 0 else []), 2, h, seed=h + num_sms)
+    c.q[3] *= 8
+    got = c.run_sparse(24, 1, 2, num_sms=num_sms)
+    assert got[3] == 0
+    c.check_sparse(got, 24, 1, 2)
+    again = c.run_sparse(24, 1, 2, num_sms=num_sms, stream=torch.cuda.Stream())
+    assert all(torch.equal(x, y) for x, y in zip(got[:3], again[:3]))
