@@ -196,11 +196,11 @@ def _ptr(t):
         raise ValueError("tensor must be on a CUDA device (no CPU path)")
     if not t.is_contiguous():
         raise ValueError("tensor must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _stream(stream=None):
-    return ctypes.c_void_p(stream.cuda_stream if stream is not None else _raw_stream(_current_device()))
+    return stream.cuda_stream if stream is not None else _raw_stream(_current_device())
 
 
 def get_metadata(problem: Problem, num_sms: int = 0, device=None, stream=None):
