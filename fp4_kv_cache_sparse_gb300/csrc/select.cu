@@ -204,22 +204,21 @@ __device__ __forceinline__ void choose(const SelectParams& p, int query, const Q
 // of 128 pages in turn; behind the cluster's barrier one of them chooses.  With
 // the choice in a kernel of its own the two took 41 + 9 us for 64 query tokens
 // of 128 heads over 2048 pages and 11 + 6 us for one of 16 heads over 125; this
-// kernel takes 36 and 8.6.
+// kernel takes 33 and 8.5.
 //
-// What bounds it at 128 heads is the way through shared memory: a tile of 128
-// pages costs 68 KB in, 64 KB to the decode warps and 128 KB of heads' codes to
-// the products, 2000 cycles at 128 bytes each, as long as the products
-// themselves (2048), and a quarter's decode takes its warps 1750 between them;
-// a tile takes 5000.  (The heads' codes in tensor memory and the pages' in
-// shared memory, so that two tiles were in flight instead of one, moved more
-// bytes: 35.4 us against 34.5 in the same arrangement.)  At 16 heads it is the
-// chain of loads, lengths, page ids, records, scores, the choice: 8.6 us.
+// What bounds it where there are many pages is the way of their means to the SMs
+// and through shared memory: a tile of 128 pages is 68 KB, in 3700 cycles some 18
+// bytes a cycle and SM, or 4.4 TB/s out of L2 in pieces of 256 bytes; its decode costs
+// 64 KB more, its products the 128 KB of 128 heads' codes (2048 cycles).  (The heads'
+// codes in tensor memory and the pages' in shared memory moved more bytes: 35.4 us
+// against 34.5 in the same arrangement.)  For few pages it is the chain of loads,
+// lengths, page ids, records, scores, the choice: 8.5 us.
 //
 // One CTA, 16 warps: decode (8), epilogue (4, of which the first issues the
 // products, a tile ahead), loads (4).  Loads by one warp took 20.5 us for 32
 // query tokens of 64 heads over 1024 pages, by two 16.0, by four 15.4, with a
-// bulk copy per record or 16-byte copies by all lanes; asked for by the
-// epilogue's warps 18.2.  Decode and epilogue warps also make a query token's
+// bulk copy per record or 16-byte copies by all lanes (15.0 in halves of the
+// dims); asked for by the epilogue's warps 18.2.  Decode and epilogue warps also make a query token's
 // codes, while its first pages are on their way.
 constexpr int kTeams = 2;
 constexpr int kScoreDecodeWarps = 4 * kTeams, kScoreEpilogueWarps = 4;
@@ -230,14 +229,16 @@ constexpr uint64_t kScoreWaitNs = 2000000000ull;
 
 template <int NR>
 struct ScoreSmem {
-  // A stage is the records of 32 pages, a quadrant of the tile's lanes, 528 bytes
-  // apart as in memory: an odd number of 16-byte units, so rows of a warp meet in
-  // no bank.
-  static constexpr int kRecords = 32, kStageBytes = kRecords * MLA_MEAN_BYTES;
-  static constexpr int kStages = NR == 128 ? 4 : 8;  // one tile or two
-  // A stage is one quadrant's: its uses are one load warp's and the same decode
-  // warps', in order.  (Who runs ahead of another's use would take the phase two before for its own.)
-  static_assert(kScoreLoadWarp0 % 4 == 0 && kStages % 4 == 0, "stages by quadrants");
+  // A stage is half of the dims of 32 pages, a quadrant of the tile's lanes, in rows
+  // of an odd number of 16-byte units, so that the rows of a warp meet in no bank;
+  // behind the first half's the 16 bytes with the scale.  (Whole records: 36.1 us
+  // instead of 33.0 at 128 heads, where shared memory holds one tile; quarters 33.7.)
+  static constexpr int kParts = 2, kRing = NR == 128 ? 2 : 4;
+  static constexpr int kRecords = 32, kPartDims = kD / kParts, kPitch = kPartDims + 16, kStageBytes = kRecords * kPitch;
+  static constexpr int kStages = 4 * kRing;
+  // Its uses are one load warp's and the same decode warps', in order.  (Who runs
+  // ahead of another's use would take the phase two before for its own.)
+  static_assert(kScoreLoadWarp0 % 4 == 0, "stages by quadrants");
   static constexpr int kKeys = kStages * kStageBytes / 4;  // scores that the choice keeps where the stages were
   static constexpr int kQOff = 0;
   static constexpr int kRawOff = NR * kD * 2;
@@ -256,7 +257,7 @@ struct ScoreSmem {
   __device__ static int arrivals(int i) {
     if (i < bRawFree) return 33;                // the lanes whose copies have landed, and the mask's
     if (i < bKFull) return kTeams;
-    if (i >= bKFull && i < bKFree) return 4;
+    if (i >= bKFull && i < bKFree) return kScoreDecodeWarps;
     if (i >= bSFree && i < bQFull) return 4;
     if (i == bQFull) return kCodeWarps;
     return 1;
@@ -286,6 +287,12 @@ __device__ __forceinline__ void codes_to_f16(uint32_t src, uint32_t (&o)[16]) {
     bytes_to_f16(v.z, o[8 * h + 4], o[8 * h + 5]);
     bytes_to_f16(v.w, o[8 * h + 6], o[8 * h + 7]);
   }
+}
+
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.volatile.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
 }
 
 // 16 bytes into shared memory, and this thread's arrival once its copies so far have landed.
@@ -374,25 +381,31 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_select_kernel(const Sel
       return n < n0 + tiles && page < query.hi ? load_i32(table + page) : -1;
     };
     const auto ask = [&](uint32_t n, int id) {
-      const uint32_t stage_no = 4 * n + quad, stage = stage_no % L::kStages;
       const bool ok = id >= 0 && id < p.num_pages;
       if (!ok && first_page(n) + quad * 32 + lane < query.hi && p.d_error) atomicOr(p.d_error, MLA_DEVERR_BAD_INDEX);
       const uint32_t there = __ballot_sync(0xFFFFFFFFu, ok);
-      wait(L::bRawFree + stage, ((stage_no / L::kStages) & 1) ^ 1);
-      if (lane == 0) {
-        masks[stage] = there;
-        mbar_arrive(&bars[L::bRawFull + stage]);
-      }
-      const uint32_t dst = smem_u32(sRaw) + stage * L::kStageBytes;
+#pragma unroll 1
+      for (int part = 0; part < L::kParts; ++part) {
+        const uint32_t no = n * L::kParts + part, stage = no % L::kRing * 4 + quad;
+        wait(L::bRawFree + stage, ((no / L::kRing) & 1) ^ 1);
+        if (lane == 0) {
+          masks[stage] = there;
+          mbar_arrive(&bars[L::bRawFull + stage]);
+        }
+        constexpr int kLanes = L::kPartDims / 16;  // of a record
+        const uint32_t dst = smem_u32(sRaw) + stage * L::kStageBytes;
+        const uint8_t* src = p.means + part * L::kPartDims + lane % kLanes * 16;
 #pragma unroll 8
-      for (int r = 0; r < 32; ++r) {
-        const int from = __shfl_sync(0xFFFFFFFFu, id, r);
-        if ((there >> r) & 1)
-          copy16(dst + r * MLA_MEAN_BYTES + lane * 16, p.means + static_cast<int64_t>(from) * MLA_MEAN_BYTES + lane * 16);
+        for (int r0 = 0; r0 < 32; r0 += 32 / kLanes) {
+          const int r = r0 + lane / kLanes, from = __shfl_sync(0xFFFFFFFFu, id, r);
+          if ((there >> r) & 1)
+            copy16(dst + r * L::kPitch + lane % kLanes * 16, src + static_cast<int64_t>(from) * MLA_MEAN_BYTES);
+        }
+        if (part == 0 && ok)
+          copy16(dst + lane * L::kPitch + L::kPartDims, p.means + static_cast<int64_t>(id) * MLA_MEAN_BYTES + kD);
+        __syncwarp();
+        copies_arrive(&bars[L::bRawFull + stage]);
       }
-      if (ok) copy16(dst + lane * MLA_MEAN_BYTES + kD, p.means + static_cast<int64_t>(id) * MLA_MEAN_BYTES + kD);
-      __syncwarp();
-      copies_arrive(&bars[L::bRawFull + stage]);
     };
     if (tiles > 0 && warp < kCodeWarps) {
       // The heads' codes; rows past the heads become zeros.  (Every product with the last token's has been read, as
@@ -447,36 +460,40 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_select_kernel(const Sel
       const int team = warp >> 2;
       const uint32_t tA = tmem + (static_cast<uint32_t>(quad * 32) << 16) + L::cA;
       for (uint32_t n = n0; n < n0 + tiles; ++n) {
-        const uint32_t stage_no = 4 * n + quad, stage = stage_no % L::kStages;
-        wait(L::bRawFull + stage, (stage_no / L::kStages) & 1);
-        const uint8_t* rec = sRaw + stage * L::kStageBytes + lane * MLA_MEAN_BYTES;
+        uint32_t e = 0;  // this page's scale byte, 256 for a page that is none
 #pragma unroll 1
-        for (int qq = team; qq < 4; qq += kTeams) {
-          const uint32_t src = smem_u32(rec) + qq * 128;
-          wait(L::bKFree + qq, (n & 1) ^ 1);
-          tc_fence_after();
+        for (int part = 0; part < L::kParts; ++part) {
+          const uint32_t no = n * L::kParts + part, stage = no % L::kRing * 4 + quad;
+          wait(L::bRawFull + stage, (no / L::kRing) & 1);
+          const uint32_t rec = smem_u32(sRaw) + stage * L::kStageBytes + lane * L::kPitch;
+          if (part == 0) e = (masks[stage] >> lane) & 1 ? lds8(rec + L::kPartDims) : 256u;
+          // A team takes 64 of a quarter's dims.
 #pragma unroll 1
-          for (int part = 0; part < 4; ++part) {
-            uint32_t o[16];
-            codes_to_f16(src + part * 32, o);
-            tmem_st16(tA + qq * 64 + part * 16, o);
+          for (int j = 0; j < 4 / L::kParts; ++j) {
+            const int qq = part * (4 / L::kParts) + j;
+            wait(L::bKFree + qq, (n & 1) ^ 1);
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              uint32_t o[16];
+              codes_to_f16(rec + j * 128 + team * 64 + k * 32, o);
+              tmem_st16(tA + qq * 64 + team * 32 + k * 16, o);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[L::bKFull + qq]);
           }
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[L::bKFull + qq]);
+          if (lane == 0) mbar_arrive(&bars[L::bRawFree + stage]);
         }
         if (team == 0) {
           wait(L::bSFree + (n & 1), ((n >> 1) & 1) ^ 1);
-          const bool there = (masks[stage] >> lane) & 1;
-          const uint32_t e = there ? rec[kD] : 255u;
           // 2^(e - 127), a negative mark for a page that is none
           scales[(n & 1) * kTile + quad * 32 + lane] =
-              !there ? -1.f : (e == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(e << 23));
+              e == 256 ? -1.f : (e == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(e << 23));
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[L::bScale + (n & 1)]);
         }
-        if (lane == 0) mbar_arrive(&bars[L::bRawFree + stage]);
       }
     } else if (warp < kCodeWarps) {
       // ---------------------------------------------------------------- the largest of a page's row

@@ -210,7 +210,7 @@ def repeated(lens, pool_pages, s, h, seed):
 @pytest.mark.parametrize("h,pages,top,sinks,local", [
     (65, 17500, 150, 1, 2),       # more scores than the choice keeps in shared memory
     (65, 12000, 6000, 0, 1),      # room for the scores, not for the list of pages behind them
-    (16, 34100, 100, 3, 3),
+    (16, 35200, 100, 3, 3),
     (16, 20000, 14000, 0, 2),
     (16, 300, 7, 3, 4),           # nothing left to choose
 ])
