@@ -44,7 +44,7 @@ __device__ __forceinline__ uint32_t key_of(float score) {
   return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
 }
 
-// Exclusive prefix sum of two counts (each below 2^31) over the block.
+// Exclusive prefix sum of two counts (each below 2^31) over the block (of at most 32 warps).
 __device__ __forceinline__ int2 block_prefix(int2 mine, int2* warps) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int2 incl = mine;
@@ -55,9 +55,9 @@ __device__ __forceinline__ int2 block_prefix(int2 mine, int2* warps) {
   }
   if (lane == 31) warps[warp] = incl;
   __syncthreads();
-  int2 before = make_int2(incl.x - mine.x, incl.y - mine.y);
-  for (int w = 0; w < warp; ++w) before.x += warps[w].x, before.y += warps[w].y;
-  return before;
+  const int2 other = lane < warp ? warps[lane] : make_int2(0, 0);
+  return make_int2(incl.x - mine.x + __reduce_add_sync(0xFFFFFFFFu, other.x),
+                   incl.y - mine.y + __reduce_add_sync(0xFFFFFFFFu, other.y));
 }
 
 // The pages of one query token, by a whole CTA, its scores in place.  The k-th
@@ -91,22 +91,29 @@ __device__ __forceinline__ void choose(const SelectParams& p, int query, const Q
   const float* scores = p.scores + static_cast<int64_t>(query) * p.max_pages + at.lo;
   const auto key_at = [&](int j) { return j < room ? keys[j] : key_of(__ldcg(scores + j)); };
   uint32_t least = ~0u, most = 0;
-#pragma unroll 4
-  for (int j = tid; j < n; j += kThreads) {
-    const uint32_t key = key_of(__ldcg(scores + j));
-    if (j < room) keys[j] = key;
-    least = min(least, key);
-    most = max(most, key);
+  constexpr int kBatch = 4;  // loads under way together (one by one 32.5 us for 64 query tokens of 128 heads, 31.3 so)
+#pragma unroll 1
+  for (int j0 = tid; j0 < n; j0 += kBatch * kThreads) {
+    float score[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) score[i] = __ldcg(scores + min(j0 + i * kThreads, n - 1));
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int j = j0 + i * kThreads;
+      const uint32_t key = key_of(score[i]);
+      if (j < min(n, room)) keys[j] = key;
+      least = min(least, key);
+      most = max(most, key);
+    }
   }
   least = __reduce_min_sync(0xFFFFFFFFu, least);
   most = __reduce_max_sync(0xFFFFFFFFu, most);
   if (tid % 32 == 0) warps[tid / 32] = make_int2(least, most);
   for (int j = tid; j < 256; j += kThreads) counts[j] = 0;
   __syncthreads();
-  for (int w = 0; w < kThreads / 32; ++w) {
-    least = min(least, static_cast<uint32_t>(warps[w].x));
-    most = max(most, static_cast<uint32_t>(warps[w].y));
-  }
+  const int2 range = warps[tid % 32 % (kThreads / 32)];
+  least = __reduce_min_sync(0xFFFFFFFFu, static_cast<uint32_t>(range.x));
+  most = __reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(range.y));
   __syncthreads();
   // Bits from `bit` up agree with `known` for every key that still counts.
   int bit = k > 0 ? 32 - __clz(least ^ most) : 0, left = k;
@@ -204,7 +211,7 @@ __device__ __forceinline__ void choose(const SelectParams& p, int query, const Q
 // of 128 pages in turn; behind the cluster's barrier one of them chooses.  With
 // the choice in a kernel of its own the two took 41 + 9 us for 64 query tokens
 // of 128 heads over 2048 pages and 11 + 6 us for one of 16 heads over 125; this
-// kernel takes 33 and 8.5.
+// kernel takes 31 and 8.0.
 //
 // What bounds it where there are many pages is the way of their means to the SMs
 // and through shared memory: a tile of 128 pages is 68 KB, in 3700 cycles some 18
@@ -212,13 +219,13 @@ __device__ __forceinline__ void choose(const SelectParams& p, int query, const Q
 // 64 KB more, its products the 128 KB of 128 heads' codes (2048 cycles).  (The heads'
 // codes in tensor memory and the pages' in shared memory moved more bytes: 35.4 us
 // against 34.5 in the same arrangement.)  For few pages it is the chain of loads,
-// lengths, page ids, records, scores, the choice: 8.5 us.
+// lengths, page ids, records, scores, the choice: 8.0 us.
 //
 // One CTA, 16 warps: decode (8), epilogue (4, of which the first issues the
 // products, a tile ahead), loads (4).  Loads by one warp took 20.5 us for 32
 // query tokens of 64 heads over 1024 pages, by two 16.0, by four 15.4, with a
-// bulk copy per record or 16-byte copies by all lanes (15.0 in halves of the
-// dims); asked for by the epilogue's warps 18.2.  Decode and epilogue warps also make a query token's
+// bulk copy per record or 16-byte copies by all lanes; asked for by the epilogue's
+// warps 18.2.  (14.3 now.)  Decode and epilogue warps also make a query token's
 // codes, while its first pages are on their way.
 constexpr int kTeams = 2;
 constexpr int kScoreDecodeWarps = 4 * kTeams, kScoreEpilogueWarps = 4;
