@@ -177,7 +177,8 @@ __device__ __forceinline__ void choose(const SelectParams& p, int query, const Q
   for (int j = j0; j < j1; ++j) {
     const uint32_t key = key_at(j) >> bit;
     if (key > known || (key == known && before.y < left)) {
-      const int place = before.x + min(before.y, left);
+      const uint32_t place = before.x + min(before.y, left);
+      if (place >= static_cast<uint32_t>(k)) break;  // (after a wait that gave up the keys may have changed)
       if (listed)
         list[place] = at.lo + j;
       else
@@ -194,7 +195,7 @@ __device__ __forceinline__ void choose(const SelectParams& p, int query, const Q
     else if (i >= k)
       take(j, at.pages - p.top + j);
     else if (listed)
-      take(j, list[i]);
+      take(j, min(list[i], static_cast<uint32_t>(at.pages) - 1));
   }
 }
 
