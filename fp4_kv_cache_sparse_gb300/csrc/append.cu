@@ -16,11 +16,14 @@
 // four lanes).
 //
 // Bound by bytes where there are many rows: 100000 fp16 rows with 128 turned
-// dims to FP8, 156 MB, take 30.6 us, 5.1 TB/s or 76 % of a copy (34.9 without
-// the next row on its way, 31.2 with the steps read from the table each time and
-// eight blocks of every SM in the grid instead of the four that are resident).
-// 8191 bf16 rows to FP4 take 4.9 us (11 MB, latency), 64 rows 2, less than the
-// host's call.
+// dims to FP8, 156 MB, take 32.4 us, 4.8 TB/s or 72 % of a copy (31.2 with the
+// hardware's fast sine and cosine, whose error is one of the whole turn, 35.3
+// with sincospif; with the former, at 30.6 then, 34.9 without the next row on its
+// way and 31.2 with the steps read from the table each time and eight blocks of
+// every SM in the grid instead of the four that are resident).
+// 100000 bf16 rows to FP4, 131 MB, take 31.9 (64 turned dims), 60000 fp32 rows to
+// FP8, 155 MB, 28.9.  8191 bf16 rows to FP4 take 5.7 us (11 MB, latency), 64 rows 2,
+// less than the host's call.
 #include <cstdint>
 
 #include "mla_device.cuh"
@@ -32,6 +35,16 @@ namespace mla {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr double kPi = 3.14159265358979323846;
+
+// Sine and cosine of an angle of at most pi / 4 by their Taylor series (to t^9 and t^10, what follows is below 2^-28 of
+// them), each within 2^-23.6 of itself: near 0 too, where a pair that lies in two blocks shows it, as the sine's part of
+// a large dim may be all there is of a small one.
+__device__ __forceinline__ void sin_cos(float t, float& s, float& c) {
+  const float q = t * t;
+  s = fmaf(t * q, fmaf(q, fmaf(q, fmaf(q, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f), t);
+  c = fmaf(q, fmaf(q, fmaf(q, fmaf(q, fmaf(q, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f), -0.5f), 1.f);
+}
 
 template <typename T, bool kFp4>
 __global__ void __launch_bounds__(kWarps * 32, 4)
@@ -83,13 +96,18 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
       for (int i = 0; i < kMine; ++i) {
         const int j = lane + 32 * i;
         if (j < pairs) {
+          // Whole quarters of a turn, and what is left with all of its leading bits.
           const uint64_t phase = static_cast<uint64_t>(pos) * step[j];
-          const float half_turns = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f;  // 2^-31
-          // The fast functions are within 2^-21.1 of the whole turn's sine and cosine; a record's smallest step is
-          // 2^-18 of its block's largest value.  (By sincospif 100000 rows of 128 turned dims took 36.0 us where
-          // they took 34.9 so.)
+          const uint32_t quarters = static_cast<uint32_t>((phase + (uint64_t(1) << 61)) >> 62);
+          const int64_t rest = static_cast<int64_t>(phase - (static_cast<uint64_t>(quarters) << 62));
           float s, c;
-          __sincosf(half_turns * 3.14159265f, &s, &c);
+          sin_cos(static_cast<float>(rest) * static_cast<float>(kPi / 9223372036854775808.0), s, c);  // 2^63 is half a turn
+          if (quarters & 1) {
+            const float sine = s;
+            s = c;
+            c = -sine;
+          }
+          if (quarters & 2) s = -s, c = -c;
           c *= table.factor;
           s *= table.factor;
           float* pa = row + p.offset + (half ? j : 2 * j);
