@@ -184,12 +184,17 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t local, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
   return r;
 }
-// Arrivals on a barrier by its cluster address.  What only the tensor cores read next
-// (tensor memory, this CTA's own operands behind their proxy fence) goes by the first; what the other
-// CTA's threads read, or lies in its shared memory, by the second, which waits until those
-// writes are performed there: some 1000 cycles.
+// Arrivals on a barrier by its cluster address, by what they hand over:
+// arrive_at, tensor memory alone, which the tcgen05 fences on both sides order around an arrival of any kind;
+// hand_at, what the warp has read or written in its own CTA's shared memory (behind a proxy fence where the tensor
+// cores read it), by a fence that is of that memory only;
+// release_at, what it has stored in the other CTA's: it waits until those writes are performed there, some 1000 cycles.
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void hand_at(uint32_t bar) {
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+  arrive_at(bar);
 }
 __device__ __forceinline__ void release_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -644,7 +649,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         commit_both(bar(L::bDrain));
       } else {
-        for (uint32_t n = 0; n < items; ++n) wait(L::bSFull, n & 1);
+        for (uint32_t n = 0; n < items; ++n) wait2(L::bSFull, n & 1);
       }
       drain_at(bar(L::bDrain), 0, p.d_error, 2 * kWaitNs);
     } else if (c == 0) {
@@ -713,7 +718,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t src = ((q >> 2) == static_cast<int>(cluster_rank()) ? mine_at : other_at) + data, at = (q & 3) * 32;
           const uint32_t sc = lds32(mine_at + scales + ((q * 4) ^ scale_turn));
           // A fresh barrier counts as one whose phase 1 is over.
-          wait(L::bKFree + slot, ((q / L::kKSlots) & 1) ^ 1);
+          wait2(L::bKFree + slot, ((q / L::kKSlots) & 1) ^ 1);
           tc_fence_after();
 #pragma unroll 1
           for (int k = 0; k < 2; ++k) {
@@ -757,7 +762,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           wait(own ? L::bOwnFull + slot : L::bForeignFull + slot, own ? (no / L::kOwn) & 1 : (no / L::kForeign) & 1);
           if (at == 0) wait(L::bInfo + n % kInfoRing, (n / kInfoRing) & 1);
           const int have = ((item_word(n, 0) >> (8 * g)) & 0xFF) - odd * 32 - tok;  // tokens below it are there
-          wait(L::bVFree + block * L::kVSlots + odd, (at & 1) ^ 1);
+          wait2(L::bVFree + block * L::kVSlots + odd, (at & 1) ^ 1);
 #pragma unroll 1
           for (int w = 0; w < 2; ++w) {
             uint4 raw[2];
@@ -778,7 +783,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) arrive_at(lead(L::bVFull + block * L::kVSlots + odd));
+          if (lane == 0) hand_at(lead(L::bVFull + block * L::kVSlots + odd));
           if (lane == 0) arrive(bar(own ? L::bOwnFree + slot : L::bForeignFree + slot));
         }
       }
@@ -850,7 +855,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        arrive_at(lead(L::bQFull));
+        hand_at(lead(L::bQFull));
         arrive(bar(L::bUnit));
         release_at(other(L::bUnit));
       }
@@ -885,7 +890,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         wait2(L::bUnit, (turns >> 1) & 1);  // the scales of all rows
         turns ^= 2;
       }
-      wait(L::bSFull, n & 1);
+      wait2(L::bSFull, n & 1);
       tc_fence_after();
       // The piece's last scores are there, so its Q has been read: the next unit's may come.
       // (None after a wait that gave up: the last one asked for has to have landed at the end.)
@@ -929,7 +934,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           store_at(in_cta(vote, c ^ 1), n + 1);
           release_at(other(L::bVote + (n & 1)));
         } else {
-          arrive_at(other(L::bVote + (n & 1)));
+          hand_at(other(L::bVote + (n & 1)));
         }
         arrive(bar(L::bVote + (n & 1)));
       }
@@ -977,8 +982,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int k = 0; k < NC; ++k) l[k] *= lds_f(sm + L::kAlphaOff + (c0 + k) * 4);
           // O^T follows, once the product before this one is complete.
           if (!(flags & kOpens)) {
-            wait(L::bPFree, (n & 1) ^ 1);
-            wait(L::bPFree + 1, (n & 1) ^ 1);
+            wait2(L::bPFree, (n & 1) ^ 1);
+            wait2(L::bPFree + 1, (n & 1) ^ 1);
             tc_fence_after();
 #pragma unroll 1
             for (int i = side; i < 2 * (NR / 8); i += 4) {
@@ -1017,7 +1022,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       // Row `row` of P^T (MN-major), when the last product has read this half of the buffer.
-      wait(L::bPFree + (row >> 6), (n & 1) ^ 1);
+      wait2(L::bPFree + (row >> 6), (n & 1) ^ 1);
       tc_fence_before();
       if ((side >> 1) == static_cast<int>(c)) {
 #pragma unroll
@@ -1026,7 +1031,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
         // (The first CTA's warps of one side of a quadrant pair also announce what comes from the second: 4 warps' 2 KB.)
         if (lane == 0) {
-            arrive_at(lead(L::bPFull + (row >> 6)));
+            hand_at(lead(L::bPFull + (row >> 6)));
         }
       } else {
         // Four lanes' pieces are transposed among them, so that a store's lanes write 64 bytes of a token's row together
@@ -1100,8 +1105,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       named_bar_sync(1, kSoftmaxThreads);
       // The next unit's Q goes in while the last product runs (this piece's scores are all done).
       if (n + 1 < items) convert_q(sm + L::kInfoOff + (n % kInfoRing) * kItemBytes + 16);
-      wait(L::bPFree, n & 1);
-      wait(L::bPFree + 1, n & 1);
+      wait2(L::bPFree, n & 1);
+      wait2(L::bPFree + 1, n & 1);
       tc_fence_after();
       // Lane = dim, columns = rows.
       const int row0 = first_row();
