@@ -648,10 +648,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           commit_both(bar(L::bSFull));
         }
         commit_both(bar(L::bDrain));
-      } else {
-        for (uint32_t n = 0; n < items; ++n) wait2(L::bSFull, n & 1);
       }
-      drain_at(bar(L::bDrain), 0, p.d_error, 2 * kWaitNs);
     } else if (c == 0) {
       // ---------------------------------------------------------------- O^T += V^T P^T, a block of dims each
       const int block = warp - kValueWarp0;
@@ -1137,6 +1134,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  // The products are complete: the softmax warps have read the last of them, unless a wait gave up.  (A barrier of one
+  // phase.  To follow an item's barriers here instead would be a wait that nothing waits for: a warp held up for two items
+  // takes the phase two on for the one that it waits for.)
+  if (warp == kScoreWarp && run_items() > 0) drain_at(bar(L::bDrain), 0, p.d_error, 2 * kWaitNs);
   // (Q's copies have landed long ago, unless a wait gave up.)
   if (tid == 0 && run_items() > 0) drain_at(bar(L::bQRaw), lds32(sm + L::kMiscOff + 24), p.d_error, kWaitNs);
   if (lds32(sm + L::kMiscOff + 4) != 0) __nanosleep(100000);  // after a wait that gave up: stores on their way have landed

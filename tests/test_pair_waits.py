@@ -43,3 +43,29 @@ def test_waits_for_the_other_cta_are_of_cluster_scope():
     near = set(re.findall(r"\bwait\((?:own \? )?L::(b\w+)", text)) | set(re.findall(r": L::(b\w+) \+ slot,", text))
     assert near and not near & there
     assert there - {"bDrain"} <= set(re.findall(r"\bwait2\(L::(b\w+)", text))
+
+
+def block(text, at):
+    """From a brace to the one that closes it."""
+    at = text.index("{", at)
+    depth, end = 1, at + 1
+    while depth:
+        depth += {"{": 1, "}": -1}.get(text[end], 0)
+        end += 1
+    return text[at:end]
+
+
+def test_nobody_follows_barriers_that_do_not_wait_for_them():
+    """A wait by phase parity cannot tell a phase from the one two before, so who follows a barrier from item to item has
+    to hold it up: scores of an item are not written again before the softmax warps have arrived, and nobody else has.
+    The second CTA's warp that issues nothing there followed them too: held up for two items, it ran out of its wait."""
+    text = source()
+    # The score issuer's role: all of its waits are the first CTA's.
+    role = block(text, text.index("warp == kScoreWarp) {"))
+    lead = block(role, role.index("if (c == 0)"))
+    assert "wait2(L::bSFree" in lead
+    assert not re.search(r"\b(wait2?|drain_at)\(", role.replace(lead, ""))
+    # The end of all products is a barrier of one phase; both CTAs wait for it once their softmax warps are through.
+    assert text.count("drain_at(bar(L::bDrain)") == 1
+    roles_end = text.rindex("named_bar_sync(1, kSoftmaxThreads);")
+    assert text.index("__syncthreads();", roles_end) < text.index("drain_at(bar(L::bDrain)")
