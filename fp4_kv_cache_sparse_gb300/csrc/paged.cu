@@ -1237,23 +1237,28 @@ PagedPlan shared_plan(const mla_paged_shared_problem_t* p, int num_parts) {
   PagedPlan pl{};
   const int64_t rows = static_cast<int64_t>(p->seq_len_q) * p->h_q, all = rows * p->batch;
   // Rows of a unit, by the same reasoning as above: as few as hold a group's
-  // rows, or as leave no part more than three or four tiles.
-  const int64_t group_rows = (all + p->groups - 1) / p->groups;
+  // rows, or as leave no part more than three or four tiles.  The groups' starts are
+  // on the device: the batch counts as split evenly over them (groups past its
+  // sequences are empty), and a group's last unit may be part full.
+  const int64_t held = p->groups < p->batch ? p->groups : p->batch, group_rows = (all + held - 1) / held;
+  const auto prefix_units = [&](int64_t nr) { return held * ((group_rows + nr - 1) / nr); };
+  const auto own_units = [&](int64_t nr) { return p->batch * ((rows + nr - 1) / nr); };
   const int64_t tiles = (p->max_prefix_pages + 1) / 2 + kUnitCost, own = (p->max_pages + 1) / 2 + kUnitCost;
   const auto fits = [&](int nr) {
-    return group_rows <= nr || 2 * (((all + nr - 1) / nr) * tiles + p->batch * ((rows + nr - 1) / nr) * own) <=
-                                   int64_t(7) * num_parts;
+    return group_rows <= nr || 2 * (prefix_units(nr) * tiles + own_units(nr) * own) <= int64_t(7) * num_parts;
   };
   pl.nr = fits(16) ? 16 : (fits(32) ? 32 : 64);
   pl.num_parts = num_parts;
   // By pairs of SMs where there are many rows to a prefix and long ones: an item of 256 tokens x 128 rows takes a pair
-  // some 8000 cycles, a tile of 128 x 64 an SM 6000, and a pair's start, exchanges and end 10 us more (64 x 128 heads
-  // over a prefix of 16k tokens 266 and 354 us; 31 x 2 x 24 heads over three of up to 9k 52 and 43; 8 x 16 heads over 4k
-  // 24 and 13).
+  // some 8000 cycles, a tile of 128 x 64 an SM 6000, and a pair's start, exchanges and end 10 us more.  Both kernels
+  // without the merge: 64 x 128 heads over a prefix of 16k tokens 267 us by pairs, 354 by single SMs; several groups over
+  // 64k tokens each, 10 of 200 rows 312 and 414, 8 of 128 rows 145 and 176, 20 of 64 rows 321 and 216, 40 of 48 rows 618
+  // and 422; 16 of 192 rows over 16k tokens 152 and 138; 31 x 2 x 24 heads over three of up to 9k 52 and 45; 8 x 16 heads
+  // over 4k 24 and 14.  (With half a unit a group beside all rows together, many small groups went by pairs.)
   const auto work = [&](int64_t nr, int64_t tokens) {
     const auto items = [&](int64_t pages) { return (pages * kPage + tokens - 1) / tokens + kUnitCost; };
-    return static_cast<double>((all + nr - 1) / nr + p->groups / 2) * items(p->max_prefix_pages) +
-           static_cast<double>(p->batch) * ((rows + nr - 1) / nr) * items(p->max_pages);
+    return static_cast<double>(prefix_units(nr)) * items(p->max_prefix_pages) +
+           static_cast<double>(own_units(nr)) * items(p->max_pages);
   };
   if (num_parts >= 2 && work(128, 256) * 8000 / (num_parts / 2) + 20000 < work(64, 128) * 6000 / num_parts) {
     pl.pair = true;
