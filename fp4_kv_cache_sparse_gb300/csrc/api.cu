@@ -579,9 +579,10 @@ mla_status_t mla_kv_append(int32_t kv_format, int32_t dtype, const void* latents
     return MLA_ERR_INVALID_ARG;
   if (!aligned16(latents) || !aligned16(pool) || !aligned_to(slots, 4) || !aligned_to(positions, 4))
     return MLA_ERR_INVALID_ARG;
-  if (row_stride < 0 || (n > 1 && row_stride > (int64_t(1) << 31))) return MLA_ERR_INVALID_ARG;
-  if (n > 1 && (row_stride * bytes) % 16 != 0) return MLA_ERR_INVALID_ARG;
   if (n >= (int64_t(1) << 31)) return MLA_ERR_UNSUPPORTED;
+  // (The last row's offset in 64 bits.)
+  if (row_stride < 0 || (n > 1 && row_stride > (int64_t(1) << 62) / bytes / n)) return MLA_ERR_INVALID_ARG;
+  if (n > 1 && (row_stride * bytes) % 16 != 0) return MLA_ERR_INVALID_ARG;
   AppendParams p{};
   p.latents = latents;
   p.positions = positions;
