@@ -39,7 +39,7 @@ struct Piece {
 };
 
 // acc += the 32 dims' values under two e4m3 scales: f16 codes times f16 scales
-// into fp32 by single instructions, exact each.  A NaN scale counts as 448.
+// into fp32 by single instructions, exact each.  A NaN scale counts as 448 of its sign.
 __device__ __forceinline__ void add32(const Piece& p, float (&acc)[32]) {
   uint32_t s2 = e4m3x2_to_f16x2(p.sc & 0x7F7Fu);
   asm("min.f16x2 %0, %0, %1;" : "+r"(s2) : "r"(0x5F005F00u));
@@ -70,7 +70,7 @@ __device__ __forceinline__ void add32(const Piece& p, float (&acc)[32]) {
   }
 }
 
-// 128 dims' worth of columns is skewed by 4 words, so that lanes that write 32
+// Every 32 dims the columns are skewed by 4 words, so that lanes that write 32
 // words each do not meet in the same banks.
 __device__ __forceinline__ int column(int d) { return d + (d >> 5) * 4; }
 constexpr int kRow = kD + (kD / 32) * 4;

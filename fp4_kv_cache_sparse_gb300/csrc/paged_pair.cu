@@ -1,6 +1,6 @@
-// paged_pair.cu -- attention over a paged FP4 cache for many query rows against
-// the same tokens (the heads of a query token, the rows of a group of sequences
-// over their shared prefix): 128 rows at a time on a pair of SMs.
+// paged_pair.cu -- attention over a paged FP4 cache for sequences that share
+// prefixes, where many query rows see the same tokens (the rows of a group over its
+// prefix, those of a sequence over its own tokens): 128 rows at a time on a pair of SMs.
 //
 // The mathematics is that of paged.cu (S^T = K Q^T, P^T = 2^(scale (S - m)),
 // O^T += V^T P^T, one pass with a lazy running maximum); the split is not.  There
@@ -101,7 +101,7 @@ struct L {
                        bForeignFree = bForeignFull + kForeign, bKFull = bForeignFree + kForeign,
                        bKFree = bKFull + kKSlots, bVFull = bKFree + kKSlots, bVFree = bVFull + 2 * kVSlots,
                        bSFull = bVFree + 2 * kVSlots, bSFree = bSFull + 1, bPFull = bSFree + 1, bPFree = bPFull + 2,
-                       bPIn = bPFree + 2, bQFull = bPIn + 2, bOFree = bQFull + 1, bQRaw = bOFree + 1, bUnit = bQRaw + 1,
+                       bQFull = bPFree + 2, bOFree = bQFull + 1, bQRaw = bOFree + 1, bUnit = bQRaw + 1,
                        bVote = bUnit + 1, bXchg = bVote + 2, bDrain = bXchg + 1, bInfo = bDrain + 1,
                        kNumBars = bInfo + kInfoRing;
   static constexpr int kColOff = (kBarOff + kNumBars * 8 + 15) & ~15;
@@ -125,7 +125,7 @@ struct L {
     if (i >= bVFull && i < bVFree) return 2;                // both CTAs
     if (i == bSFree || i == bQFull || i == bOFree || i == bUnit || i == bVote || i == bVote + 1)
       return 2 * kSoftmaxWarps;
-    // Half of P: the warps that write to their own CTA, four of each, and the second CTA's word of what came in there.
+    // Half of P, the tokens of two lane quadrants: eight warps of each CTA, whichever CTA their rows' P goes to.
     if (i == bPFull || i == bPFull + 1) return kSoftmaxWarps;
     if (i == bPFree || i == bPFree + 1) return 2;              // both value issuers
     if (i == bXchg) return 2 * 4;
@@ -1026,10 +1026,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int k = 0; k < NC / 8; ++k) sts128(p_at ^ (k * 16), e[4 * k], e[4 * k + 1], e[4 * k + 2], e[4 * k + 3]);
         fence_proxy_async_smem();
         __syncwarp();
-        // (The first CTA's warps of one side of a quadrant pair also announce what comes from the second: 4 warps' 2 KB.)
-        if (lane == 0) {
-            hand_at(lead(L::bPFull + (row >> 6)));
-        }
+        if (lane == 0) hand_at(lead(L::bPFull + (row >> 6)));
       } else {
         // Four lanes' pieces are transposed among them, so that a store's lanes write 64 bytes of a token's row together
         // (16 bytes a row of 128 each they went one by one: 64 x 128 heads over a prefix of 16k tokens 277 us, 271 so).

@@ -414,7 +414,7 @@ mla_status_t mla_kv_append(int32_t kv_format, int32_t dtype, const void* latents
  * A mean is a record of MLA_MEAN_BYTES: 512 int8 codes, the byte 127 + e, 15
  * zeros.  With the exact mean m and the least e that gives max |m_d| 2^-e <= 127
  * (e = 0 for a mean of zeros), code d is m_d 2^-e rounded to nearest even: no
- * other rounding.  A NaN scale in a record counts as 448.
+ * other rounding.  A NaN scale in a record counts as 448 (of its sign).
  *   pool     uint8 [num_pages][64][288] FP4 records, 16-byte aligned.
  *   slots    int32 [n] (device); -1 = skip, others outside the pool are skipped
  *            and flagged (MLA_DEVERR_BAD_INDEX).
