@@ -22,8 +22,8 @@
 // way and 31.2 with the steps read from the table each time and eight blocks of
 // every SM in the grid instead of the four that are resident).
 // 100000 bf16 rows to FP4, 131 MB, take 31.9 (64 turned dims), 60000 fp32 rows to
-// FP8, 155 MB, 28.9.  8191 bf16 rows to FP4 take 5.7 us (11 MB, latency), 64 rows 2,
-// less than the host's call.
+// FP8, 155 MB, 28.9.  8191 bf16 rows to FP4 take 5.7 us (11 MB, latency), 64 rows
+// 2.6, less than the host's call.  (All with L2 written over before.)
 #include <cstdint>
 
 #include "mla_device.cuh"

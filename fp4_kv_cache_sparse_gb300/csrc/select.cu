@@ -212,15 +212,16 @@ __device__ __forceinline__ void choose(const SelectParams& p, int query, const Q
 // of 128 pages in turn; behind the cluster's barrier one of them chooses.  With
 // the choice in a kernel of its own the two took 41 + 9 us for 64 query tokens
 // of 128 heads over 2048 pages and 11 + 6 us for one of 16 heads over 125; this
-// kernel takes 31 and 8.0.
+// kernel takes 31 and 7.8.
 //
 // What bounds it where there are many pages is the way of their means to the SMs
-// and through shared memory: a tile of 128 pages is 68 KB, in 3700 cycles some 18
-// bytes a cycle and SM, or 4.4 TB/s out of L2 in pieces of 256 bytes; its decode costs
+// and through shared memory: a tile of 128 pages is 68 KB, in 2.5 us with 128 heads
+// and 2.2 with 16 (the slope of the time over 512 to 4096 pages, the choice's part in
+// it) 3.5 TB/s out of L2 in pieces of 256 bytes; its decode costs
 // 64 KB more, its products the 128 KB of 128 heads' codes (2048 cycles).  (The heads'
 // codes in tensor memory and the pages' in shared memory moved more bytes: 35.4 us
 // against 34.5 in the same arrangement.)  For few pages it is the chain of loads,
-// lengths, page ids, records, scores, the choice: 8.0 us.
+// lengths, page ids, records, scores, the choice: 7.8 us.
 //
 // One CTA, 16 warps: decode (8), epilogue (4, of which the first issues the
 // products, a tile ahead), loads (4).  Loads by one warp took 20.5 us for 32
